@@ -312,6 +312,152 @@ int gptq_block_attention(const float* x1, int64_t n_tokens, int32_t d, int32_t n
 /* M = silu(G) * U elementwise, silu(x) = x / (1 + exp(-x)); n elements. */
 int gptq_swiglu(const float* G, const float* U, int64_t n, float* M, hipStream_t s);
 
+/* ---------------------------------------------------------------- running the packed layer
+ * Operators for running and fine-tuning a block whose layers are packed to 4
+ * bits.  They share one description of a packed weight:
+ *  packed     [d_out x d_in/8] uint32, gptq_pack_int4's layout, columns in
+ *             processing order (codes[:, perm] for desc_act, else as they are).
+ *  scales, zeros  [d_out x n_groups] fp32 / int32, as gptq_quantize_layer
+ *             writes them; group_size a multiple of 8, or -1 for one group per
+ *             row; n_groups = ceil(d_in / group_size).
+ *  perm       NULL, or the [d_in] int32 processing order (a permutation):
+ *             packed column k belongs to channel perm[k].
+ * The weight is W[r][perm[k]] = round16(scales[r][k/G] * (code[r][k] - zeros[r][k/G])),
+ * the product in fp32, rounded (ties to even) to the activations' type, as in
+ * gptq_w4a16_gemm.  d_in is a multiple of 8, at most 2^20.  Sums are fp32.
+ * The struct itself is host memory and is read before the call returns. */
+typedef struct {
+  const uint32_t* packed;
+  const float* scales;
+  const int32_t* zeros;
+  const int32_t* perm;
+  int32_t d_out;
+  int32_t d_in;
+  int32_t group_size;
+  int32_t n_groups;
+} gptq_w4_weight;
+
+/* SILU x / (1 + exp(-x)); GELU x Phi(x); GELU_TANH its tanh approximation
+ * x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2. */
+typedef enum {
+  GPTQ_ACT_NONE = 0,
+  GPTQ_ACT_RELU = 1,
+  GPTQ_ACT_SILU = 2,
+  GPTQ_ACT_GELU = 3,
+  GPTQ_ACT_GELU_TANH = 4
+} gptq_act;
+
+/* Y = act(X W^T + bias) + R.  bias, activation and residual are applied to the
+ * fp32 sums, which are rounded once, to y_dtype.
+ *  X [m x d_in] f16/bf16, row t at X + t*ldx elements (ldx >= d_in).
+ *  bias [d_out] of x_dtype, or NULL.  R [m x d_out] of y_dtype, row pitch ldr,
+ *  or NULL; R may be Y itself (with ldr = ldy).  Y [m x d_out] of y_dtype
+ *  (F32, F16 or BF16), row pitch ldy; elements between rows stay as they are.
+ *  ws  scratch of gptq_w4_linear_workspace_size(m, w) bytes (the 16-bit weight
+ *      of large products, X in processing order; 0 bytes for small ones
+ *      without perm: ws may be NULL then).  X rows that are not 16-byte
+ *      aligned are copied to the workspace: the query's size covers that.
+ *  m == 0 is a no-op.  INVALID_ARG: null pointers, bad sizes, types, pitches
+ *  or group sizes. */
+size_t gptq_w4_linear_workspace_size(int64_t m, const gptq_w4_weight* w);
+int gptq_w4_linear(const void* X, gptq_dtype x_dtype, int64_t m, int64_t ldx, const gptq_w4_weight* w,
+                   const void* bias, gptq_act act, const void* R, int64_t ldr, void* Y,
+                   gptq_dtype y_dtype, int64_t ldy, void* ws, size_t ws_bytes, hipStream_t s);
+
+/* The gated feed-forward block's first half in one product: G = X Wg^T,
+ * U = X Wu^T, M = act(G) * U, from the fp32 sums of both.
+ *  gate, up: packed weights of one shape, with the same group_size and the
+ *  same perm pointer (they share one Hessian, so one order).
+ *  X [m x d_in], row pitch ldx.  M [m x d_out] of x_dtype, contiguous.  G and
+ *  U (both or neither; NULL when no backward pass follows): [m x d_out] of
+ *  x_dtype, contiguous.  act: SILU, GELU or GELU_TANH. */
+size_t gptq_w4_gated_workspace_size(int64_t m, const gptq_w4_weight* gate, const gptq_w4_weight* up);
+int gptq_w4_gated(const void* X, gptq_dtype x_dtype, int64_t m, int64_t ldx, const gptq_w4_weight* gate,
+                  const gptq_w4_weight* up, gptq_act act, void* G, void* U, void* M, void* ws,
+                  size_t ws_bytes, hipStream_t s);
+
+/* Its backward pass through the frozen packed weights: from dM, G and U
+ *   dU = dM * act(G),  dG = dM * U * act'(G),  dX = dG Wg + dU Wu.
+ * All [m x d_out] (dX: [m x d_in]) of one 16-bit type, contiguous.  dG and dU
+ * are rounded to that type (what an adapter's gradient needs; each may be
+ * NULL), and dX's products take the rounded values: one rounding more than
+ * exact, of the size of dX's own.  dX is written whole, in channel order.
+ * dG may be G and dU may be U. */
+size_t gptq_w4_gated_backward_workspace_size(int64_t m, const gptq_w4_weight* gate,
+                                             const gptq_w4_weight* up);
+int gptq_w4_gated_backward(const void* dM, const void* G, const void* U, gptq_dtype dtype, int64_t m,
+                           const gptq_w4_weight* gate, const gptq_w4_weight* up, gptq_act act, void* dG,
+                           void* dU, void* dX, void* ws, size_t ws_bytes, hipStream_t s);
+
+/* ---------------------------------------------------------------- a cache held in 4 bits
+ * Keys and values of a decoder block in pages of 4-bit rows.  A row is one
+ * token's head_dim values of one kv head, on its own min-max grid:
+ *   lo = fp16(min), step = fp16(max(max - lo, 0) / 15) (fp32 arithmetic),
+ *   code = clamp(rint((x - lo) / step), 0, 15) (0 when step is 0),
+ * and stands for lo + step * code.  Inputs beyond +-65504 count as +-65504, a
+ * NaN as the row's minimum (0 in a row of NaNs).
+ *  k_codes, v_codes  [n_pages x n_kv_heads x page_size x head_dim/8] uint32,
+ *                    code i of a row in bits 4(i%8) of word i/8; 16-byte aligned.
+ *  k_grid, v_grid    [n_pages x n_kv_heads x page_size x 2] fp16: step, lo;
+ *                    16-byte aligned.
+ *  page_table        [n_seqs x max_pages] int32: token j of sequence b is row
+ *                    j % page_size of page page_table[b][j / page_size].
+ *  head_dim 64 or 128; page_size a multiple of 16.
+ * A batch is described on the device: sequence b's new tokens are rows
+ * q_start[b] .. q_start[b+1]-1 of the token-major inputs and outputs
+ * ([n_seqs + 1] int32, not decreasing), and kv_len[b] ([n_seqs] int32) is its
+ * length in the cache with them: its new token i sits at position
+ * kv_len[b] - n_q + i.  Rows outside [q_start[0], q_start[n_seqs]) are neither
+ * read nor written.  Tokens at positions below 0 or on a page whose number is
+ * outside [0, n_pages) or past max_pages are not there: append skips them,
+ * read gives zeros, attention does not see them.  Pages of one batch's
+ * sequences may be shared (a common prefix) as long as no call appends to
+ * them through two sequences. */
+typedef struct {
+  uint32_t* k_codes;
+  uint32_t* v_codes;
+  void* k_grid;
+  void* v_grid;
+  const int32_t* page_table;
+  int32_t n_pages;
+  int32_t n_kv_heads;
+  int32_t page_size;
+  int32_t head_dim;
+  int32_t n_seqs;
+  int32_t max_pages;
+} gptq_kv4_cache;
+
+/* Quantize the new tokens' keys and values into their places.
+ *  K, V: token t's row of head h at K + t*ldk + h*head_dim elements (f16, bf16
+ *  or f32), ldk, ldv >= n_kv_heads * head_dim.  n_tokens: rows that K and V
+ *  have (q_start is cut to it). */
+int gptq_kv4_append(const gptq_kv4_cache* cache, const void* K, const void* V, gptq_dtype dtype,
+                    int64_t n_tokens, int64_t ldk, int64_t ldv, const int32_t* q_start,
+                    const int32_t* kv_len, hipStream_t s);
+
+/* The values that the cache holds for the batch's tokens, in append's layout
+ * (contiguous rows [n_tokens x n_kv_heads x head_dim]); K or V may be NULL. */
+int gptq_kv4_read(const gptq_kv4_cache* cache, void* K, void* V, gptq_dtype dtype, int64_t n_tokens,
+                  const int32_t* q_start, const int32_t* kv_len, hipStream_t s);
+
+/* Causal attention of the batch's tokens over the cache: new token i of
+ * sequence b, query head h, sees the positions j <= kv_len[b] - n_q + i of kv
+ * head h / (n_heads / n_kv_heads):
+ *   out = softmax_j(scale * q . k_j) v_j,
+ * sums and statistics in fp32.  A row that sees nothing is 0.
+ *  Q: token t, head h at Q + t*ldq + h*head_dim (f16/bf16, 16-byte aligned
+ *  rows); out likewise with ldo.
+ *  max_q_len, max_kv_len: host bounds on n_q and kv_len; tokens past
+ *  max_q_len of a sequence are left alone, positions past max_kv_len unseen.
+ *  ws  scratch of gptq_kv4_attention_workspace_size(...) bytes (partial
+ *      results of long sequences, joined in a fixed order). */
+size_t gptq_kv4_attention_workspace_size(int64_t n_tokens, int32_t n_heads, const gptq_kv4_cache* cache,
+                                         int32_t max_q_len, int32_t max_kv_len);
+int gptq_kv4_attention(const void* Q, gptq_dtype dtype, int64_t n_tokens, int32_t n_heads, int64_t ldq,
+                       const gptq_kv4_cache* cache, const int32_t* q_start, const int32_t* kv_len,
+                       int32_t max_q_len, int32_t max_kv_len, float scale, void* out, int64_t ldo,
+                       void* ws, size_t ws_bytes, hipStream_t s);
+
 /* ---------------------------------------------------------------- misc */
 const char* gptq_status_string(int status);
 int gptq_abi_version(void);

@@ -14,7 +14,10 @@ from ._lib import (  # noqa: F401
     gptq_w4a16_gemm, AWQ_DEFAULT_GRID, gptq_awq_act_sumsq, gptq_awq_quantize, gptq_awq_search,
     gptq_awq_search_workspace_size, gptq_awq_sumsq_workspace_size, gptq_block_attention,
     gptq_block_attention_workspace_size, gptq_linear, gptq_linear_workspace_size, gptq_rmsnorm,
-    gptq_swiglu,
+    gptq_swiglu, GPTQ_ACTS, KV4Cache, W4Weight, gptq_kv4_append, gptq_kv4_attention,
+    gptq_kv4_attention_workspace_size, gptq_kv4_read, gptq_w4_gated, gptq_w4_gated_backward,
+    gptq_w4_gated_backward_workspace_size, gptq_w4_gated_workspace_size, gptq_w4_linear,
+    gptq_w4_linear_workspace_size,
     gptq_prepare_hinv_workspace_size, gptq_quantize_layer, gptq_quantize_workspace_size,
     gptq_status_string, lib, make_config,
 )
