@@ -6,10 +6,10 @@
 // a wave holds NB x MB accumulators of v_mfma_f32_32x32x16.  Stages of 32 k are
 // copied HBM -> LDS by buffer_load ... lds (16 bytes per lane, no staging
 // registers) into a ring of kRing slots, kRing - 2 stages ahead.  A stage row
-// is 64 bytes; its 16-byte chunk c sits at c ^ ((row / 2) % 4), so the eight
-// lanes that read eight consecutive rows of one chunk hit eight different
-// 16-byte columns of the banks (the copy applies the swizzle by permuting the
-// lanes' source addresses).  The sync point of stage k sits before the last
+// is 64 bytes; its 16-byte chunk c sits at c ^ ((row / 4) % 4), so the sixteen
+// lanes that read sixteen consecutive rows of one chunk hit sixteen different
+// 16-byte columns of the 64 banks (the copy applies the swizzle by permuting
+// the lanes' source addresses).  The sync point of stage k sits before the last
 // k-slice of stage k-1: there every wave has waited for its copies of stage k
 // and has finished reading stage k-2, whose slot takes the next copies; the
 // last slice's MFMAs overlap the first operand reads of stage k.
@@ -101,7 +101,7 @@ __global__ __launch_bounds__(256, MB == 4 && NB == 4 ? 1 : 2) void gemm16_kernel
   int voffA[MB], voffB[NB];
   {
     const int R = 16 * wave + (lane >> 2);
-    const int c = (lane & 3) ^ ((R >> 1) & 3);
+    const int c = (lane & 3) ^ ((R >> 2) & 3);
 #pragma unroll
     for (int i = 0; i < MB; ++i)
       voffA[i] = m0 + R + 64 * i < g.m ? (int)((R + 64 * i) * g.lda * 2) + 16 * c : kPastEnd;
@@ -122,7 +122,7 @@ __global__ __launch_bounds__(256, MB == 4 && NB == 4 ? 1 : 2) void gemm16_kernel
     else copy16_lds(lds + slot * kSlot + TM * 64 + 4096u * (q - MB) + 1024u * wave, rb, voffB[q >= MB ? q - MB : 0]);
   };
   // operand reads: row lane % 32 of a 32-row block, k chunk 2 slice + lane / 32
-  const uint32_t sw = ((lane & 31) * 64) + (((lane >> 5) ^ ((lane >> 1) & 3)) << 4);
+  const uint32_t sw = ((lane & 31) * 64) + (((lane >> 5) ^ ((lane >> 2) & 3)) << 4);
   const uint32_t rdA = lds + wm * (32 * MB * 64) + sw, rdB = lds + TM * 64 + wn * (32 * NB * 64) + sw;
   const uint32_t rdA1 = rdA ^ 32u, rdB1 = rdB ^ 32u;   // slice 1: chunk 2 + lane / 32
   auto rd = [&](uint32_t at) { return *(LDS_AS const v8*)(uintptr_t)at; };

@@ -12,6 +12,7 @@ struct KvDev {
   uint32_t* v_grid;
   const int32_t* table;
   int n_pages, n_kv, page, n_seqs, max_pages;
+  int page_shift;          // log2(page), or -1
 };
 
 // One batch: where a sequence's new tokens are and how long it is.
@@ -43,14 +44,15 @@ GPTQ_DEV int seq_of_token(const int32_t* q_start, int n_seqs, int64_t t) {
   return count >= 1 && count <= n_seqs ? count - 1 : -1;
 }
 
-// Row of position p of sequence b, kv head h; -1 where there is none.
-GPTQ_DEV int64_t kv_row(const KvDev& c, int b, int h, int64_t p) {
-  if (p < 0) return -1;
-  const int64_t i = p / c.page;
-  if (i >= c.max_pages) return -1;
+// Row of position p of sequence b, kv head h; -1 where there is none.  Rows
+// and positions are counted in 32 bits (the host checks that they fit).
+GPTQ_DEV int kv_row(const KvDev& c, int b, int h, int64_t p) {
+  if (p < 0 || p >= (int64_t)c.max_pages * c.page) return -1;
+  const uint32_t q = (uint32_t)p;
+  const uint32_t i = c.page_shift >= 0 ? q >> c.page_shift : q / (uint32_t)c.page;
   const int pg = c.table[(int64_t)b * c.max_pages + i];
   if (pg < 0 || pg >= c.n_pages) return -1;
-  return ((int64_t)pg * c.n_kv + h) * c.page + (p - i * c.page);
+  return (pg * c.n_kv + h) * c.page + (int)(q - i * (uint32_t)c.page);
 }
 
 GPTQ_DEV float grid_step(uint32_t w) { return (float)__builtin_bit_cast(_Float16, (uint16_t)w); }
@@ -74,7 +76,7 @@ constexpr float kCodeBase = 16.0f;
 template <typename T, int K> GPTQ_DEV uint32_t code_pair(uint32_t w) {
   constexpr int sh = 4 * K - Code16<T>::kBit;
   const uint32_t v = sh >= 0 ? w >> (sh >= 0 ? sh : 0) : w << (sh < 0 ? -sh : 0);
-  return (v & Code16<T>::kMask) | Code16<T>::kBase;
+  return and_or(v, Code16<T>::kMask, Code16<T>::kBase);
 }
 // a word's eight codes: elements in the order 0 4 1 5 2 6 3 7
 template <typename T> GPTQ_DEV uint4 code_word(uint32_t w) {

@@ -125,18 +125,24 @@ struct AttnArgs {
   int64_t ldq, ldo;
   int n_heads, rep;            // query heads, query heads per kv head
   int max_q, max_kv;
-  float scale2;                // scale * log2(e)
+  float scale2;                // |scale| * log2(e), at least 1e-30
+  float lazy;                  // kLazy in units of q . k
+  uint32_t q_flip;             // sign bits to flip in Q (a negative scale)
   int chunk, n_chunks;         // keys per workgroup; 1 chunk: no partial results
   int row_tiles;
   float* part_o;               // [chunk][token][head][HD], not normalized
   float2* part_ml;             // [chunk][token][head]: maximum (log2 units), sum
 };
 
-constexpr float kNoMax = -3.0e38f;   // running maximum of a row that has seen nothing
+constexpr float kNoMax = -1.0e30f;    // running maximum of a row that has seen nothing
+// A row's reference maximum follows the true one only when some row of the
+// wave has outgrown its own by 2^8: the terms stay below 2^8 (2^9 with fp16's
+// steps), and most tiles rescale nothing.
+constexpr float kLazy = 8.0f;
 
 // Few rows (a query row is one new token's one query head; a sequence has
 // n_q * rep rows per kv head): a workgroup takes 16 rows against `chunk` keys,
-// each of its four waves a quarter of them, 32 keys a step, all in registers.
+// its four waves in turn 32 keys a step, all in registers.
 //
 // Scores are formed transposed, S^T[key][row] = K Q^T, on v_mfma_f32_16x16x32
 // with the codes themselves as operand (16 + code, exact): operand lane l is
@@ -156,7 +162,7 @@ constexpr float kNoMax = -3.0e38f;   // running maximum of a row that has seen n
 // 330 vector instructions per 32 keys.  A step's loads are in flight while the
 // step before is computed.
 template <typename T, int HD>
-__global__ __launch_bounds__(256) void kv4_rows_kernel(AttnArgs a, KvDev c, KvBatch q) {
+__global__ __launch_bounds__(256, 3) void kv4_rows_kernel(AttnArgs a, KvDev c, KvBatch q) {
   typedef typename T16<T>::v8 v8;
   typedef typename T16<__bf16>::v8 b8;
   constexpr int KW = HD / 32;          // packed words of a key per lane
@@ -167,12 +173,11 @@ __global__ __launch_bounds__(256) void kv4_rows_kernel(AttnArgs a, KvDev c, KvBa
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i = lane & 15, g = lane >> 4;
-  int id = blockIdx.x;
-  const int ch = id % a.n_chunks;
-  id /= a.n_chunks;
-  const int rt = id % a.row_tiles;
-  id /= a.row_tiles;
-  const int h = id % c.n_kv, b = id / c.n_kv;
+  // x: chunks, the row tiles and kv heads of one chunk next to each other
+  const int per = c.n_kv * a.row_tiles;
+  const int ch = blockIdx.x / per, b = blockIdx.y + 32768 * blockIdx.z;
+  const int rt = (blockIdx.x % per) / c.n_kv, h = (blockIdx.x % per) % c.n_kv;
+  if (b >= c.n_seqs) return;
   int64_t t0;
   int n_q;
   q.span(b, t0, n_q);
@@ -185,9 +190,8 @@ __global__ __launch_bounds__(256) void kv4_rows_kernel(AttnArgs a, KvDev c, KvBa
   const int row = rt * 16 + i;
   const int ti = min(row, rows - 1) / a.rep, hq = h * a.rep + min(row, rows - 1) % a.rep;
   const int seen = row < rows ? (int)max(min(first + ti + 1, most), (int64_t)0) : 0;
-  // the tile's longest and shortest row
+  // the tile's longest row
   const int seen_max = (int)max(min(first + (min(rt * 16 + 15, rows - 1) / a.rep) + 1, most), (int64_t)0);
-  const int seen_min = (int)max(min(first + (rt * 16) / a.rep + 1, most), (int64_t)0);
   const int c0 = ch * a.chunk;
   if (ch > 0 && c0 >= seen_max) return;
 
@@ -198,7 +202,8 @@ __global__ __launch_bounds__(256) void kv4_rows_kernel(AttnArgs a, KvDev c, KvBa
     const uint16_t* qp = a.Q + (t0 + ti) * a.ldq + (int64_t)hq * HD + 8 * KW * g;
 #pragma unroll
     for (int j = 0; j < KW; ++j) {
-      const uint4 v = *reinterpret_cast<const uint4*>(qp + 8 * j);
+      uint4 v = *reinterpret_cast<const uint4*>(qp + 8 * j);
+      v.x ^= a.q_flip; v.y ^= a.q_flip; v.z ^= a.q_flip; v.w ^= a.q_flip;
       qsum += (lo16f<T>(v.x) + hi16f<T>(v.x)) + (lo16f<T>(v.y) + hi16f<T>(v.y)) +
               ((lo16f<T>(v.z) + hi16f<T>(v.z)) + (lo16f<T>(v.w) + hi16f<T>(v.w)));
       qv[j] = __builtin_bit_cast(v8, code_order(v));
@@ -206,92 +211,112 @@ __global__ __launch_bounds__(256) void kv4_rows_kernel(AttnArgs a, KvDev c, KvBa
     qsum += __shfl_xor(qsum, 16);
     qsum += __shfl_xor(qsum, 32);
   }
-  const float qs2 = qsum * a.scale2;
+  const float qbase = -kCodeBase * qsum;
 
-  const int quarter = a.chunk >> 2;
-  const int kb0 = c0 + wave * quarter, kb1 = min(kb0 + quarter, seen_max);
-  const int steps = kb1 > kb0 ? (kb1 - kb0 + 31) >> 5 : 0;
-  // lane l: the cache row of 16-key tile l of this wave's keys, -1 if there is none
+  // wave w takes the steps of 32 keys w, w + 4, ...
+  const int k_end = min(c0 + a.chunk, seen_max), kw0 = c0 + 32 * wave;
+  const int steps = k_end > kw0 ? (k_end - kw0 + 127) >> 7 : 0;
+  // lane l: the cache row of 16-key block l % 2 of this wave's step l / 2, -1 if there is none
   int tile_row = -1;
-  if (kb0 + 16 * lane < kb1) tile_row = (int)kv_row(c, b, h, kb0 + 16 * lane);
+  {
+    const int p = kw0 + 128 * (lane >> 1) + 16 * (lane & 1);
+    if (p < k_end) tile_row = kv_row(c, b, h, p);
+  }
 
-  struct Step {
-    uint32_t k[2][KW];
-    uint32_t v[8];
-    uint4 kg[2], vg[2];
-  };
-  auto load = [&](int st, Step& s) {
+  // a step's packed words and grids; each half is loaded again as soon as it
+  // has been used, so its loads are in flight during the other half's work
+  uint32_t kw[2][KW], vw[8];
+  uint4 kg[2], vg[2];
+  auto row_of = [&](int st, int u) { return (uint32_t)max(__builtin_amdgcn_readlane(tile_row, 2 * st + u), 0); };
+  const uint32_t k_off = 4 * (i * RW + KW * g), v_off = 4 * (4 * g * RW + (i % RW));     // bytes
+  auto load_k = [&](int st) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int64_t r = max(__builtin_amdgcn_readlane(tile_row, 2 * st + u), 0);
-      const uint32_t* kp = c.k_codes + (r + i) * RW + KW * g;
-      if constexpr (KW == 4) *reinterpret_cast<uint4*>(s.k[u]) = *reinterpret_cast<const uint4*>(kp);
-      else *reinterpret_cast<uint2*>(s.k[u]) = *reinterpret_cast<const uint2*>(kp);
-      s.kg[u] = *reinterpret_cast<const uint4*>(c.k_grid + r + 4 * g);
-      s.vg[u] = *reinterpret_cast<const uint4*>(c.v_grid + r + 4 * g);
+      const uint32_t r = row_of(st, u);
+      const char* kp = reinterpret_cast<const char*>(c.k_codes + (size_t)r * RW);
+      if constexpr (KW == 4) *reinterpret_cast<uint4*>(kw[u]) = *reinterpret_cast<const uint4*>(kp + k_off);
+      else *reinterpret_cast<uint2*>(kw[u]) = *reinterpret_cast<const uint2*>(kp + k_off);
+      kg[u] = *reinterpret_cast<const uint4*>(c.k_grid + r + 4 * g);
+    }
+  };
+  auto load_v = [&](int st) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s.v[4 * u + e] = c.v_codes[(r + 4 * g + e) * RW + (i % RW)];
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t r = row_of(st, u);
+      const char* vp = reinterpret_cast<const char*>(c.v_codes + (size_t)r * RW);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) vw[4 * u + e] = *reinterpret_cast<const uint32_t*>(vp + v_off + 4 * e * RW);
+      vg[u] = *reinterpret_cast<const uint4*>(c.v_grid + r + 4 * g);
     }
   };
 
   f32x4_t o[NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j) o[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  float m = kNoMax, l = 0.0f, base = 0.0f;
-  Step cur, nxt;
-  if (steps > 0) load(0, cur);
-  for (int st = 0; st < steps; ++st) {
-    if (st + 1 < steps) load(st + 1, nxt);
-    const int kb = kb0 + 32 * st;
-    float s[8], vs[8], vl[8];
+  float m = kNoMax, l = 0.0f, base = 0.0f, sum_w = 0.0f;
+  if (steps > 0) {
+    load_k(0);
+    load_v(0);
+  }
+  // Everything before the exponential is in units of q . k: the row's sum in
+  // the accumulator's start takes 16 sum(q) off, and step and lo multiply as
+  // the fp16 halves they are stored as (two mixed instructions a score).
+  // WHOLE: every row sees all 32 keys.
+  auto turn = [&]<bool WHOLE>(int st) {
+    const int kb = kw0 + 128 * st;
+    float s[8];
+    bool ok[8];
     float mt = m;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      f32x4_t d = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      f32x4_t d = f32x4_t{qbase, qbase, qbase, qbase};
 #pragma unroll
-      for (int j = 0; j < KW; ++j) d = T16<T>::mfma16(__builtin_bit_cast(v8, code_word<T>(cur.k[u][j])), qv[j], d);
-      const uint32_t kg[4] = {cur.kg[u].x, cur.kg[u].y, cur.kg[u].z, cur.kg[u].w};
-      const uint32_t vg[4] = {cur.vg[u].x, cur.vg[u].y, cur.vg[u].z, cur.vg[u].w};
-      const bool there = __builtin_amdgcn_readlane(tile_row, 2 * st + u) >= 0;
-      const bool whole = there && kb + 16 * u + 16 <= seen_min;
+      for (int j = 0; j < KW; ++j) d = T16<T>::mfma16(__builtin_bit_cast(v8, code_word<T>(kw[u][j])), qv[j], d);
+      const uint32_t gw[4] = {kg[u].x, kg[u].y, kg[u].z, kg[u].w};
+      const bool there = WHOLE || __builtin_amdgcn_readlane(tile_row, 2 * st + u) >= 0;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int e = 4 * u + r;
-        uint32_t kw = kg[r], vw = vg[r];
-        bool ok = true;
-        if (!whole) {
-          // what lies behind a row's end or on a missing page may be anything
-          ok = there && kb + 16 * u + 4 * g + r < seen;
-          kw = ok ? kw : 0u;
-          vw = ok ? vw : 0u;
-        }
-        const float ks = grid_step(kw), kl = grid_lo(kw);
-        const float sc = fmaf(ks * a.scale2, d[r], fmaf(-kCodeBase, ks, kl) * qs2);
-        s[e] = ok ? sc : -INFINITY;
-        vs[e] = grid_step(vw);
-        vl[e] = fmaf(-kCodeBase, vs[e], grid_lo(vw));
+        // what lies behind a row's end or on a missing page may be anything
+        ok[e] = WHOLE || (there && kb + 16 * u + 4 * g + r < seen);
+        s[e] = fma_lo(gw[r], d[r], fma_hi(gw[r], qsum, 0.0f));
+        if constexpr (!WHOLE) s[e] = ok[e] ? s[e] : -INFINITY;
         mt = fmaxf(mt, s[e]);
       }
     }
+    if (st + 1 < steps) load_k(st + 1);
     mt = fmaxf(mt, __shfl_xor(mt, 16));
     mt = fmaxf(mt, __shfl_xor(mt, 32));
-    if (__any(mt > m)) {
-      const float al = __builtin_amdgcn_exp2f(m - mt);
+    if (__any(mt > m + a.lazy)) {
+      const float al = __builtin_amdgcn_exp2f((m - mt) * a.scale2);
 #pragma unroll
       for (int j = 0; j < NJ; ++j) o[j] *= al;
       l *= al;
       base *= al;
+      sum_w *= al;
       m = mt;
     }
+    const float off = -m * a.scale2;
     uint32_t ph[4], pl[4];
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-      const float p0 = __builtin_amdgcn_exp2f(s[e] - m), p1 = __builtin_amdgcn_exp2f(s[e + 1] - m);
-      l += p0 + p1;
-      base = fmaf(p0, vl[e], fmaf(p1, vl[e + 1], base));
-      const float w0 = p0 * vs[e], w1 = p1 * vs[e + 1];
-      ph[e / 2] = pack2<__bf16>(w0, w1);
-      pl[e / 2] = pack2<__bf16>(w0 - lo16f<__bf16>(ph[e / 2]), w1 - hi16f<__bf16>(ph[e / 2]));
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t gw[4] = {vg[u].x, vg[u].y, vg[u].z, vg[u].w};
+#pragma unroll
+      for (int r = 0; r < 4; r += 2) {
+        const int e = 4 * u + r;
+        float p[2], w[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t gr = ok[e + y] ? gw[r + y] : 0u;
+          p[y] = __builtin_amdgcn_exp2f(fmaf(s[e + y], a.scale2, off));
+          l += p[y];
+          base = fma_hi(gr, p[y], base);
+          w[y] = fma_lo(gr, p[y], 0.0f);
+          sum_w += w[y];
+        }
+        ph[e / 2] = pack2<__bf16>(w[0], w[1]);
+        pl[e / 2] = pack2<__bf16>(w[0] - lo16f<__bf16>(ph[e / 2]), w[1] - hi16f<__bf16>(ph[e / 2]));
+      }
     }
     const b8 hv = __builtin_bit_cast(b8, make_uint4(ph[0], ph[1], ph[2], ph[3]));
     const b8 lv = __builtin_bit_cast(b8, make_uint4(pl[0], pl[1], pl[2], pl[3]));
@@ -300,12 +325,13 @@ __global__ __launch_bounds__(256) void kv4_rows_kernel(AttnArgs a, KvDev c, KvBa
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if constexpr (HD == 128) {
-        z[0][e] = __builtin_amdgcn_perm(cur.v[2 * e + 1], cur.v[2 * e], 0x05040100u);
-        z[HD == 128 ? 1 : 0][e] = __builtin_amdgcn_perm(cur.v[2 * e + 1], cur.v[2 * e], 0x07060302u);
+        z[0][e] = __builtin_amdgcn_perm(vw[2 * e + 1], vw[2 * e], 0x05040100u);
+        z[HD == 128 ? 1 : 0][e] = __builtin_amdgcn_perm(vw[2 * e + 1], vw[2 * e], 0x07060302u);
       } else {
-        z[0][e] = __builtin_amdgcn_perm(cur.v[2 * e + 1], cur.v[2 * e], i < 8 ? 0x05040100u : 0x07060302u);
+        z[0][e] = __builtin_amdgcn_perm(vw[2 * e + 1], vw[2 * e], i < 8 ? 0x05040100u : 0x07060302u);
       }
     }
+    if (st + 1 < steps) load_v(st + 1);
     auto pv = [&]<int J>() {
       constexpr int zi = J / 4, K = J % 4;
       const b8 vv = __builtin_bit_cast(b8, make_uint4(code_pair<__bf16, K>(z[zi][0]), code_pair<__bf16, K>(z[zi][1]),
@@ -314,8 +340,16 @@ __global__ __launch_bounds__(256) void kv4_rows_kernel(AttnArgs a, KvDev c, KvBa
       o[J] = T16<__bf16>::mfma16(vv, lv, o[J]);
     };
     [&]<int... J>(std::integer_sequence<int, J...>) { (pv.template operator()<J>(), ...); }(std::make_integer_sequence<int, NJ>{});
-    cur = nxt;
-  }
+  };
+  // the steps in front that need no masks (all their pages there, all their
+  // keys seen by the tile's shortest row)
+  const int seen_min = rt * 16 + 15 < rows ? (int)max(min(first + (rt * 16) / a.rep + 1, most), (int64_t)0) : 0;
+  int plain = max(0, min(steps, (seen_min - kw0 + 96) >> 7));
+  const uint64_t missing = __ballot(tile_row < 0);
+  if (missing) plain = min(plain, (__ffsll((unsigned long long)missing) - 1) >> 1);
+  for (int st = 0; st < plain; ++st) turn.template operator()<true>(st);
+  for (int st = plain; st < steps; ++st) turn.template operator()<false>(st);
+  base = fmaf(-kCodeBase, sum_w, base);
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
   base += __shfl_xor(base, 16);
@@ -332,7 +366,7 @@ __global__ __launch_bounds__(256) void kv4_rows_kernel(AttnArgs a, KvDev c, KvBa
     }
   }
   if (g == 0) {
-    sM[wave][i] = m;
+    sM[wave][i] = m * a.scale2;
     sL[wave][i] = l;
   }
   __syncthreads();
@@ -354,13 +388,16 @@ __global__ __launch_bounds__(256) void kv4_rows_kernel(AttnArgs a, KvDev c, KvBa
 #pragma unroll
     for (int e = 0; e < HD / 16; ++e) v[e] = fmaf(al, sO[w][jr][(HD / 16) * (tid & 15) + e], v[e]);
   }
-  if (a.n_chunks > 1) {
+  // rows of one chunk need no joining
+  const int64_t seen2 = min(first + row2 / a.rep + 1, most);
+  if (seen2 > a.chunk) {
+    if (c0 >= seen2) return;
     const int64_t at = ((int64_t)ch * q.n_tokens + tok) * a.n_heads + head;
 #pragma unroll
     for (int e = 0; e < HD / 16; e += 4)
       *reinterpret_cast<float4*>(a.part_o + at * HD + (HD / 16) * (tid & 15) + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
     if ((tid & 15) == 0) a.part_ml[at] = make_float2(mm, ll);
-  } else {
+  } else if (ch == 0) {
     const float inv = ll != 0.0f ? 1.0f / ll : 0.0f;       // a row that saw nothing is 0; NaN stays
 #pragma unroll
     for (int e = 0; e < HD / 16; ++e) v[e] *= inv;
@@ -368,14 +405,395 @@ __global__ __launch_bounds__(256) void kv4_rows_kernel(AttnArgs a, KvDev c, KvBa
   }
 }
 
-// Joins the chunks of each row in their order: a wave per (token, head).
+// Many rows (prompts): a workgroup takes 128 rows, 16 to each of eight waves,
+// and walks the keys in tiles of 64.  A tile's codes are unpacked once for the
+// eight waves: keys as 16 + code rows (waves 0..3), values transposed (waves
+// 4..7; channel rows, the keys of a 16-byte chunk in the order in which the
+// softmax's registers hold them), both in the activations' type, double
+// buffered; the next tile's words are loaded while one is multiplied.  Products
+// and register layouts are those of kv4_rows_kernel.
+//
+// w_j = p_j step_j is rounded to the activations' type once, and what the
+// rounding is multiplied with has to be of the values' own size, not 16 + code:
+//   bf16  out = sum_j w_j ((16 + code_j) + lo_j / step_j - 16) / sum_j w_j / step_j
+//         with the rounded w_j in all three sums: its error is p's own, as if
+//         p had been rounded.  The last two sums are six more rows of V^T
+//         (lo / step - 16 and 1 / step, each in three bf16 pieces, 24 bits), so
+//         they cost two products a tile and no vector instructions; a step of
+//         0 counts as 1e-20.
+//   fp16  out = (sum_j w_j (code_j - 8) + sum_j p_j (lo_j + 8 step_j)) / sum_j p_j,
+//         the codes made signed by one packed addition (1 / step need not fit
+//         fp16).  The running maximum carries the exponent of the largest step
+//         seen, so w_j stays in [0, 2^9] whatever the steps are; bf16 has
+//         fp32's range and needs no such thing.
+//
+// 16-byte LDS accesses serve 16 lanes a cycle: the swizzles give 16 consecutive
+// rows of one chunk 16 different 16-byte columns of the 64 banks.
+//
+// 32 rows a wave on the 32 x 32 products read LDS half as often, but their 96
+// accumulators leave two waves per SIMD, and the loop then waits for LDS more
+// than it computes (279 us against KV4_TILE_US for 2565 tokens of 32 heads over
+// 4613 positions); 16 rows fit four waves.
+constexpr float kNoStep = 1e-20f;
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+constexpr int kTileWaves = 12;
+
+template <typename T, int HD>
+__global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kernel(AttnArgs a, KvDev c, KvBatch q) {
+  typedef typename T16<T>::v8 v8;
+  constexpr int RW = HD / 8;           // packed words per row
+  constexpr int KS = HD / 32;          // k-slices of the first product
+  constexpr int NJ = HD / 16;          // 16-channel blocks of the second
+  constexpr bool kScaled = T16<T>::kType == GPTQ_F16;
+  constexpr int TR = 16 * kTileWaves;
+  // LDS: [buffer][keys 64 x HD | values HD x 64 | six rows x 64 | ks, kl, vs, vl | vmax, there]
+  constexpr uint32_t kOffV = 64 * HD * 2, kOffX = 2 * kOffV, kOffG = kOffX + 8 * 128, kBuf = kOffG + 5 * 256;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * kBuf];
+  const uint32_t lds = (uint32_t)(uintptr_t)(LDS_AS const char*)smem;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int i = lane & 15, g = lane >> 4;
+  // row tiles by falling length, folded
+  const int ch = blockIdx.x % a.n_chunks;
+  int id = blockIdx.x / a.n_chunks;
+  const int items = a.row_tiles * c.n_kv * c.n_seqs;
+  id = id < (items + 1) / 2 ? 2 * id : 2 * (items - 1 - id) + 1;
+  const int rt = a.row_tiles - 1 - id / (c.n_kv * c.n_seqs);
+  id %= c.n_kv * c.n_seqs;
+  const int h = id % c.n_kv, b = id / c.n_kv;
+  int64_t t0;
+  int n_q;
+  q.span(b, t0, n_q);
+  const int64_t first = (int64_t)q.kv_len[b] - n_q;
+  n_q = min(n_q, a.max_q);
+  const int rows = n_q * a.rep;
+  if (rt * TR >= rows) return;
+  const int64_t most = min((int64_t)a.max_kv, (int64_t)c.max_pages * c.page);
+  auto seen_of = [&](int row) { return (int)max(min(first + row / a.rep + 1, most), (int64_t)0); };
+  const int seen_max = seen_of(min(rt * TR + TR - 1, rows - 1));
+  const int c0 = ch * a.chunk, c1 = min(c0 + a.chunk, seen_max);
+  if (ch > 0 && c0 >= seen_max) return;
+  // this wave's shortest and longest row (none: nothing to compute)
+  const int w0 = rt * TR + 16 * wave;
+  const int wmin = w0 < rows ? seen_of(w0) : 0, wmax = w0 < rows ? seen_of(min(w0 + 15, rows - 1)) : 0;
+  const int row = w0 + i;
+  const int seen = row < rows ? seen_of(row) : 0;
+  v8 qv[KS];
+  float qs2 = 0.0f;
+  {
+    const int64_t tok = t0 + min(row, rows - 1) / a.rep;
+    const int hq = h * a.rep + min(row, rows - 1) % a.rep;
+    const uint16_t* qp = a.Q + tok * a.ldq + (int64_t)hq * HD + 8 * g;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      uint4 v = *reinterpret_cast<const uint4*>(qp + 32 * s);
+      v.x ^= a.q_flip; v.y ^= a.q_flip; v.z ^= a.q_flip; v.w ^= a.q_flip;
+      qs2 += (lo16f<T>(v.x) + hi16f<T>(v.x)) + (lo16f<T>(v.y) + hi16f<T>(v.y)) +
+             ((lo16f<T>(v.z) + hi16f<T>(v.z)) + (lo16f<T>(v.w) + hi16f<T>(v.w)));
+      qv[s] = __builtin_bit_cast(v8, code_order(v));
+    }
+    qs2 += __shfl_xor(qs2, 16);
+    qs2 += __shfl_xor(qs2, 32);
+    qs2 *= a.scale2;
+  }
+
+  // chunk swizzles: key rows of HD / 8 chunks (256 or 128 bytes), channel rows of 8
+  auto swz_k = [](int key) { return HD == 128 ? key & 15 : (key >> 1) & 7; };
+  auto swz_v = [](int chn) { return ((chn >> 1) ^ (chn >> 4)) & 7; };
+
+  // Staging.  Wave w < 4: keys 16 w .. 16 w + 15, 16 bytes (four words) per
+  // lane.  Wave 4 + u: chunks 2u and 2u + 1 of the values; chunk 4t + y is the
+  // keys 32 t + 4 y + 0..3 and 16 further, a lane takes one word column of
+  // them and unpacks four of its channels.  head_dim 64 takes half the lanes.
+  const bool is_k = wave < 4, is_v = wave >= 4 && wave < 8;
+  const int u = wave & 3;
+  const int kkey = HD == 128 ? lane >> 2 : (lane & 31) >> 1, kq = HD == 128 ? lane & 3 : lane & 1;
+  const int vb = lane & (RW - 1), vz = (lane >> (HD == 128 ? 4 : 3)) & 1, vc = 2 * u + ((lane >> (HD == 128 ? 5 : 4)) & 1);
+  const bool busy = HD == 128 || lane < 32;
+  const uint32_t k_off = 4 * (kkey * RW + 4 * kq), v_off = 4 * (4 * (vc & 3) * RW + vb);     // bytes
+  const uint32_t v_sel = vz ? 0x07060302u : 0x05040100u;
+  // LDS offsets of the lane's first chunk each; the others flip or add constants
+  const int key_t = 16 * u + kkey, vchn = 8 * vb + 4 * vz;
+  const uint32_t s_at = is_k ? key_t * (2 * HD) + (((4 * kq) ^ swz_k(key_t)) << 4)
+                             : kOffV + vchn * 128 + ((vc ^ swz_v(vchn)) << 4);
+  const uint32_t x_at = kOffX + ((4 * (u >> 1) + ((lane >> 2) & 3)) << 4) + 2 * ((lane & 3) + 4 * (u & 1));
+  const uint32_t g_at = kOffG + 4 * (16 * u + i);
+  const int n0 = c0 >> 6, n1 = (c1 + 63) >> 6;
+  // lane l: cache rows of this wave's 16-key blocks of tile row_base + l: its
+  // grids' block u (keys: all it needs), and the other block of its chunks
+  int rows_u = -1, rows_o = -1;
+  int row_base = n0;
+  auto fetch_rows = [&](int n) {
+    const int p = 64 * (n + lane) + 16 * u, po = p ^ 16;
+    row_base = n;
+    rows_u = p < c1 ? kv_row(c, b, h, p) : -1;
+    if (is_v) rows_o = po < c1 ? kv_row(c, b, h, po) : -1;
+  };
+  uint32_t gw[8], gg = 0;
+  bool g_there = false;
+  auto load = [&](int n) {
+    if (!is_k && !is_v) return;
+    if (n - row_base >= 64) fetch_rows(n);
+    const int ru = __builtin_amdgcn_readlane(rows_u, n - row_base);
+    const uint32_t r = (uint32_t)max(ru, 0);
+    g_there = ru >= 0;
+    if (is_k) {
+      if (busy)
+        *reinterpret_cast<uint4*>(gw) =
+            *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(c.k_codes + (size_t)r * RW) + k_off);
+    } else if (is_v) {
+      const uint32_t ro = (uint32_t)max(__builtin_amdgcn_readlane(rows_o, n - row_base), 0);
+      const char* v0 = reinterpret_cast<const char*>(c.v_codes + (size_t)(u & 1 ? ro : r) * RW);
+      const char* v1 = reinterpret_cast<const char*>(c.v_codes + (size_t)(u & 1 ? r : ro) * RW);
+      if (busy) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          gw[e] = *reinterpret_cast<const uint32_t*>(v0 + v_off + 4 * e * RW);
+          gw[4 + e] = *reinterpret_cast<const uint32_t*>(v1 + v_off + 4 * e * RW);
+        }
+      }
+    }
+    // a key past the rows' end or on a missing page stands for zeros
+    const bool in = g_there && lane < 16 && 64 * n + 16 * u + lane < seen_max;
+    gg = in ? ((is_k ? c.k_grid : c.v_grid) + r)[lane] : 0u;
+  };
+  auto store = [&](uint32_t buf) {
+    auto put = [&](uint32_t at, uint4 v) { *(LDS_AS u32x4_t*)(uintptr_t)at = u32x4_t{v.x, v.y, v.z, v.w}; };
+    // opaque, so that the flipped addresses are formed where they are used
+    // instead of being kept in two dozen registers through the loop
+    uint32_t sa = buf + s_at, xa = buf + x_at, ga = buf + g_at;
+    asm volatile("" : "+v"(sa), "+v"(xa), "+v"(ga));
+    LDS_AS float* tail = (LDS_AS float*)(uintptr_t)(buf + kOffG + 4 * 256);
+    auto grid = [&](int plane) -> LDS_AS float& { return *(LDS_AS float*)(uintptr_t)(ga + 256 * plane); };
+    if (is_k) {
+      if (busy) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) put(sa ^ (j << 4), code_word<T>(gw[j]));
+      }
+      if (lane < 16) {
+        const float ks = grid_step(gg);
+        grid(0) = ks * a.scale2;
+        grid(1) = fmaf(-kCodeBase, ks, grid_lo(gg));
+        if (lane == 0) ((LDS_AS int*)tail)[4 + u] = g_there;
+      }
+    } else if (is_v) {
+      if (busy) {
+        uint32_t z[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[e] = __builtin_amdgcn_perm(gw[2 * e + 1], gw[2 * e], v_sel);
+        auto column = [&]<int K>() {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            w[e] = code_pair<T, K>(z[e]);
+            if constexpr (kScaled) {
+              const f16x2w_t off = {(_Float16)-24.0f, (_Float16)-24.0f};
+              w[e] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2w_t, w[e]) + off);
+            }
+          }
+          put((sa ^ ((K >> 1) << 4)) + 128 * K, make_uint4(w[0], w[1], w[2], w[3]));
+        };
+        column.template operator()<0>();
+        column.template operator()<1>();
+        column.template operator()<2>();
+        column.template operator()<3>();
+      }
+      if (lane < 16) {
+        const float vr = grid_step(gg), vs = kScaled || vr != 0.0f ? vr : kNoStep;
+        grid(2) = vs;
+        if constexpr (kScaled) {
+          grid(3) = fmaf(8.0f, vs, grid_lo(gg));
+          float mx = vs;
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o, 16));
+          if (lane == 0) tail[u] = mx;
+        } else {
+          // three pieces each of lo / step - 16 and 1 / step: rows 0..5, this key's slot of its chunk
+          const float inv = 1.0f / vs;
+          float x[2] = {grid_lo(gg) * inv - kCodeBase, inv};
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {
+              const int rr = 3 * y + p;
+              const uint16_t bits = bits16<T>(x[y]);
+              x[y] -= (float)__builtin_bit_cast(T, bits);
+              *(LDS_AS uint16_t*)(uintptr_t)((xa ^ (rr << 4)) + 128 * rr) = bits;
+            }
+        }
+      }
+    }
+  };
+
+  // Operand reads: slice s of a key row is chunk 4 s + g; the swizzle of channel
+  // row 16 j + i differs from row i's by j, so each read is the lane's first
+  // address with some bits flipped and a constant added.
+  const uint32_t k_rd = i * (2 * HD) + ((g ^ swz_k(i)) << 4);
+  const uint32_t v_rd = kOffV + i * 128 + ((g ^ swz_v(i)) << 4);
+  const uint32_t x_rd = kOffX + (i & 7) * 128 + ((g ^ (i & 7)) << 4);
+
+  f32x4_t o[NJ], ox = {0.0f, 0.0f, 0.0f, 0.0f};   // ox: the sums of V^T's extra rows (bf16)
+  float m = kNoMax, l = 0.0f, base = 0.0f;
+  float top = kNoMax, ex = -24.0f;     // largest score seen (m follows it); exponent of the largest step (fp16)
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) o[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+  if (n0 < n1) {
+    fetch_rows(n0);
+    load(n0);
+    store(lds);
+  }
+  __syncthreads();
+  uint32_t buf = lds, other = lds + kBuf;
+  int n = n0;
+  auto there = [&](int w) { return ((const LDS_AS int*)(uintptr_t)(buf + kOffG + 4 * 256 + 16))[w]; };
+  auto next_tile = [&]() {
+    if (n + 1 < n1) store(other);
+    __syncthreads();
+    const uint32_t t = buf;
+    buf = other;
+    other = t;
+    ++n;
+  };
+  // Tiles as long as `more` says so; WHOLE: every row of the wave sees all
+  // their keys.  The accumulators are rescaled outside the inner loop, which
+  // stops at a tile whose scores have outgrown the maximum and takes it again
+  // afterwards: as a branch inside it, the rescaling made the compiler keep
+  // them in two sets of registers and spill the rest.
+  auto tiles = [&]<bool WHOLE>(auto&& more) {
+    for (;;) {
+      bool grow = false;
+      float mt = top;
+      while (n < n1 && more()) {
+        auto rd = [&](uint32_t at) { return *(LDS_AS const v8*)(uintptr_t)at; };
+        uint32_t kr = buf + k_rd, vr = buf + v_rd, xr = buf + x_rd, gr = buf + kOffG + 16 * g;
+        asm volatile("" : "+v"(kr), "+v"(vr), "+v"(xr), "+v"(gr));
+        // plane's values of keys 16 kt + 4 g + 0..3
+        auto rd4 = [&](int plane, int kt) { return *(LDS_AS const f32x4_t*)(uintptr_t)(gr + 256 * plane + 64 * kt); };
+        f32x4_t s[4];
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) s[kt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int kt = 0; kt < 4; ++kt) s[kt] = T16<T>::mfma16(rd((kr ^ (ks << 6)) + kt * (32 * HD)), qv[ks], s[kt]);
+        mt = top;
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {
+          const f32x4_t ks = rd4(0, kt), kl = rd4(1, kt);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float x = fmaf(ks[r], s[kt][r], kl[r] * qs2);
+            if constexpr (!WHOLE) x = 64 * n + 16 * kt + 4 * g + r < seen && there(kt) ? x : -INFINITY;
+            s[kt][r] = x;
+            mt = fmaxf(mt, x);
+          }
+        }
+        mt = fmaxf(mt, __shfl_xor(mt, 16));
+        mt = fmaxf(mt, __shfl_xor(mt, 32));
+        top = mt;
+        if constexpr (kScaled) {
+          const LDS_AS float* vmax = (const LDS_AS float*)(uintptr_t)(buf + kOffG + 4 * 256);
+          const float vm = fmaxf(fmaxf(vmax[0], vmax[1]), fmaxf(vmax[2], vmax[3]));
+          if (vm > 0.0f) ex = fmaxf(ex, (float)(__builtin_amdgcn_frexp_expf(vm) - 1));
+          mt = mt > kNoMax ? mt + ex : mt;
+        }
+        grow = __any(mt > m + kLazy);
+        if (grow) break;
+        if (n + 1 < n1) load(n + 1);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int kt = 2 * t + y;
+            const f32x4_t vs = rd4(2, kt);
+            float p[4], w[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              p[r] = __builtin_amdgcn_exp2f(s[kt][r] - m);
+              // a key that this row does not see may hold anything
+              w[r] = !WHOLE && s[kt][r] == -INFINITY ? 0.0f : p[r] * vs[r];
+            }
+            if constexpr (kScaled) {
+              const f32x4_t vl = rd4(3, kt);
+              l += (p[0] + p[1]) + (p[2] + p[3]);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) base = fmaf(p[r], !WHOLE && s[kt][r] == -INFINITY ? 0.0f : vl[r], base);
+            }
+            pk[2 * y] = pack2<T>(w[0], w[1]);
+            pk[2 * y + 1] = pack2<T>(w[2], w[3]);
+          }
+          const v8 pv = __builtin_bit_cast(v8, make_uint4(pk[0], pk[1], pk[2], pk[3]));
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) o[j] = T16<T>::mfma16(rd((vr ^ (((4 * t) ^ (j & 7)) << 4)) + 2048 * j), pv, o[j]);
+          if constexpr (!kScaled) ox = T16<T>::mfma16(rd(xr ^ (t << 6)), pv, ox);
+        }
+        next_tile();
+      }
+      if (!grow) break;
+      const float m_new = fmaxf(m, mt), al = __builtin_amdgcn_exp2f(m - m_new);
+      m = m_new;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) o[j] *= al;
+      if constexpr (!kScaled) ox *= al;
+      l *= al;
+      base *= al;
+    }
+  };
+  // one after the other (the waves of a workgroup may be in different ones,
+  // each turn of each has one barrier): tiles seen whole, tiles that need
+  // their masks, tiles past the wave's rows, which it only helps to unpack
+  tiles.template operator()<true>([&]() { return 64 * n + 64 <= wmin && (there(0) & there(1) & there(2) & there(3)); });
+  tiles.template operator()<false>([&]() { return 64 * n < wmax; });
+  while (n < n1) {
+    if (n + 1 < n1) load(n + 1);
+    next_tile();
+  }
+  if constexpr (kScaled) {
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    base += __shfl_xor(base, 16);
+    base += __shfl_xor(base, 32);
+  } else {
+    // rows 0..3 of the extra block are the registers of g = 0, 4 and 5 the first two of g = 1
+    base = __shfl(ox[0] + (ox[1] + ox[2]), i);
+    l = __shfl(ox[3], i) + __shfl(ox[0] + ox[1], 16 + i);
+  }
+  if (row >= rows) return;
+  const int64_t tok = t0 + row / a.rep;
+  const int hq = h * a.rep + row % a.rep;
+  if (seen > a.chunk) {                // rows of one chunk need no joining
+    if (c0 >= seen) return;
+    const int64_t at = ((int64_t)ch * q.n_tokens + tok) * a.n_heads + hq;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      *reinterpret_cast<float4*>(a.part_o + at * HD + 16 * j + 4 * g) =
+          make_float4(o[j][0] + base, o[j][1] + base, o[j][2] + base, o[j][3] + base);
+    if (g == 0) a.part_ml[at] = make_float2(m, l);
+  } else if (ch == 0) {
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      float v[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = (o[j][r] + base) * inv;
+      store_n<T, 4>(a.out + tok * a.ldo + (int64_t)hq * HD + 16 * j + 4 * g, true, 4, v);
+    }
+  }
+}
+
+// Joins the chunks of each row: a workgroup per (token, head), HD / 4 lanes
+// across the channels and the chunks dealt to the groups of lanes, then the
+// groups in order (the same sums every time).
 template <typename T, int HD>
 __global__ __launch_bounds__(256) void kv4_join_kernel(AttnArgs a, KvDev c, KvBatch q) {
-  const int lane = threadIdx.x & 63;
-  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int64_t tok = id / a.n_heads;
-  const int head = (int)(id % a.n_heads);
-  if (tok >= q.n_tokens) return;
+  constexpr int L = HD / 4, NG = 256 / L;
+  __shared__ f32x4_t sv[NG][L];
+  __shared__ float sl[NG], sm[4];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int64_t tok = blockIdx.x / a.n_heads;
+  const int head = blockIdx.x % a.n_heads;
   const int b = seq_of_token(q.q_start, c.n_seqs, tok);
   if (b < 0) return;
   int64_t t0;
@@ -384,26 +802,44 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(AttnArgs a, KvDev c, KvBa
   if (tok - t0 >= a.max_q) return;
   const int64_t most = min((int64_t)a.max_kv, (int64_t)c.max_pages * c.page);
   const int64_t seen = max(min((int64_t)q.kv_len[b] - n_q + (tok - t0) + 1, most), (int64_t)0);
+  if (seen <= a.chunk) return;               // written by its only chunk
   const int n = (int)((seen + a.chunk - 1) / a.chunk);
   const int64_t at = tok * a.n_heads + head, step = q.n_tokens * a.n_heads;
   float m = kNoMax;
-  for (int k = lane; k < n; k += 64) m = fmaxf(m, a.part_ml[at + k * step].x);
+  for (int k = tid; k < n; k += 256) m = fmaxf(m, a.part_ml[at + k * step].x);
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-  constexpr int E = HD / 64;
-  float l = 0.0f, v[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) v[e] = 0.0f;
-  for (int k = 0; k < n; ++k) {
+  if (lane == 0) sm[tid >> 6] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+  const int grp = tid / L, li = tid % L;
+  float l = 0.0f;
+  f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int k = grp; k < n; k += NG) {
     const float2 ml = a.part_ml[at + k * step];
+    const f32x4_t x = *reinterpret_cast<const f32x4_t*>(a.part_o + (at + k * step) * HD + 4 * li);
     const float al = __builtin_amdgcn_exp2f(ml.x - m);
     l = fmaf(al, ml.y, l);
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = fmaf(al, a.part_o[(at + k * step) * HD + E * lane + e], v[e]);
+    for (int e = 0; e < 4; ++e) v[e] = fmaf(al, x[e], v[e]);
+  }
+  sv[grp][li] = v;
+  if (li == 0) sl[grp] = l;
+  __syncthreads();
+  if (tid >= L) return;
+  l = sl[0];
+  v = sv[0][tid];
+#pragma unroll
+  for (int g = 1; g < NG; ++g) {
+    l += sl[g];
+    v += sv[g][tid];
   }
   const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+  float r[4];
 #pragma unroll
-  for (int e = 0; e < E; ++e) a.out[tok * a.ldo + (int64_t)head * HD + E * lane + e] = bits16<T>(v[e] * inv);
+  for (int e = 0; e < 4; ++e) r[e] = v[e] * inv;
+  store_n<T, 4>(a.out + tok * a.ldo + (int64_t)head * HD + 4 * tid, true, 4, r);
 }
 
 // ---------------------------------------------------------------- host side
@@ -420,7 +856,8 @@ static bool cache_ok(const gptq_kv4_cache* c) {
 }
 static KvDev dev_of(const gptq_kv4_cache* c) {
   return KvDev{c->k_codes, c->v_codes, static_cast<uint32_t*>(c->k_grid), static_cast<uint32_t*>(c->v_grid), c->page_table,
-               c->n_pages, c->n_kv_heads, c->page_size, c->n_seqs, c->max_pages};
+               c->n_pages, c->n_kv_heads, c->page_size, c->n_seqs, c->max_pages,
+               (c->page_size & (c->page_size - 1)) == 0 ? __builtin_ctz((unsigned)c->page_size) : -1};
 }
 static bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 static bool elem_al(const void* p, gptq_dtype t) { return (reinterpret_cast<uintptr_t>(p) & (t == GPTQ_F32 ? 3 : 1)) == 0; }
@@ -437,16 +874,32 @@ template <typename F> static int with_kind(gptq_dtype t, int hd, F&& f) {
   return GPTQ_OK;
 }
 
-// Keys per workgroup.
+// Keys per workgroup of few rows: at least 512 workgroups where the keys allow
+// it, and at least 16 pieces of the longest sequence, so that a batch of many
+// lengths has no long tail (lengths are on the device: the host knows only
+// their bound).  Measured, chunks of 256, 512, 1024, 2048: 48 sequences of 1 to
+// 8192 positions 41, 37, 39, 50 us; one of 131072 57, 48, 45, 43 us.
 static int chunk_of(int64_t groups, int max_kv) {
   if (max_kv <= 512) return 512;
-  int64_t want = (int64_t)max_kv * groups / 2048;
-  int c = 512;
-  while (c < 4096 && c < want) c *= 2;
+  int c = groups * max_kv < (int64_t)256 * 512 ? 256 : 512;
+  while (c < 4096 && 32 * c <= max_kv && groups * max_kv >= (int64_t)2 * c * 512) c *= 2;
   return c;
 }
 
+// Many rows: the keys are split only where there are too few row tiles for the
+// 512 workgroups that the chip holds.
+static int tile_chunk_of(int64_t groups, int max_kv) {
+  const int all = (max_kv + 63) / 64 * 64;
+  if (groups >= 256) return all;
+  const int64_t want = ((int64_t)max_kv * groups / 512 + 63) / 64 * 64;
+  return (int)std::min<int64_t>(all, std::max<int64_t>(want, 512));
+}
+
+// rows of a sequence and kv head from which the unpacked tiles pay
+constexpr int kTileRows = 33;
+
 struct AttnPlan {
+  int per;                   // rows per workgroup: 16, or the unpacked tiles' 128
   int chunk, n_chunks, row_tiles;
   int64_t grid;
   size_t off_ml, total;
@@ -457,12 +910,14 @@ static bool attn_plan(int64_t n_tokens, int n_heads, const gptq_kv4_cache* c, in
   max_kv = (int)std::min<int64_t>(max_kv, (int64_t)c->max_pages * c->page_size);
   const int64_t rows = (int64_t)max_q * (n_heads / c->n_kv_heads);
   if (rows > INT_MAX - 16) return false;
-  p.row_tiles = (int)((rows + 15) / 16);
-  const int64_t groups = (int64_t)c->n_seqs * c->n_kv_heads * p.row_tiles;
-  p.chunk = chunk_of(groups, max_kv);
+  const int64_t seqs = (int64_t)c->n_seqs * c->n_kv_heads;
+  p.per = rows < kTileRows ? 16 : 16 * kTileWaves;
+  p.row_tiles = (int)((rows + p.per - 1) / p.per);
+  const int64_t groups = seqs * p.row_tiles;
+  p.chunk = p.per > 16 ? tile_chunk_of(groups, max_kv) : chunk_of(groups, max_kv);
   p.n_chunks = (max_kv + p.chunk - 1) / p.chunk;
   p.grid = groups * p.n_chunks;
-  if (p.grid > INT_MAX) return false;
+  if (p.grid > INT_MAX || n_tokens * n_heads > INT_MAX) return false;
   const size_t n = p.n_chunks > 1 ? (size_t)p.n_chunks * n_tokens * n_heads : 0;
   p.off_ml = align_up(n * c->head_dim * sizeof(float));
   p.total = p.off_ml + align_up(n * sizeof(float2));
@@ -471,11 +926,17 @@ static bool attn_plan(int64_t n_tokens, int n_heads, const gptq_kv4_cache* c, in
 
 template <typename T>
 static int attend(const AttnArgs& a, const KvDev& c, const KvBatch& q, const AttnPlan& p, int hd, hipStream_t s) {
-  if (hd == 128) kv4_rows_kernel<T, 128><<<(unsigned)p.grid, 256, 0, s>>>(a, c, q);
-  else kv4_rows_kernel<T, 64><<<(unsigned)p.grid, 256, 0, s>>>(a, c, q);
+  if (p.per > 16) {
+    if (hd == 128) kv4_tile_kernel<T, 128><<<(unsigned)p.grid, 64 * kTileWaves, 0, s>>>(a, c, q);
+    else kv4_tile_kernel<T, 64><<<(unsigned)p.grid, 64 * kTileWaves, 0, s>>>(a, c, q);
+  } else {
+    const dim3 grid((unsigned)(p.grid / c.n_seqs), (unsigned)std::min(c.n_seqs, 32768), (unsigned)((c.n_seqs + 32767) / 32768));
+    if (hd == 128) kv4_rows_kernel<T, 128><<<grid, 256, 0, s>>>(a, c, q);
+    else kv4_rows_kernel<T, 64><<<grid, 256, 0, s>>>(a, c, q);
+  }
   GPTQ_LAUNCH_CHECK();
   if (p.n_chunks > 1) {
-    const unsigned grid = (unsigned)((q.n_tokens * a.n_heads + 3) / 4);
+    const unsigned grid = (unsigned)(q.n_tokens * a.n_heads);
     if (hd == 128) kv4_join_kernel<T, 128><<<grid, 256, 0, s>>>(a, c, q);
     else kv4_join_kernel<T, 64><<<grid, 256, 0, s>>>(a, c, q);
     GPTQ_LAUNCH_CHECK();
@@ -536,9 +997,10 @@ extern "C" int gptq_kv4_attention(const void* Q, gptq_dtype dtype, int64_t n_tok
   if (!Q || !out || ldq < row || ldo < row || ldq % 8 != 0 || ldo % 8 != 0 || !al16(Q) || !al16(out)) return GPTQ_ERR_INVALID_ARG;
   if (p.total && (!ws || ws_bytes < p.total || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)))) return GPTQ_ERR_WORKSPACE;
   char* w = static_cast<char*>(ws);
+  const float scale2 = std::max(std::fabs(scale) * 1.44269504088896341f, 1.0e-30f);
   AttnArgs a{static_cast<const uint16_t*>(Q), static_cast<uint16_t*>(out), ldq, ldo, n_heads, n_heads / cache->n_kv_heads,
              max_q_len, (int)std::min<int64_t>(max_kv_len, (int64_t)cache->max_pages * cache->page_size),
-             scale * 1.44269504088896341f, p.chunk, p.n_chunks, p.row_tiles, reinterpret_cast<float*>(w),
+             scale2, std::min(kLazy / scale2, 1.0e29f), scale < 0.0f ? 0x80008000u : 0u, p.chunk, p.n_chunks, p.row_tiles, reinterpret_cast<float*>(w),
              reinterpret_cast<float2*>(w + p.off_ml)};
   const KvDev c = dev_of(cache);
   const KvBatch q{q_start, kv_len, n_tokens};

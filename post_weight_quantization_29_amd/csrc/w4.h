@@ -35,6 +35,15 @@ template <typename T> GPTQ_DEV uint16_t bits16(float a) { return __builtin_bit_c
 template <typename T> GPTQ_DEV float lo16f(uint32_t p) { return (float)__builtin_bit_cast(T, (uint16_t)p); }
 template <typename T> GPTQ_DEV float hi16f(uint32_t p) { return (float)__builtin_bit_cast(T, (uint16_t)(p >> 16)); }
 
+// (v & mask) | base in one instruction: it takes one scalar operand, so the
+// mask is held in a scalar and the base in a vector register (left to itself
+// the compiler folds both as literals into two instructions)
+GPTQ_DEV uint32_t and_or(uint32_t v, uint32_t mask, uint32_t base) {
+  uint32_t r;
+  asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(v), "s"(mask), "v"(base));
+  return r;
+}
+
 // ---------------------------------------------------------------- dequantization
 // The eight weights of word p in order, as four packed pairs: w = RN16(RN32(
 // scale * (code - zero))), bit for bit gptq_w4a16_gemm's.
@@ -48,15 +57,14 @@ template <typename T> GPTQ_DEV float hi16f(uint32_t p) { return (float)__builtin
 // multiplication; single-token products are bound by that count next to HBM.
 constexpr float kZeroFast = 1000.0f;
 
-GPTQ_DEV float mix_lo(uint32_t n, float s) {
-  float r;
-  asm("v_fma_mix_f32 %0, %1, %2, 0 op_sel:[0,0,0] op_sel_hi:[1,0,0]" : "=v"(r) : "v"(n), "v"(s));
-  return r;
+// an fp16 half of n, as fp32, times s plus a: one mixed instruction.  (Left to
+// the compiler, not asm: it also places the waits that an operand fresh from a
+// matrix instruction or an exponential needs.)
+GPTQ_DEV float fma_lo(uint32_t n, float s, float a) {
+  return __builtin_fmaf((float)__builtin_bit_cast(_Float16, (uint16_t)n), s, a);
 }
-GPTQ_DEV float mix_hi(uint32_t n, float s) {
-  float r;
-  asm("v_fma_mix_f32 %0, %1, %2, 0 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(r) : "v"(n), "v"(s));
-  return r;
+GPTQ_DEV float fma_hi(uint32_t n, float s, float a) {
+  return __builtin_fmaf((float)__builtin_bit_cast(_Float16, (uint16_t)(n >> 16)), s, a);
 }
 
 // -(1024 + zero) in both halves, for |zero| <= kZeroFast
@@ -71,10 +79,10 @@ GPTQ_DEV void dequant_fast(uint32_t p, float s, uint32_t zp, uint32_t (&w)[4]) {
   float a[4], b[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const uint32_t c = ((p >> (4 * k)) & 0x000F000Fu) | 0x64006400u;
+    const uint32_t c = and_or(p >> (4 * k), 0x000F000Fu, 0x64006400u);
     const f16x2w_t n = __builtin_bit_cast(f16x2w_t, c) + __builtin_bit_cast(f16x2w_t, zp);
-    a[k] = mix_lo(__builtin_bit_cast(uint32_t, n), s);
-    b[k] = mix_hi(__builtin_bit_cast(uint32_t, n), s);
+    a[k] = fma_lo(__builtin_bit_cast(uint32_t, n), s, 0.0f);
+    b[k] = fma_hi(__builtin_bit_cast(uint32_t, n), s, 0.0f);
   }
   w[0] = pack2<T>(a[0], a[1]);
   w[1] = pack2<T>(a[2], a[3]);
