@@ -47,6 +47,12 @@ GPTQ_DEV void copy16_lds(uint32_t lds_dst, const i32x4g_t& rsrc, int voff) {
                : "s"(__builtin_amdgcn_readfirstlane((int)lds_dst)), "v"(voff), "s"(rsrc)
                : "memory", "m0");
 }
+GPTQ_DEV void copy4_lds(uint32_t lds_dst, const i32x4g_t& rsrc, int voff) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane((int)lds_dst)), "v"(voff), "s"(rsrc)
+               : "memory", "m0");
+}
 template <int N> GPTQ_DEV void wait_copies() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
 }

@@ -1,6 +1,7 @@
 // Attention over a paged cache held in 4 bits: gptq_kv4_append, gptq_kv4_read
 // and gptq_kv4_attention.  A cached row (one token, one kv head) is head_dim
 // 4-bit codes with a step and a minimum: x = lo + step * code.
+#include "gemm16.h"
 #include "kv4.h"
 #include "w4_epilogue.h"
 
@@ -405,12 +406,12 @@ __global__ __launch_bounds__(256, 3) void kv4_rows_kernel(AttnArgs a, KvDev c, K
   }
 }
 
-// Many rows (prompts): a workgroup takes 128 rows, 16 to each of eight waves,
+// Many rows (prompts): a workgroup takes 192 rows, 16 to each of twelve waves,
 // and walks the keys in tiles of 64.  A tile's codes are unpacked once for the
-// eight waves: keys as 16 + code rows (waves 0..3), values transposed (waves
+// twelve: keys as 16 + code rows (waves 0..3), values transposed (waves
 // 4..7; channel rows, the keys of a 16-byte chunk in the order in which the
 // softmax's registers hold them), both in the activations' type, double
-// buffered; the next tile's words are loaded while one is multiplied.  Products
+// buffered; the packed words come three tiles ahead.  Products
 // and register layouts are those of kv4_rows_kernel.
 //
 // w_j = p_j step_j is rounded to the activations' type once, and what the
@@ -432,11 +433,12 @@ __global__ __launch_bounds__(256, 3) void kv4_rows_kernel(AttnArgs a, KvDev c, K
 //
 // 32 rows a wave on the 32 x 32 products read LDS half as often, but their 96
 // accumulators leave two waves per SIMD, and the loop then waits for LDS more
-// than it computes (279 us against KV4_TILE_US for 2565 tokens of 32 heads over
-// 4613 positions); 16 rows fit four waves.
+// than it computes (279 us against 226 for 2565 tokens of 32 heads over
+// 4613 positions); 16 rows fit three.
 constexpr float kNoStep = 1e-20f;
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 constexpr int kTileWaves = 12;
+constexpr uint32_t kRawSlots = 4, kRawBytes = 1024 + 128;
 
 template <typename T, int HD>
 __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kernel(AttnArgs a, KvDev c, KvBatch q) {
@@ -448,18 +450,20 @@ __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kern
   constexpr int TR = 16 * kTileWaves;
   // LDS: [buffer][keys 64 x HD | values HD x 64 | six rows x 64 | ks, kl, vs, vl | vmax, there]
   constexpr uint32_t kOffV = 64 * HD * 2, kOffX = 2 * kOffV, kOffG = kOffX + 8 * 128, kBuf = kOffG + 5 * 256;
-  __shared__ __attribute__((aligned(1024))) char smem[2 * kBuf];
+  __shared__ __attribute__((aligned(1024))) char smem[2 * kBuf + 8 * kRawSlots * kRawBytes];
   const uint32_t lds = (uint32_t)(uintptr_t)(LDS_AS const char*)smem;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i = lane & 15, g = lane >> 4;
-  // row tiles by falling length, folded
+  // Row tiles by falling length, so that what is left for the end is short; the
+  // heads shift by one from length to length: workgroups go to the XCDs in
+  // turn, and 32 CUs of one XCD on one head's keys at the same time wait for
+  // the same few lines of its L2 (369 us instead of 250).
   const int ch = blockIdx.x % a.n_chunks;
   int id = blockIdx.x / a.n_chunks;
-  const int items = a.row_tiles * c.n_kv * c.n_seqs;
-  id = id < (items + 1) / 2 ? 2 * id : 2 * (items - 1 - id) + 1;
-  const int rt = a.row_tiles - 1 - id / (c.n_kv * c.n_seqs);
-  id %= c.n_kv * c.n_seqs;
+  const int heads = c.n_kv * c.n_seqs;
+  const int rt = a.row_tiles - 1 - id / heads;
+  id = (id + rt) % heads;
   const int h = id % c.n_kv, b = id / c.n_kv;
   int64_t t0;
   int n_q;
@@ -510,7 +514,6 @@ __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kern
   const int kkey = HD == 128 ? lane >> 2 : (lane & 31) >> 1, kq = HD == 128 ? lane & 3 : lane & 1;
   const int vb = lane & (RW - 1), vz = (lane >> (HD == 128 ? 4 : 3)) & 1, vc = 2 * u + ((lane >> (HD == 128 ? 5 : 4)) & 1);
   const bool busy = HD == 128 || lane < 32;
-  const uint32_t k_off = 4 * (kkey * RW + 4 * kq), v_off = 4 * (4 * (vc & 3) * RW + vb);     // bytes
   const uint32_t v_sel = vz ? 0x07060302u : 0x05040100u;
   // LDS offsets of the lane's first chunk each; the others flip or add constants
   const int key_t = 16 * u + kkey, vchn = 8 * vb + 4 * vz;
@@ -529,35 +532,59 @@ __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kern
     rows_u = p < c1 ? kv_row(c, b, h, p) : -1;
     if (is_v) rows_o = po < c1 ? kv_row(c, b, h, po) : -1;
   };
-  uint32_t gw[8], gg = 0;
-  bool g_there = false;
-  auto load = [&](int n) {
+  // The packed words of a tile go HBM -> LDS without registers, kAhead tiles
+  // ahead, each wave its own (a wave waits for nobody else's): a slot holds 1 KB
+  // of codes (values: 8 rows each of two blocks), 16 grid words, a flag.
+  const uint32_t raw = lds + 2 * kBuf + (is_k || is_v ? wave : 0) * kRawSlots * kRawBytes;
+  const uint32_t code_off = is_k ? 16 * lane : 16 * (lane & (2 * HD / 8 - 1)) + 8 * (u & 1) * (HD / 2);
+  auto copy_tile = [&](int n) {
     if (!is_k && !is_v) return;
-    if (n - row_base >= 64) fetch_rows(n);
-    const int ru = __builtin_amdgcn_readlane(rows_u, n - row_base);
-    const uint32_t r = (uint32_t)max(ru, 0);
-    g_there = ru >= 0;
+    const int nn = min(n, n1 - 1);       // past the end: the last one again, so that the counts below hold
+    if (nn - row_base >= 64) fetch_rows(nn);
+    const int ru = __builtin_amdgcn_readlane(rows_u, nn - row_base);
+    const uint32_t r = (uint32_t)max(ru, 0), slot = raw + (n % kRawSlots) * kRawBytes;
+    if (lane == 0) *(LDS_AS int*)(uintptr_t)(slot + 1024 + 64) = ru >= 0;
+    auto from = [&](const uint32_t* p) {
+      return tile_rsrc(reinterpret_cast<uint64_t>(p), true);
+    };
     if (is_k) {
-      if (busy)
-        *reinterpret_cast<uint4*>(gw) =
-            *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(c.k_codes + (size_t)r * RW) + k_off);
-    } else if (is_v) {
-      const uint32_t ro = (uint32_t)max(__builtin_amdgcn_readlane(rows_o, n - row_base), 0);
-      const char* v0 = reinterpret_cast<const char*>(c.v_codes + (size_t)(u & 1 ? ro : r) * RW);
-      const char* v1 = reinterpret_cast<const char*>(c.v_codes + (size_t)(u & 1 ? r : ro) * RW);
-      if (busy) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          gw[e] = *reinterpret_cast<const uint32_t*>(v0 + v_off + 4 * e * RW);
-          gw[4 + e] = *reinterpret_cast<const uint32_t*>(v1 + v_off + 4 * e * RW);
-        }
+      const i32x4g_t rs = from(c.k_codes + (size_t)r * RW);
+      if (HD == 128 || lane < 32) copy16_lds(slot, rs, code_off);
+    } else {
+      const uint32_t ro = (uint32_t)max(__builtin_amdgcn_readlane(rows_o, nn - row_base), 0);
+      const i32x4g_t r0 = from(c.v_codes + (size_t)(u & 1 ? ro : r) * RW), r1 = from(c.v_codes + (size_t)(u & 1 ? r : ro) * RW);
+      if (lane < 2 * HD / 8) {
+        copy16_lds(slot, r0, code_off);
+        copy16_lds(slot + 512, r1, code_off);
       }
     }
-    // a key past the rows' end or on a missing page stands for zeros
-    const bool in = g_there && lane < 16 && 64 * n + 16 * u + lane < seen_max;
-    gg = in ? ((is_k ? c.k_grid : c.v_grid) + r)[lane] : 0u;
+    const i32x4g_t rg = from((is_k ? c.k_grid : c.v_grid) + r);
+    if (lane < 16) copy4_lds(slot + 1024, rg, 4 * lane);
   };
-  auto store = [&](uint32_t buf) {
+  // tile n into an unpacked buffer; `later` tiles' copies are still in flight
+  auto store = [&](int n, uint32_t buf) {
+    if (!is_k && !is_v) return;
+    if (is_k) wait_copies<2 * (kRawSlots - 2)>();
+    else wait_copies<3 * (kRawSlots - 2)>();
+    asm volatile("" ::: "memory");
+    const uint32_t slot = raw + (n % kRawSlots) * kRawBytes;
+    const bool g_there = *(LDS_AS const int*)(uintptr_t)(slot + 1024 + 64);
+    const bool in = g_there && 64 * n + 16 * u + i < seen_max;
+    // a key past the rows' end or on a missing page stands for zeros
+    const uint32_t gg = in ? *(LDS_AS const uint32_t*)(uintptr_t)(slot + 1024 + 4 * i) : 0u;
+    uint32_t gw[8];
+    if (is_k) {
+      const u32x4_t v = *(LDS_AS const u32x4_t*)(uintptr_t)(slot + 16 * (HD == 128 ? lane : lane & 31));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) gw[e] = v[e];
+    } else {
+      const LDS_AS uint32_t* p = (const LDS_AS uint32_t*)(uintptr_t)(slot + (4 * (vc & 1) * RW + vb) * 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        gw[e] = p[e * RW];
+        gw[4 + e] = p[128 + e * RW];
+      }
+    }
     auto put = [&](uint32_t at, uint4 v) { *(LDS_AS u32x4_t*)(uintptr_t)at = u32x4_t{v.x, v.y, v.z, v.w}; };
     // opaque, so that the flipped addresses are formed where they are used
     // instead of being kept in two dozen registers through the loop
@@ -576,7 +603,7 @@ __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kern
         grid(1) = fmaf(-kCodeBase, ks, grid_lo(gg));
         if (lane == 0) ((LDS_AS int*)tail)[4 + u] = g_there;
       }
-    } else if (is_v) {
+    } else {
       if (busy) {
         uint32_t z[4];
 #pragma unroll
@@ -639,16 +666,17 @@ __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kern
   for (int j = 0; j < NJ; ++j) o[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
   if (n0 < n1) {
-    fetch_rows(n0);
-    load(n0);
-    store(lds);
+    if (is_k || is_v) fetch_rows(n0);
+#pragma unroll
+    for (int e = 0; e < kRawSlots - 1; ++e) copy_tile(n0 + e);
+    store(n0, lds);
   }
   __syncthreads();
   uint32_t buf = lds, other = lds + kBuf;
   int n = n0;
   auto there = [&](int w) { return ((const LDS_AS int*)(uintptr_t)(buf + kOffG + 4 * 256 + 16))[w]; };
   auto next_tile = [&]() {
-    if (n + 1 < n1) store(other);
+    if (n + 1 < n1) store(n + 1, other);
     __syncthreads();
     const uint32_t t = buf;
     buf = other;
@@ -700,7 +728,7 @@ __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kern
         }
         grow = __any(mt > m + kLazy);
         if (grow) break;
-        if (n + 1 < n1) load(n + 1);
+        copy_tile(n + kRawSlots - 1);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           uint32_t pk[4];
@@ -747,9 +775,10 @@ __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kern
   tiles.template operator()<true>([&]() { return 64 * n + 64 <= wmin && (there(0) & there(1) & there(2) & there(3)); });
   tiles.template operator()<false>([&]() { return 64 * n < wmax; });
   while (n < n1) {
-    if (n + 1 < n1) load(n + 1);
+    copy_tile(n + kRawSlots - 1);
     next_tile();
   }
+  wait_copies<0>();                      // no copy may land after the workgroup's end
   if constexpr (kScaled) {
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
@@ -899,7 +928,7 @@ static int tile_chunk_of(int64_t groups, int max_kv) {
 constexpr int kTileRows = 33;
 
 struct AttnPlan {
-  int per;                   // rows per workgroup: 16, or the unpacked tiles' 128
+  int per;                   // rows per workgroup: 16, or the unpacked tiles' 192
   int chunk, n_chunks, row_tiles;
   int64_t grid;
   size_t off_ml, total;
