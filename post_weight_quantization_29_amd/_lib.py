@@ -399,27 +399,26 @@ def gptq_swiglu(G: torch.Tensor, U: torch.Tensor, M: torch.Tensor, stream=None) 
 GPTQ_ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 
-def _on(t: Optional[torch.Tensor], name: str, device, dtype=None, rows: bool = False) -> None:
-    """t is on `device`, of `dtype` and contiguous (rows: only inside its rows)."""
+def _on(t: Optional[torch.Tensor], name: str, index: int, dtype=None, rows: bool = False) -> None:
+    """t is on device `index`, of `dtype` and contiguous (rows: only inside its rows)."""
     if t is None:
         return
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if dtype is not None and t.dtype != dtype:
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if not (t.stride(-1) == 1 or t.shape[-1] == 1 if rows else t.is_contiguous()):
+    if not t.is_contiguous() and not (rows and (t.stride(-1) == 1 or t.shape[-1] == 1)):
         raise ValueError(f"{name} must be contiguous" + (" inside its rows" if rows else ""))
 
 
-def _shape(t: Optional[torch.Tensor], name: str, *shape) -> None:
-    if t is not None and tuple(t.shape) != shape:
+def _shape(t: Optional[torch.Tensor], name: str, shape: tuple) -> None:
+    if t is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
 
 
 def _pitch(t: torch.Tensor) -> int:
-    """Elements from one row to the next ([m, d] or [m, heads, d] with the heads side by side)."""
-    width = t[0].numel() if t.shape[0] else 0
-    return t.stride(0) if t.shape[0] > 1 else max(width, t.stride(0))
+    """Elements from one row to the next; a single row counts as one whose successor would be aligned."""
+    return t.stride(0) if t.shape[0] > 1 else (t.numel() + 7) & ~7
 
 
 def _act(act) -> int:
@@ -434,33 +433,30 @@ def _dtype16(t: torch.Tensor, name: str) -> int:
     return _DTYPE[t.dtype]
 
 
-def _run(name: str, device, stream, *args) -> None:
+def _run(name: str, index: int, stream, *args) -> None:
     """The call on `stream` (default: the tensors' device's current one), with that device current."""
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(device.index)
-    elif stream.device != device:
-        raise ValueError(f"{name}: the stream is on {stream.device}, the tensors are on {device}")
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device.index != index:
+        raise ValueError(f"{name}: the stream is on {stream.device}, the tensors are on cuda:{index}")
     else:
         raw = stream.cuda_stream
     f = getattr(lib(), name)
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == index:
         st = f(*args, raw)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             st = f(*args, raw)
     if st != OK:
         _check(st, name)
 
 
-def _scratch(nbytes: int, ws: Optional[torch.Tensor], device, stream):
-    """(tensor to keep until the call returns, its address, its bytes)."""
-    if ws is not None:
-        _on(ws, "ws", device)
-    elif nbytes == 0:
-        return None, None, 0
-    else:
-        ws = _ws(nbytes, None, device, stream)
-    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+def _scratch(nbytes: int, ws: Optional[torch.Tensor], index: int, stream) -> torch.Tensor:
+    """The caller's workspace or one of nbytes (the tensor has to live until the call returns)."""
+    if ws is None:
+        return _ws(nbytes, None, torch.device("cuda", index), stream)
+    _on(ws, "ws", index)
+    return ws
 
 
 class W4Weight:
@@ -470,18 +466,19 @@ class W4Weight:
 
     def __init__(self, packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, group_size: int = 128,
                  perm: Optional[torch.Tensor] = None):
-        _on(packed, "packed", packed.device); _on(scales, "scales", packed.device, torch.float32)
-        _on(zeros, "zeros", packed.device, torch.int32); _on(perm, "perm", packed.device, torch.int32)
+        index = packed.device.index if packed.is_cuda else 0
+        _on(packed, "packed", index); _on(scales, "scales", index, torch.float32)
+        _on(zeros, "zeros", index, torch.int32); _on(perm, "perm", index, torch.int32)
         if packed.dtype not in (torch.int32, torch.uint32):
             raise ValueError(f"packed must be int32 or uint32, got {packed.dtype}")
         d_out, words = packed.shape
         G = 8 * words if group_size == -1 else group_size
         if G <= 0 or G % 8:
             raise ValueError(f"group_size must be -1 or a multiple of 8, got {group_size}")
-        _shape(scales, "scales", d_out, -(-8 * words // G)); _shape(zeros, "zeros", d_out, -(-8 * words // G))
-        _shape(perm, "perm", 8 * words)
+        _shape(scales, "scales", (d_out, -(-8 * words // G))); _shape(zeros, "zeros", (d_out, -(-8 * words // G)))
+        _shape(perm, "perm", (8 * words,))
         self.packed, self.scales, self.zeros, self.perm, self.group_size = packed, scales, zeros, perm, group_size
-        self.d_out, self.d_in, self.device = d_out, 8 * words, packed.device
+        self.d_out, self.d_in, self.index = d_out, 8 * words, index
         self.c = gptq_w4_weight(_ptr(packed), _ptr(scales), _ptr(zeros), _ptr(perm), d_out, 8 * words, group_size,
                                 scales.shape[1])
         self.ref = ctypes.pointer(self.c)
@@ -495,37 +492,44 @@ def gptq_w4_linear(X: torch.Tensor, w: W4Weight, Y: torch.Tensor, bias: Optional
                    act: str = "none", R: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
                    stream=None) -> None:
     """Y [m, d_out] = act(X W^T + bias) + R.  X, Y and R may have pitched rows; R may be Y."""
-    dev = w.device
+    dev, m = w.index, X.shape[0]
     _on(X, "X", dev, rows=True); _on(Y, "Y", dev, rows=True)
-    _on(bias, "bias", dev, X.dtype); _on(R, "R", dev, Y.dtype, rows=True)
-    m = X.shape[0]
-    _shape(X, "X", m, w.d_in); _shape(Y, "Y", m, w.d_out); _shape(bias, "bias", w.d_out); _shape(R, "R", m, w.d_out)
+    _shape(X, "X", (m, w.d_in)); _shape(Y, "Y", (m, w.d_out))
+    if bias is not None:
+        _on(bias, "bias", dev, X.dtype); _shape(bias, "bias", (w.d_out,))
+    if R is not None:
+        _on(R, "R", dev, Y.dtype, rows=True); _shape(R, "R", (m, w.d_out))
     xt = _dtype16(X, "X")
     if Y.dtype not in _DTYPE:
         raise ValueError(f"Y must be float32, float16 or bfloat16, got {Y.dtype}")
-    keep, wp, wn = _scratch(0 if ws is not None else gptq_w4_linear_workspace_size(m, w), ws, dev, stream)
+    ws = _scratch(0 if ws is not None else gptq_w4_linear_workspace_size(m, w), ws, dev, stream)
     _run("gptq_w4_linear", dev, stream, X.data_ptr(), xt, m, _pitch(X), w.ref, _ptr(bias), _act(act), _ptr(R),
-         0 if R is None else _pitch(R), Y.data_ptr(), _DTYPE[Y.dtype], _pitch(Y), wp, wn)
+         0 if R is None else _pitch(R), Y.data_ptr(), _DTYPE[Y.dtype], _pitch(Y), ws.data_ptr(), ws.nbytes)
 
 
 def gptq_w4_gated_workspace_size(m: int, gate: W4Weight, up: W4Weight) -> int:
     return int(lib().gptq_w4_gated_workspace_size(m, gate.ref, up.ref))
 
 
+def _same_device(gate: W4Weight, up: W4Weight) -> None:
+    if gate.index != up.index:
+        raise ValueError(f"gate is on cuda:{gate.index}, up on cuda:{up.index}")
+
+
 def gptq_w4_gated(X: torch.Tensor, gate: W4Weight, up: W4Weight, M: torch.Tensor, G: Optional[torch.Tensor] = None,
                   U: Optional[torch.Tensor] = None, act: str = "silu", ws: Optional[torch.Tensor] = None,
                   stream=None) -> None:
     """M [m, f] = act(X Wg^T) * (X Wu^T); G and U, where given, take both products for the backward pass."""
-    dev = gate.device
-    _on(X, "X", dev, rows=True); _on(up.packed, "up", dev)
-    m = X.shape[0]
-    _shape(X, "X", m, gate.d_in)
+    dev, m = gate.index, X.shape[0]
+    _same_device(gate, up)
+    _on(X, "X", dev, rows=True); _shape(X, "X", (m, gate.d_in))
     for t, n in ((M, "M"), (G, "G"), (U, "U")):
-        _on(t, n, dev, X.dtype); _shape(t, n, m, gate.d_out)
+        if t is not None:
+            _on(t, n, dev, X.dtype); _shape(t, n, (m, gate.d_out))
     xt = _dtype16(X, "X")
-    keep, wp, wn = _scratch(0 if ws is not None else gptq_w4_gated_workspace_size(m, gate, up), ws, dev, stream)
+    ws = _scratch(0 if ws is not None else gptq_w4_gated_workspace_size(m, gate, up), ws, dev, stream)
     _run("gptq_w4_gated", dev, stream, X.data_ptr(), xt, m, _pitch(X), gate.ref, up.ref, _act(act), _ptr(G), _ptr(U),
-         M.data_ptr(), wp, wn)
+         M.data_ptr(), ws.data_ptr(), ws.nbytes)
 
 
 def gptq_w4_gated_backward_workspace_size(m: int, gate: W4Weight, up: W4Weight) -> int:
@@ -536,16 +540,16 @@ def gptq_w4_gated_backward(dM: torch.Tensor, G: torch.Tensor, U: torch.Tensor, g
                            dX: torch.Tensor, dG: Optional[torch.Tensor] = None, dU: Optional[torch.Tensor] = None,
                            act: str = "silu", ws: Optional[torch.Tensor] = None, stream=None) -> None:
     """dX [m, d], dG and dU [m, f] (optional) from dM and the forward pass's G and U."""
-    dev = gate.device
-    m = dM.shape[0]
-    _on(up.packed, "up", dev)
+    dev, m = gate.index, dM.shape[0]
+    _same_device(gate, up)
     for t, n in ((dM, "dM"), (G, "G"), (U, "U"), (dG, "dG"), (dU, "dU")):
-        _on(t, n, dev, dM.dtype); _shape(t, n, m, gate.d_out)
-    _on(dX, "dX", dev, dM.dtype); _shape(dX, "dX", m, gate.d_in)
+        if t is not None:
+            _on(t, n, dev, dM.dtype); _shape(t, n, (m, gate.d_out))
+    _on(dX, "dX", dev, dM.dtype); _shape(dX, "dX", (m, gate.d_in))
     dt = _dtype16(dM, "dM")
-    keep, wp, wn = _scratch(0 if ws is not None else gptq_w4_gated_backward_workspace_size(m, gate, up), ws, dev, stream)
+    ws = _scratch(0 if ws is not None else gptq_w4_gated_backward_workspace_size(m, gate, up), ws, dev, stream)
     _run("gptq_w4_gated_backward", dev, stream, dM.data_ptr(), G.data_ptr(), U.data_ptr(), dt, m, gate.ref, up.ref,
-         _act(act), _ptr(dG), _ptr(dU), dX.data_ptr(), wp, wn)
+         _act(act), _ptr(dG), _ptr(dU), dX.data_ptr(), ws.data_ptr(), ws.nbytes)
 
 
 # ---------------------------------------------------------------- a cache held in 4 bits
@@ -557,18 +561,18 @@ class KV4Cache:
 
     def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_grid: torch.Tensor, v_grid: torch.Tensor,
                  page_table: torch.Tensor):
-        dev = k_codes.device
+        dev = k_codes.device.index if k_codes.is_cuda else 0
         for t, n in ((k_codes, "k_codes"), (v_codes, "v_codes")):
-            _on(t, n, dev, torch.int32); _shape(t, n, *k_codes.shape)
+            _on(t, n, dev, torch.int32); _shape(t, n, tuple(k_codes.shape))
         for t, n in ((k_grid, "k_grid"), (v_grid, "v_grid")):
-            _on(t, n, dev, torch.float16); _shape(t, n, *k_codes.shape[:3], 2)
+            _on(t, n, dev, torch.float16); _shape(t, n, (*k_codes.shape[:3], 2))
         _on(page_table, "page_table", dev, torch.int32)
         n_pages, n_kv, page, words = k_codes.shape
         n_seqs, max_pages = page_table.shape
         if page <= 0 or page % 16 or 8 * words not in (64, 128):
             raise ValueError(f"page_size must be a multiple of 16 and head_dim 64 or 128, got {page} and {8 * words}")
         self.k_codes, self.v_codes, self.k_grid, self.v_grid, self.page_table = k_codes, v_codes, k_grid, v_grid, page_table
-        self.n_kv_heads, self.head_dim, self.page_size, self.n_seqs, self.device = n_kv, 8 * words, page, n_seqs, dev
+        self.n_kv_heads, self.head_dim, self.page_size, self.n_seqs, self.index = n_kv, 8 * words, page, n_seqs, dev
         self.c = gptq_kv4_cache(_ptr(k_codes), _ptr(v_codes), _ptr(k_grid), _ptr(v_grid), _ptr(page_table), n_pages,
                                 n_kv, page, 8 * words, n_seqs, max_pages)
         self.ref = ctypes.pointer(self.c)
@@ -582,26 +586,24 @@ class KV4Cache:
         return cls(*codes, *grids, page_table)
 
 
-def _heads(t: Optional[torch.Tensor], name: str, dev, heads: int, hd: int, dtype=None) -> None:
+def _heads(t: torch.Tensor, name: str, index: int, heads: int, hd: int, dtype=None) -> None:
     """[tokens, heads, hd], heads side by side inside a token's row."""
-    if t is None:
-        return
-    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, hd):
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != hd:
         raise ValueError(f"{name} must have shape (tokens, {heads}, {hd}), got {tuple(t.shape)}")
-    _on(t, name, dev, dtype, rows=True)
+    _on(t, name, index, dtype, rows=True)
     if heads > 1 and t.stride(1) != hd:
         raise ValueError(f"{name}'s heads must lie side by side")
 
 
 def _batch(cache: KV4Cache, q_start: torch.Tensor, kv_len: torch.Tensor) -> None:
-    _on(q_start, "q_start", cache.device, torch.int32); _shape(q_start, "q_start", cache.n_seqs + 1)
-    _on(kv_len, "kv_len", cache.device, torch.int32); _shape(kv_len, "kv_len", cache.n_seqs)
+    _on(q_start, "q_start", cache.index, torch.int32); _shape(q_start, "q_start", (cache.n_seqs + 1,))
+    _on(kv_len, "kv_len", cache.index, torch.int32); _shape(kv_len, "kv_len", (cache.n_seqs,))
 
 
 def gptq_kv4_append(cache: KV4Cache, K: torch.Tensor, V: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
                     stream=None) -> None:
     """Quantize the new tokens' K and V [tokens, n_kv_heads, head_dim] into the cache; kv_len counts them."""
-    dev = cache.device
+    dev = cache.index
     _batch(cache, q_start, kv_len)
     _heads(K, "K", dev, cache.n_kv_heads, cache.head_dim); _heads(V, "V", dev, cache.n_kv_heads, cache.head_dim, K.dtype)
     if V.shape[0] != K.shape[0] or K.dtype not in _DTYPE:
@@ -614,15 +616,16 @@ def gptq_kv4_append(cache: KV4Cache, K: torch.Tensor, V: torch.Tensor, q_start: 
 def gptq_kv4_read(cache: KV4Cache, K: Optional[torch.Tensor], V: Optional[torch.Tensor], q_start: torch.Tensor,
                   kv_len: torch.Tensor, stream=None) -> None:
     """K, V [tokens, n_kv_heads, head_dim] (each may be None): the values the cache holds for the batch's tokens."""
-    dev = cache.device
+    dev = cache.index
     _batch(cache, q_start, kv_len)
     some = K if K is not None else V
     if some is None:
         return
     for t, n in ((K, "K"), (V, "V")):
-        _heads(t, n, dev, cache.n_kv_heads, cache.head_dim, some.dtype); _on(t, n, dev)
-        if t is not None and t.shape[0] != some.shape[0]:
-            raise ValueError("K and V must have as many tokens")
+        if t is not None:
+            _heads(t, n, dev, cache.n_kv_heads, cache.head_dim, some.dtype); _on(t, n, dev)
+            if t.shape[0] != some.shape[0]:
+                raise ValueError("K and V must have as many tokens")
     if some.dtype not in _DTYPE:
         raise ValueError(f"K and V must be float32, float16 or bfloat16, got {some.dtype}")
     _run("gptq_kv4_read", dev, stream, cache.ref, _ptr(K), _ptr(V), _DTYPE[some.dtype], some.shape[0],
@@ -638,20 +641,20 @@ def gptq_kv4_attention(Q: torch.Tensor, cache: KV4Cache, q_start: torch.Tensor, 
                        max_kv_len: int, out: torch.Tensor, scale: Optional[float] = None,
                        ws: Optional[torch.Tensor] = None, stream=None) -> None:
     """out [tokens, n_heads, head_dim] = causal attention of Q over the cache (scale None: 1/sqrt(head_dim))."""
-    dev = cache.device
+    dev, hd = cache.index, cache.head_dim
     _batch(cache, q_start, kv_len)
     if Q.dim() != 3:
-        raise ValueError(f"Q must have shape (tokens, heads, {cache.head_dim}), got {tuple(Q.shape)}")
+        raise ValueError(f"Q must have shape (tokens, heads, {hd}), got {tuple(Q.shape)}")
     T, n_heads = Q.shape[0], Q.shape[1]
-    _heads(Q, "Q", dev, n_heads, cache.head_dim); _heads(out, "out", dev, n_heads, cache.head_dim, Q.dtype)
+    _heads(Q, "Q", dev, n_heads, hd); _heads(out, "out", dev, n_heads, hd, Q.dtype)
     if out.shape[0] != T:
         raise ValueError(f"out must have {T} tokens, got {out.shape[0]}")
     qt = _dtype16(Q, "Q")
     need = 0 if ws is not None else gptq_kv4_attention_workspace_size(T, n_heads, cache, max_q_len, max_kv_len)
-    keep, wp, wn = _scratch(need, ws, dev, stream)
+    ws = _scratch(need, ws, dev, stream)
     _run("gptq_kv4_attention", dev, stream, Q.data_ptr(), qt, T, n_heads, _pitch(Q), cache.ref, q_start.data_ptr(),
-         kv_len.data_ptr(), max_q_len, max_kv_len, cache.head_dim ** -0.5 if scale is None else float(scale),
-         out.data_ptr(), _pitch(out), wp, wn)
+         kv_len.data_ptr(), max_q_len, max_kv_len, hd ** -0.5 if scale is None else float(scale), out.data_ptr(),
+         _pitch(out), ws.data_ptr(), ws.nbytes)
 
 
 def gptq_layer_error_workspace_size(d_out: int, d_in: int) -> int:
