@@ -2,8 +2,8 @@
 // epilogue: the tile loop of the large products on the packed layer (B is the
 // weight dequantized to the workspace; 2 m n K operations dwarf that pass).
 //
-// A workgroup of four waves (2 x 2) takes 64 MB rows of A by 64 NB rows of B;
-// a wave holds NB x MB accumulators of v_mfma_f32_32x32x16.  Stages of 32 k are
+// A workgroup of WM x WN waves takes 32 MB WM rows of A by 32 NB WN rows of B; a
+// wave holds NB x MB accumulators of v_mfma_f32_32x32x16.  Stages of 32 k are
 // copied HBM -> LDS by buffer_load ... lds (16 bytes per lane, no staging
 // registers) into a ring of kRing slots, kRing - 2 stages ahead.  A stage row
 // is 64 bytes; its 16-byte chunk c sits at c ^ ((row / 4) % 4), so the sixteen
@@ -85,35 +85,36 @@ GPTQ_DEV bool tile_of(int wg, int tm, int tn, int& im, int& in) {
   return true;
 }
 
-template <typename T, int MB, int NB, typename Epi>
-__global__ __launch_bounds__(256, MB == 4 && NB == 4 ? 1 : 2) void gemm16_kernel(Gemm16Args g, Epi epi) {
+template <typename T, int MB, int NB, int WM, int WN, typename Epi>
+__global__ __launch_bounds__(64 * WM * WN, 2) void gemm16_kernel(Gemm16Args g, Epi epi) {
   typedef typename T16<T>::v8 v8;
-  constexpr int TM = 64 * MB, TN = 64 * NB;
+  constexpr int W = WM * WN, TM = 32 * MB * WM, TN = 32 * NB * WN;
   constexpr uint32_t kSlot = (TM + TN) * 64;
-  constexpr int kCopies = MB + NB;                 // copies per wave and stage
-  constexpr int kEpWave = 32 * MB * kEpPitch * 4 * Epi::kPlanes;
-  constexpr uint32_t kLds = kRing * kSlot > 4 * kEpWave ? kRing * kSlot : 4 * kEpWave;
+  constexpr int CA = TM / (16 * W), CB = TN / (16 * W), kCopies = CA + CB;   // copies per wave and stage
+  constexpr int kEpWave = 32 * kEpPitch * 4 * Epi::kPlanes;
+  constexpr uint32_t kLds = kRing * kSlot;
+  static_assert(W * kEpWave <= (int)kLds && TM % (16 * W) == 0 && TN % (16 * W) == 0, "tile");
   __shared__ __attribute__((aligned(1024))) char smem[kLds];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 1, wn = wave & 1;
+  const int wm = wave / WN, wn = wave % WN;
   int im, in;
   if (!tile_of(blockIdx.x, g.tiles_m, g.tiles_n, im, in)) return;
   const int64_t m0 = (int64_t)im * TM;
   const int n0 = in * TN;
   const uint32_t lds = (uint32_t)(uintptr_t)(LDS_AS const char*)smem;
 
-  // copy i of a stage: rows 16 (wave + 4 i) + lane / 4, chunk lane % 4
-  int voffA[MB], voffB[NB];
+  // copy i of a stage: rows 16 (wave + W i) + lane / 4, chunk lane % 4
+  int voffA[CA], voffB[CB];
   {
     const int R = 16 * wave + (lane >> 2);
     const int c = (lane & 3) ^ ((R >> 2) & 3);
 #pragma unroll
-    for (int i = 0; i < MB; ++i)
-      voffA[i] = m0 + R + 64 * i < g.m ? (int)((R + 64 * i) * g.lda * 2) + 16 * c : kPastEnd;
+    for (int i = 0; i < CA; ++i)
+      voffA[i] = m0 + R + 16 * W * i < g.m ? (int)((R + 16 * W * i) * g.lda * 2) + 16 * c : kPastEnd;
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
-      voffB[i] = n0 + R + 64 * i < g.n ? (int)((R + 64 * i) * g.ldb * 2) + 16 * c : kPastEnd;
+    for (int i = 0; i < CB; ++i)
+      voffB[i] = n0 + R + 16 * W * i < g.n ? (int)((R + 16 * W * i) * g.ldb * 2) + 16 * c : kPastEnd;
   }
   const uint64_t a0 = reinterpret_cast<uint64_t>(g.A0 + m0 * g.lda), a1 = reinterpret_cast<uint64_t>(g.A1 + m0 * g.lda);
   const uint64_t b0 = reinterpret_cast<uint64_t>(g.B + (int64_t)n0 * g.ldb);
@@ -124,8 +125,8 @@ __global__ __launch_bounds__(256, MB == 4 && NB == 4 ? 1 : 2) void gemm16_kernel
     rb = tile_rsrc(b0 + (uint64_t)k * (kGk * 2), live);
   };
   auto copy = [&](const i32x4g_t& ra, const i32x4g_t& rb, int slot, int q) {
-    if (q < MB) copy16_lds(lds + slot * kSlot + 4096u * q + 1024u * wave, ra, voffA[q < MB ? q : 0]);
-    else copy16_lds(lds + slot * kSlot + TM * 64 + 4096u * (q - MB) + 1024u * wave, rb, voffB[q >= MB ? q - MB : 0]);
+    if (q < CA) copy16_lds(lds + slot * kSlot + 1024u * (W * q + wave), ra, voffA[q < CA ? q : 0]);
+    else copy16_lds(lds + slot * kSlot + TM * 64 + 1024u * (W * (q - CA) + wave), rb, voffB[q >= CA ? q - CA : 0]);
   };
   // operand reads: row lane % 32 of a 32-row block, k chunk 2 slice + lane / 32
   const uint32_t sw = ((lane & 31) * 64) + (((lane >> 5) ^ ((lane >> 2) & 3)) << 4);
@@ -174,22 +175,25 @@ __global__ __launch_bounds__(256, MB == 4 && NB == 4 ? 1 : 2) void gemm16_kernel
         ring_barrier();
         rsrc_of(k + kRing - 1, ra, rb);
       }
-      constexpr int P = MB * NB;
+      constexpr int P = MB * NB, F = MB + NB;
 #pragma unroll
       for (int q = 0; q < P; ++q) {
         const int i = q / MB, j = q % MB;
         acc[i][j] = T16<T>::mfma32(opB[ks][i], opA[ks][j], acc[i][j]);
         // the next slice's operands and (last slice) the copies, spread over the MFMAs
 #pragma unroll
-        for (int f = q * kCopies / P; f < (q + 1) * kCopies / P; ++f) {
+        for (int f = q * F / P; f < (q + 1) * F / P; ++f) {
           if (!last) {
             if (f < MB) opA[1][f < MB ? f : 0] = rd(rdA1 + SLOT * kSlot + 2048u * f);
             else opB[1][f >= MB ? f - MB : 0] = rd(rdB1 + SLOT * kSlot + 2048u * (f - MB));
           } else {
             if (f < MB) opA[0][f < MB ? f : 0] = rd(rdA + NS * kSlot + 2048u * f);
             else opB[0][f >= MB ? f - MB : 0] = rd(rdB + NS * kSlot + 2048u * (f - MB));
-            copy(ra, rb, DS, f);
           }
+        }
+        if (last) {
+#pragma unroll
+          for (int f = q * kCopies / P; f < (q + 1) * kCopies / P; ++f) copy(ra, rb, DS, f);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -213,46 +217,47 @@ __global__ __launch_bounds__(256, MB == 4 && NB == 4 ? 1 : 2) void gemm16_kernel
   wait_copies<0>();
   __syncthreads();
 
-  // Epilogue: per block of 32 rows of B, the wave's tokens x 32 values go
-  // through its own part of LDS, so that a lane finishes eight neighbouring
-  // values of one token and stores 16 bytes.
+  // Epilogue: blocks of 32 tokens x 32 values (x kPlanes) go through the wave's
+  // own part of LDS, so that a lane finishes eight neighbouring values of one
+  // token and stores 16 bytes.
   float* ep = reinterpret_cast<float*>(smem) + wave * (kEpWave / 4);
   constexpr int PL = Epi::kPlanes;
   const int64_t mw = m0 + wm * 32 * MB;
 #pragma unroll
-  for (int ib = 0; ib < NB; ib += PL) {
+  for (int ib = 0; ib < NB; ib += PL)
 #pragma unroll
-    for (int p = 0; p < PL; ++p)
+    for (int j = 0; j < MB; ++j) {
 #pragma unroll
-      for (int j = 0; j < MB; ++j)
+      for (int p = 0; p < PL; ++p)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           f32x4_t v;
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = acc[ib + p][j][4 * q + e];
-          *reinterpret_cast<f32x4_t*>(ep + (p * 32 * MB + 32 * j + (lane & 31)) * kEpPitch + 8 * q + 4 * (lane >> 5)) = v;
+          *reinterpret_cast<f32x4_t*>(ep + (32 * p + (lane & 31)) * kEpPitch + 8 * q + 4 * (lane >> 5)) = v;
         }
-    __builtin_amdgcn_wave_barrier();
-    const int nb = (n0 + wn * 32 * NB + 32 * ib) / PL;   // first output column of the block
-    for (int t = 0; t < 2 * MB; ++t) {
-      const int tok = 16 * t + (lane >> 2), c = 8 * (lane & 3);
-      if (mw + tok < g.m) {
-        float v[PL][8];
+      __builtin_amdgcn_wave_barrier();
+      const int nb = (n0 + wn * 32 * NB + 32 * ib) / PL;   // first output column of the block
+#pragma unroll 1
+      for (int t = 0; t < 2; ++t) {
+        const int tok = 16 * t + (lane >> 2), c = 8 * (lane & 3);
+        if (mw + 32 * j + tok < g.m) {
+          float v[PL][8];
 #pragma unroll
-        for (int p = 0; p < PL; ++p) {
-          const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(ep + (p * 32 * MB + tok) * kEpPitch + c);
-          const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(ep + (p * 32 * MB + tok) * kEpPitch + c + 4);
+          for (int p = 0; p < PL; ++p) {
+            const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(ep + (32 * p + tok) * kEpPitch + c);
+            const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(ep + (32 * p + tok) * kEpPitch + c + 4);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[p][e] = lo[e];
-            v[p][4 + e] = hi[e];
+            for (int e = 0; e < 4; ++e) {
+              v[p][e] = lo[e];
+              v[p][4 + e] = hi[e];
+            }
           }
+          epi.template finish<8>(v, mw + 32 * j + tok, nb + c);
         }
-        epi.template finish<8>(v, mw + tok, nb + c);
       }
+      __builtin_amdgcn_wave_barrier();
     }
-    __builtin_amdgcn_wave_barrier();
-  }
 }
 
 }  // namespace gptq

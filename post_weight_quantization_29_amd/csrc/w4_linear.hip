@@ -354,15 +354,17 @@ static int launch_skinny(const uint16_t* X, int64_t ldx, int64_t m, const gptq_w
 template <typename T, typename Epi>
 static int launch_gemm16(Gemm16Args g, const Epi& epi, hipStream_t s) {
   auto tiles = [&](int tm, int tn) { return ((g.m + tm - 1) / tm) * (int64_t)((g.n + tn - 1) / tn); };
-  const bool big = tiles(256, 256) >= 192;
+  // A round of 256 large tiles takes 1, one of 512 small ones (two a CU) 2/3.
+  const int64_t r256 = (tiles(256, 256) + 255) / 256, r128 = (tiles(128, 128) + 511) / 512;
+  const bool big = 3 * r256 <= 2 * r128;
   const int64_t t = big ? tiles(256, 256) : tiles(128, 128);
   if (t > INT_MAX / 16) return GPTQ_ERR_INVALID_ARG;
   const int e = big ? 256 : 128;
   g.tiles_m = (int)((g.m + e - 1) / e);
   g.tiles_n = (g.n + e - 1) / e;
   const unsigned grid = (unsigned)(8 * ((t + 7) / 8));
-  if (big) gemm16_kernel<T, 4, 4, Epi><<<grid, 256, 0, s>>>(g, epi);
-  else gemm16_kernel<T, 2, 2, Epi><<<grid, 256, 0, s>>>(g, epi);
+  if (big) gemm16_kernel<T, 4, 2, 2, 4, Epi><<<grid, 512, 0, s>>>(g, epi);
+  else gemm16_kernel<T, 2, 2, 2, 2, Epi><<<grid, 256, 0, s>>>(g, epi);
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
 }
