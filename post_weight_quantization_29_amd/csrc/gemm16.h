@@ -5,19 +5,24 @@
 // A workgroup of WM x WN waves takes 32 MB WM rows of A by 32 NB WN rows of B; a
 // wave holds NB x MB accumulators of v_mfma_f32_32x32x16.  Stages of 32 k are
 // copied HBM -> LDS by buffer_load ... lds (16 bytes per lane, no staging
-// registers) into a ring of kRing slots, kRing - 2 stages ahead.  A stage row
-// is 64 bytes; its 16-byte chunk c sits at c ^ ((row / 4) % 4), so the sixteen
-// lanes that read sixteen consecutive rows of one chunk hit sixteen different
-// 16-byte columns of the 64 banks (the copy applies the swizzle by permuting
-// the lanes' source addresses).  The sync point of stage k sits before the last
-// k-slice of stage k-1: there every wave has waited for its copies of stage k
-// and has finished reading stage k-2, whose slot takes the next copies; the
-// last slice's MFMAs overlap the first operand reads of stage k.
+// registers) into a ring of five slots.  Two stages share each 128-byte cache
+// line of A and B, so they are copied as a pair, the second half of a line
+// right behind the first: copied a stage at a time, each line came through the
+// CU's L1 twice, and that path was busier than the matrix pipe.  Pair (k+4,
+// k+5) is issued when stage k (even) has been read, into its slot and the spare
+// one, three stages before it is needed.  Measured (8192 x 13824 x 5120, 4096 x
+// 4096 x 22016, 4096 x 22016 x 4096): 1.11, 1.18, 1.26 PFLOP/s, a stage at a
+// time 1.04, 1.08, 1.18; stages of 64 k in two slots the same within 2 %.
+// A stage row is 64 bytes; its 16-byte chunk c sits at c ^ ((row / 4) % 4), so
+// the sixteen lanes that read sixteen consecutive rows of one chunk hit sixteen
+// different 16-byte columns of the 64 banks (the copy applies the swizzle by
+// permuting the lanes' source addresses).  The sync point of a stage sits before
+// the last 16-k slice of the stage before it, whose MFMAs overlap the copies
+// and the next stage's first operand reads.
 //
-// What bounds it: the matrix pipe.  The 256 x 256 tile (MB = NB = 4) reads
-// 8 KB of operands from LDS per wave and 16 MFMAs, half of what LDS delivers;
-// the 128 x 128 tile (MB = NB = 2, two workgroups per CU) reads twice that per
-// MFMA and serves products with too few large tiles for 256 CUs.
+// The 256 x 256 tile (eight waves, two a SIMD) reads 6 KB of operands from LDS
+// per wave and 8 MFMAs; the 128 x 128 tile (four waves, two workgroups per CU)
+// serves products with too few large tiles for 256 CUs.
 #pragma once
 #include "w4.h"
 
@@ -26,19 +31,19 @@ namespace gptq {
 typedef int i32x4g_t __attribute__((ext_vector_type(4)));
 
 struct Gemm16Args {
-  const uint16_t* A0;   // stages [0, k0_stages)
-  const uint16_t* A1;   // stages after them (a second matrix of A's shape, its k from 0)
+  const uint16_t* A0;   // pairs of stages [0, k0_pairs)
+  const uint16_t* A1;   // pairs after them (a second matrix of A's shape, its k from 0)
   int64_t lda;          // elements, a multiple of 8
   const uint16_t* B;
   int64_t ldb;
   int64_t m;
   int n;                // rows of B that exist
-  int k0_stages, n_stages;
+  int k0_pairs, n_pairs;
   int tiles_m, tiles_n;
 };
 
-constexpr int kGk = 32;          // k per stage
-constexpr int kRing = 5;         // stage slots
+constexpr int kGk = 64;          // k per pair of stages
+constexpr int kSlots = 5;        // stage slots
 constexpr int kEpPitch = 36;     // floats per token row of the epilogue's LDS tile
 
 GPTQ_DEV void copy16_lds(uint32_t lds_dst, const i32x4g_t& rsrc, int voff) {
@@ -56,6 +61,8 @@ GPTQ_DEV void copy4_lds(uint32_t lds_dst, const i32x4g_t& rsrc, int voff) {
 template <int N> GPTQ_DEV void wait_copies() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
 }
+// before a slot is given back: the wave's own LDS reads of it are done
+GPTQ_DEV void wait_lds_reads() { __builtin_amdgcn_s_waitcnt(0xC07F); }
 GPTQ_DEV void ring_barrier() { asm volatile("s_barrier" ::: "memory"); }
 
 // rows past the end carry an offset beyond every buffer range: they read zero
@@ -89,10 +96,10 @@ template <typename T, int MB, int NB, int WM, int WN, typename Epi>
 __global__ __launch_bounds__(64 * WM * WN, 2) void gemm16_kernel(Gemm16Args g, Epi epi) {
   typedef typename T16<T>::v8 v8;
   constexpr int W = WM * WN, TM = 32 * MB * WM, TN = 32 * NB * WN;
-  constexpr uint32_t kSlot = (TM + TN) * 64;
-  constexpr int CA = TM / (16 * W), CB = TN / (16 * W), kCopies = CA + CB;   // copies per wave and stage
+  constexpr uint32_t kRow = kGk, kSlot = (TM + TN) * kRow;       // bytes of a stage row, of a stage
+  constexpr int CA = TM / (16 * W), CB = TN / (16 * W), kCopies = 2 * (CA + CB);   // copies per wave and pair
   constexpr int kEpWave = 32 * kEpPitch * 4 * Epi::kPlanes;
-  constexpr uint32_t kLds = kRing * kSlot;
+  constexpr uint32_t kLds = kSlots * kSlot;
   static_assert(W * kEpWave <= (int)kLds && TM % (16 * W) == 0 && TN % (16 * W) == 0, "tile");
   __shared__ __attribute__((aligned(1024))) char smem[kLds];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -118,20 +125,28 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm16_kernel(Gemm16Args g, E
   }
   const uint64_t a0 = reinterpret_cast<uint64_t>(g.A0 + m0 * g.lda), a1 = reinterpret_cast<uint64_t>(g.A1 + m0 * g.lda);
   const uint64_t b0 = reinterpret_cast<uint64_t>(g.B + (int64_t)n0 * g.ldb);
-  const int nk = g.n_stages;
-  auto rsrc_of = [&](int k, i32x4g_t& ra, i32x4g_t& rb) {
-    const bool live = k < nk;
-    ra = tile_rsrc(k < g.k0_stages ? a0 + (uint64_t)k * (kGk * 2) : a1 + (uint64_t)(k - g.k0_stages) * (kGk * 2), live);
-    rb = tile_rsrc(b0 + (uint64_t)k * (kGk * 2), live);
+  const int np = g.n_pairs;
+  // descriptors of a pair's first and second stages (an instruction offset
+  // would move the LDS address as well)
+  struct Pair {
+    i32x4g_t a[2], b[2];
   };
-  auto copy = [&](const i32x4g_t& ra, const i32x4g_t& rb, int slot, int q) {
-    if (q < CA) copy16_lds(lds + slot * kSlot + 1024u * (W * q + wave), ra, voffA[q < CA ? q : 0]);
-    else copy16_lds(lds + slot * kSlot + TM * 64 + 1024u * (W * (q - CA) + wave), rb, voffB[q >= CA ? q - CA : 0]);
+  auto rsrc_of = [&](int p) {
+    const bool live = p < np;
+    const uint64_t pa = p < g.k0_pairs ? a0 + (uint64_t)p * (kGk * 2) : a1 + (uint64_t)(p - g.k0_pairs) * (kGk * 2);
+    const uint64_t pb = b0 + (uint64_t)p * (kGk * 2);
+    return Pair{{tile_rsrc(pa, live), tile_rsrc(pa + 64, live)}, {tile_rsrc(pb, live), tile_rsrc(pb + 64, live)}};
+  };
+  // copy q of a pair: half q % 2 of the lines of copy q / 2, into slots s0, s1
+  auto copy = [&](const Pair& r, int s0, int s1, int q) {
+    const int y = q >> 1;
+    const uint32_t slot = lds + ((q & 1) ? s1 : s0) * kSlot;
+    if (y < CA) copy16_lds(slot + 1024u * (W * y + wave), r.a[q & 1], voffA[y < CA ? y : 0]);
+    else copy16_lds(slot + TM * kRow + 1024u * (W * (y - CA) + wave), r.b[q & 1], voffB[y >= CA ? y - CA : 0]);
   };
   // operand reads: row lane % 32 of a 32-row block, k chunk 2 slice + lane / 32
-  const uint32_t sw = ((lane & 31) * 64) + (((lane >> 5) ^ ((lane >> 2) & 3)) << 4);
-  const uint32_t rdA = lds + wm * (32 * MB * 64) + sw, rdB = lds + TM * 64 + wn * (32 * NB * 64) + sw;
-  const uint32_t rdA1 = rdA ^ 32u, rdB1 = rdB ^ 32u;   // slice 1: chunk 2 + lane / 32
+  const uint32_t sw = (lane & 31) * kRow + (((lane >> 5) ^ ((lane >> 2) & 3)) << 4);
+  const uint32_t rdA = lds + wm * (32 * MB * kRow) + sw, rdB = lds + TM * kRow + wn * (32 * NB * kRow) + sw;
   auto rd = [&](uint32_t at) { return *(LDS_AS const v8*)(uintptr_t)at; };
 
   f32x16_t acc[NB][MB];
@@ -142,76 +157,82 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm16_kernel(Gemm16Args g, E
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-  constexpr int kInFlight = (kRing - 3) * kCopies;
+  auto copy_pair = [&](int p, int s0, int s1) {
+    const Pair r = rsrc_of(p);
 #pragma unroll
-  for (int a = 0; a <= kRing - 3; ++a) {
-    i32x4g_t ra, rb;
-    rsrc_of(a, ra, rb);
-#pragma unroll
-    for (int q = 0; q < kCopies; ++q) copy(ra, rb, a, q);
-  }
-  wait_copies<kInFlight>();
+    for (int q = 0; q < kCopies; ++q) copy(r, s0, s1, q);
+  };
+  copy_pair(0, 0, 1);
+  copy_pair(1, 2, 3);
+  wait_copies<kCopies>();
   ring_barrier();
-  {
-    i32x4g_t ra, rb;
-    rsrc_of(kRing - 2, ra, rb);
-#pragma unroll
-    for (int q = 0; q < kCopies; ++q) copy(ra, rb, kRing - 2, q);
-  }
   v8 opA[2][MB], opB[2][NB];
 #pragma unroll
-  for (int j = 0; j < MB; ++j) opA[0][j] = rd(rdA + 2048u * j);
+  for (int j = 0; j < MB; ++j) opA[0][j] = rd(rdA + 32 * kRow * j);
 #pragma unroll
-  for (int i = 0; i < NB; ++i) opB[0][i] = rd(rdB + 2048u * i);
+  for (int i = 0; i < NB; ++i) opB[0][i] = rd(rdB + 32 * kRow * i);
 
-  auto stage = [&]<int SLOT>(int k) {
-    constexpr int NS = (SLOT + 1) % kRing, DS = (SLOT + kRing - 1) % kRing;
-    i32x4g_t ra, rb;
+  // Stage S of ten (the ring's period and the pairs'), in pair p
+  auto stage = [&]<int S>(int p) {
+    constexpr int SLOT = S % kSlots, NS = (S + 1) % kSlots, SPARE = (S + 4) % kSlots;
+    constexpr bool even = S % 2 == 0;
+    Pair r;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       const bool last = ks == 1;
       if (last) {
-        wait_copies<kInFlight>();
-        ring_barrier();
-        rsrc_of(k + kRing - 1, ra, rb);
+        if constexpr (even) {
+          // stage S's slot and the spare one are free once every wave has its last operands
+          wait_lds_reads();
+          ring_barrier();
+          r = rsrc_of(p + 2);
+        } else {
+          wait_copies<kCopies>();            // the next pair has landed
+          ring_barrier();
+        }
       }
       constexpr int P = MB * NB, F = MB + NB;
 #pragma unroll
       for (int q = 0; q < P; ++q) {
         const int i = q / MB, j = q % MB;
         acc[i][j] = T16<T>::mfma32(opB[ks][i], opA[ks][j], acc[i][j]);
-        // the next slice's operands and (last slice) the copies, spread over the MFMAs
+        // The next slice's operands, one (or two) per MFMA from the first on, in
+        // the order in which its MFMAs want them: B's first block, A's blocks,
+        // B's others.
 #pragma unroll
-        for (int f = q * F / P; f < (q + 1) * F / P; ++f) {
-          if (!last) {
-            if (f < MB) opA[1][f < MB ? f : 0] = rd(rdA1 + SLOT * kSlot + 2048u * f);
-            else opB[1][f >= MB ? f - MB : 0] = rd(rdB1 + SLOT * kSlot + 2048u * (f - MB));
-          } else {
-            if (f < MB) opA[0][f < MB ? f : 0] = rd(rdA + NS * kSlot + 2048u * f);
-            else opB[0][f >= MB ? f - MB : 0] = rd(rdB + NS * kSlot + 2048u * (f - MB));
-          }
+        for (int f = q * F / (P < F ? P : F); f < (q + 1) * F / (P < F ? P : F) && f < F; ++f) {
+          const bool isA = f >= 1 && f <= MB;
+          const int x = f == 0 ? 0 : isA ? f - 1 : f - MB;
+          // slice 1 is chunk 2 + lane / 32: bit 5 flips
+          const uint32_t at = ((isA ? rdA : rdB) ^ (last ? 0u : 32u)) + (last ? NS : SLOT) * kSlot + 32 * kRow * x;
+          if (isA) opA[ks ^ 1][isA ? x : 0] = rd(at);
+          else opB[ks ^ 1][isA ? 0 : x] = rd(at);
         }
-        if (last) {
+        if (last && even) {
 #pragma unroll
-          for (int f = q * kCopies / P; f < (q + 1) * kCopies / P; ++f) copy(ra, rb, DS, f);
+          for (int f = q * kCopies / P; f < (q + 1) * kCopies / P; ++f) copy(r, SPARE, SLOT, f);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
-  static_assert(kRing == 5, "stages run in groups of five");
-  int k = 0;
-  for (; k + 5 <= nk; k += 5) {
-    stage.template operator()<0>(k);
-    stage.template operator()<1>(k + 1);
-    stage.template operator()<2>(k + 2);
-    stage.template operator()<3>(k + 3);
-    stage.template operator()<4>(k + 4);
+  auto pair = [&]<int S>(int p) {
+    stage.template operator()<S>(p);
+    stage.template operator()<S + 1>(p);
+  };
+  static_assert(kSlots == 5, "ten stages to a turn");
+  int p = 0;
+  for (; p + 5 <= np; p += 5) {
+    pair.template operator()<0>(p);
+    pair.template operator()<2>(p + 1);
+    pair.template operator()<4>(p + 2);
+    pair.template operator()<6>(p + 3);
+    pair.template operator()<8>(p + 4);
   }
-  if (k < nk) stage.template operator()<0>(k++);
-  if (k < nk) stage.template operator()<1>(k++);
-  if (k < nk) stage.template operator()<2>(k++);
-  if (k < nk) stage.template operator()<3>(k++);
+  if (p < np) pair.template operator()<0>(p++);
+  if (p < np) pair.template operator()<2>(p++);
+  if (p < np) pair.template operator()<4>(p++);
+  if (p < np) pair.template operator()<6>(p++);
 
   // the copies issued past the end (they write zeros) land before the ring is reused
   wait_copies<0>();
