@@ -4,8 +4,9 @@
 // practice page m.lqnn.cn/news/117696, section 4.3: at inference the 4-bit
 // weights are dequantized to a 16-bit type and then multiplied.
 //
-//  few tokens (m <= kSkinnyMax)  w4_skinny_kernel: packed words go straight
-//                 into matrix-instruction operands; bound by reading the codes
+//  few tokens     w4_skinny_kernel (m < kMidMin), w4_mid_kernel (to kSkinnyMax):
+//                 packed words go straight into matrix-instruction operands;
+//                 bound by reading the codes
 //  more           w4_dense_kernel writes the 16-bit weight to the workspace
 //                 once, then gemm16_kernel; bound by the matrix pipe
 //  backward       dG, dU elementwise, the 16-bit weights transposed to the
@@ -25,20 +26,27 @@ struct W4Dev {
 static W4Dev dev_of(const gptq_w4_weight* w) { return W4Dev{w->packed, w->scales, w->zeros}; }
 
 // ---------------------------------------------------------------- few tokens
-// A wave holds 16 MT weight rows (of each of NMAT matrices) against 16 NT
+// A wave holds 16 weight rows (of each of NMAT matrices) against 16 NT
 // tokens on v_mfma_f32_16x16x32: operand lane l is row l % 16 with eight k of
 // k-group l / 16, which is exactly one packed word, so a word is dequantized
 // in registers where it is consumed and nothing goes through LDS.  A lane's
 // 16-byte load is four words, 32 k; a chunk (64 lanes) covers 16 rows x 128 k.
 // The NW waves of a workgroup split k in chunk pairs (256 k: one 128-byte line
 // per row), each with the next pair's loads in flight while one is multiplied,
-// and their sums are joined through LDS in wave order.  FAST: rows allow
-// 16-byte loads and a lane's 32 k share a group.
-template <typename T, int MT, int NT, int NMAT, int NW, bool FAST, typename Epi>
+// and their sums are joined through LDS in wave order.
+// GRID 0: any layout.  1: rows allow 16-byte loads and a lane's 32 k share a
+// group.  2: as 1, and the rows' scales and zero points fit LDS, where the
+// workgroup puts them first, in one coalesced sweep: loaded where they are
+// used, each touches 16 cache lines for 16 numbers, which cost more than the
+// codes themselves (11008 x 4096 gate and up, one token: 26 us, 17 from LDS).
+template <typename T, int NT, int NMAT, int NW, int GRID, typename Epi>
 __global__ __launch_bounds__(64 * NW) void w4_skinny_kernel(const uint16_t* __restrict__ X, int64_t ldx, int m, W4Dev wa,
                                                             W4Dev wb, int d_out, int d_in, int G, int ng, Epi epi) {
   typedef typename T16<T>::v8 v8;
+  constexpr bool FAST = GRID > 0;
+  constexpr int MT = 1;
   constexpr int NG = FAST ? 1 : 4;          // (scale, zero) pairs per lane and chunk
+  extern __shared__ float2 sgrid[];         // [NMAT][16][ng + 1] (scale, zero) when GRID == 2
   __shared__ f32x4_t red[NW][NMAT * MT * NT][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r0 = blockIdx.x * 16 * MT;
@@ -70,9 +78,11 @@ __global__ __launch_bounds__(64 * NW) void w4_skinny_kernel(const uint16_t* __re
             o.s[0] = o.z[0] = 0.0f;                          // past the end: weights of 0
             if (k0 < d_in) {
               v = *reinterpret_cast<const uint4*>(prow + (k0 >> 3));
-              const int g = group_of(k0, G, invG);
-              o.s[0] = srow[g];
-              o.z[0] = (float)zrow[g];
+              if constexpr (GRID == 1) {
+                const int g = group_of(k0, G, invG);
+                o.s[0] = srow[g];
+                o.z[0] = (float)zrow[g];
+              }
             }
             o.p[0] = v.x; o.p[1] = v.y; o.p[2] = v.z; o.p[3] = v.w;
           } else {
@@ -106,6 +116,19 @@ __global__ __launch_bounds__(64 * NW) void w4_skinny_kernel(const uint16_t* __re
   for (int n = 0; n < NT; ++n) xrow[n] = X + (int64_t)min(16 * n + lr, m - 1) * ldx;   // tokens past the end: likewise
 
   if (wave < pairs) load(wave, cur);
+  if constexpr (GRID == 2) {
+    const int n = 16 * ng, have = min(n, (d_out - r0) * ng);
+#pragma unroll
+    for (int a = 0; a < NMAT; ++a) {
+      const W4Dev& w = a ? wb : wa;
+      for (int e = tid; e < have; e += 64 * NW) {
+        const int row = group_of(e, ng, 1.0f / (float)ng);
+        sgrid[(a * 16 + row) * (ng + 1) + e - row * ng] =
+            make_float2(w.scales[(size_t)r0 * ng + e], (float)w.zeros[(size_t)r0 * ng + e]);
+      }
+    }
+    __syncthreads();
+  }
   for (int pair = wave; pair < pairs; pair += NW) {
     if (pair + NW < pairs) load(pair + NW, nxt);
 #pragma unroll
@@ -121,7 +144,14 @@ __global__ __launch_bounds__(64 * NW) void w4_skinny_kernel(const uint16_t* __re
       for (int a = 0; a < NMAT; ++a)
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-          const Chunk& c = cur[u][a][t];
+          Chunk& c = cur[u][a][t];
+          if constexpr (GRID == 2) {
+            if (k0 < d_in) {
+              const float2 sz = sgrid[(a * 16 + min(lr, d_out - 1 - r0)) * (ng + 1) + group_of(k0, G, invG)];
+              c.s[0] = sz.x;
+              c.z[0] = sz.y;
+            }
+          }
           bool far = false;
 #pragma unroll
           for (int q = 0; q < NG; ++q) far |= fabsf(c.z[q]) > kZeroFast;
@@ -175,6 +205,166 @@ __global__ __launch_bounds__(64 * NW) void w4_skinny_kernel(const uint16_t* __re
     const int tok = 16 * (tile % NT) + (l & 15);
     if (tok < m) epi.template finish<4>(v, tok, r0 + 16 * (tile / NT) + 4 * (l >> 4));
   }
+}
+
+// ---------------------------------------------------------------- some tokens
+// 17 to 64 tokens: the activations no longer are a small part of what a CU
+// reads, so eight waves of 16 weight rows share them.  A workgroup takes 128
+// rows (64 of gate and 64 of up) against all tokens over a slice of k; stages
+// of 256 k of the activations are copied HBM -> LDS (buffer_load ... lds, 16
+// bytes a lane, three slots, two stages ahead), the codes go to registers two
+// stages ahead, the slice's scales and zero points to LDS first.  Slices'
+// sums go to the workspace and w4_join_kernel adds them in order and finishes
+// them.  Measured, 24 tokens, 28672 -> 8192: W4_MID_US against 129 us with
+// every 16 rows reading the activations themselves.
+// A token's row in LDS is 512 bytes; the 16-byte chunk c of its half y sits at
+// c ^ (token % 16): 16 tokens' reads of one chunk hit 16 columns of the banks.
+constexpr int kMidK = 256;          // k per stage
+constexpr int kMidSlots = 3;
+constexpr int kMidWaves = 8;
+
+template <typename T, int NT, int NMAT>
+__global__ __launch_bounds__(64 * kMidWaves, 2) void w4_mid_kernel(const uint16_t* __restrict__ X, int64_t ldx, int m, W4Dev wa,
+                                                                   W4Dev wb, int d_out, int d_in, int G, int ng, int slice_k,
+                                                                   int slice_groups, float* __restrict__ part) {
+  typedef typename T16<T>::v8 v8;
+  constexpr uint32_t kSlot = NT * 16 * 2 * kMidK;
+  constexpr int RB = 16 * kMidWaves / NMAT;          // rows of a matrix per workgroup
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  float2* sgrid = reinterpret_cast<float2*>(smem + kMidSlots * kSlot);   // [wave][16][slice_groups + 1]
+  const uint32_t lds = (uint32_t)(uintptr_t)(LDS_AS const char*)smem;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, lg = lane >> 4;
+  const int mat = NMAT == 2 ? wave / (kMidWaves / 2) : 0;
+  const int r0 = blockIdx.x * RB + 16 * (wave % (RB / 16));
+  const W4Dev& w = mat ? wb : wa;
+  const int nw = d_in >> 3;
+  const float invG = 1.0f / (float)G;
+  const int k_lo = blockIdx.y * slice_k, k_hi = min(k_lo + slice_k, d_in);
+  const int stages = (k_hi - k_lo + kMidK - 1) / kMidK;
+  const int g_lo = group_of(k_lo, G, invG);
+
+  // copy i of a stage: tokens 2 (wave + 8 i) + lane / 32, half (lane / 16) % 2, chunk lane % 16
+  const uint64_t xb = reinterpret_cast<uint64_t>(X);
+  int x_off[NT];
+  int x_k;
+  {
+    const int tl = 2 * wave + (lane >> 5);
+    x_k = 128 * ((lane >> 4) & 1) + 8 * ((lane & 15) ^ (tl & 15));
+#pragma unroll
+    for (int i = 0; i < NT; ++i) x_off[i] = (int)(min(tl + 16 * i, m - 1) * ldx + x_k) * 2;
+  }
+  auto copy_x = [&](int st) {
+    const int k0 = k_lo + st * kMidK;
+    const i32x4g_t rs = tile_rsrc(xb + (uint64_t)k0 * 2, st < stages);
+    const bool in = k0 + x_k < k_hi;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+      copy16_lds(lds + (st % kMidSlots) * kSlot + 1024u * (wave + kMidWaves * i), rs, in ? x_off[i] : kPastEnd);
+  };
+  // Codes of stage st: 32 k at k0 + 32 lg and at 128 further.  Past the slice's
+  // end the last ones again, with scale 0: always two loads, as the waits count.
+  const uint32_t* prow = w.packed + (size_t)min(r0 + lr, d_out - 1) * nw;
+  uint4 p[3][2];
+  auto load_p = [&](int st, uint4 (&o)[2]) {
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+      o[y] = *reinterpret_cast<const uint4*>(prow + (min(k_lo + st * kMidK + 128 * y + 32 * lg, k_hi - 32) >> 3));
+  };
+  f32x4_t acc[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) acc[n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+  load_p(0, p[0]);
+  copy_x(0);
+  load_p(1, p[1]);
+  copy_x(1);
+  // this wave's scales and zero points; 0, 0 past the ends
+  {
+    const int n = 16 * slice_groups;
+    for (int e = lane; e < n; e += 64) {
+      const int row = e / slice_groups, g = e - row * slice_groups;
+      const bool in = r0 + row < d_out && g_lo + g < ng;
+      const size_t at = (size_t)(r0 + row) * ng + g_lo + g;
+      sgrid[(wave * 16 + row) * (slice_groups + 1) + g] = in ? make_float2(w.scales[at], (float)w.zeros[at]) : make_float2(0.0f, 0.0f);
+    }
+  }
+  const float2* grow = sgrid + (wave * 16 + lr) * (slice_groups + 1);
+  wait_copies<0>();
+  __syncthreads();
+
+  auto stage = [&]<int S>(int st) {
+    load_p(st + 2, p[(S + 2) % 3]);
+    copy_x(st + 2);
+    const uint32_t xs = lds + S * kSlot + lr * (2 * kMidK);
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int k = k_lo + st * kMidK + 128 * y + 32 * lg;
+      float2 sz = make_float2(0.0f, 0.0f);
+      if (k < k_hi) sz = grow[group_of(k, G, invG) - g_lo];
+      const uint32_t c[4] = {p[S][y].x, p[S][y].y, p[S][y].z, p[S][y].w};
+      uint32_t wv[4][4];
+      if (!__any(fabsf(sz.y) > kZeroFast)) {
+        const uint32_t zp = zero_pair(sz.y);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dequant_fast<T>(c[j], sz.x, zp, wv[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dequant_any<T>(c[j], sz.x, sz.y, wv[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const v8 a = __builtin_bit_cast(v8, make_uint4(wv[j][0], wv[j][1], wv[j][2], wv[j][3]));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const v8 b = *(LDS_AS const v8*)(uintptr_t)(xs + n * (16 * 2 * kMidK) + 256 * y + (((4 * lg + j) ^ lr) << 4));
+          acc[n] = T16<T>::mfma16(a, b, acc[n]);
+        }
+      }
+    }
+    // the next stage's copies are older than this stage's NT copies and two code loads
+    wait_copies<NT + 2>();
+    wait_lds_reads();
+    ring_barrier();
+  };
+  int st = 0;
+  for (; st + 3 <= stages; st += 3) {
+    stage.template operator()<0>(st);
+    stage.template operator()<1>(st + 1);
+    stage.template operator()<2>(st + 2);
+  }
+  if (st < stages) stage.template operator()<0>(st++);
+  if (st < stages) stage.template operator()<1>(st++);
+  wait_copies<0>();                     // no copy may land after the workgroup's end
+
+  // lane l: rows r0 + 4 (l / 16) + 0..3 of token 16 n + l % 16
+  const int dp = (d_out + 3) & ~3;
+  if (r0 + 4 * lg < dp) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      if (16 * n + lr < m)
+        *reinterpret_cast<f32x4_t*>(part + ((size_t)(blockIdx.y * NMAT + mat) * m + 16 * n + lr) * dp + r0 + 4 * lg) = acc[n];
+  }
+}
+
+// The slices' sums in order, and the epilogue: four outputs of a token per thread.
+template <typename Epi>
+__global__ __launch_bounds__(256) void w4_join_kernel(const float* __restrict__ part, int slices, int m, int d_out, Epi epi) {
+  constexpr int PL = Epi::kPlanes;
+  const int dp = (d_out + 3) & ~3;
+  const int c = 4 * (blockIdx.x * 256 + threadIdx.x), tok = blockIdx.y;
+  if (c >= dp) return;
+  float v[PL][4];
+#pragma unroll
+  for (int a = 0; a < PL; ++a) {
+    f32x4_t sum = *reinterpret_cast<const f32x4_t*>(part + ((size_t)a * m + tok) * dp + c);
+#pragma unroll 8
+    for (int s = 1; s < slices; ++s) sum += *reinterpret_cast<const f32x4_t*>(part + ((size_t)(s * PL + a) * m + tok) * dp + c);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[a][e] = sum[e];
+  }
+  epi.template finish<4>(v, tok, c);
 }
 
 // ---------------------------------------------------------------- operands of the large products
@@ -315,8 +505,8 @@ static unsigned grid_rows(int64_t rows) { return (unsigned)std::min<int64_t>(row
 
 // X has to be copied (and brought into processing order)
 static bool copies_x(const void* X, int64_t ldx, int64_t m, const gptq_w4_weight* w) {
-  if (w->perm || !aligned16(X) || (ldx % 8) != 0) return true;
-  return m > kSkinnyMax && (w->d_in % kGk != 0 || ldx * 2 > kMaxRowBytes);
+  if (w->perm || !aligned16(X) || (ldx % 8) != 0 || ldx * 2 > kMaxRowBytes) return true;
+  return m > kSkinnyMax && w->d_in % kGk != 0;
 }
 static size_t x_copy_bytes(int64_t m, int d_in) { return align_up((size_t)m * pad_k(d_in) * 2); }
 
@@ -328,24 +518,71 @@ static int order_x(const void* X, int64_t ldx, int64_t m, const gptq_w4_weight* 
   return GPTQ_OK;
 }
 
+// The slices of k that w4_mid_kernel takes for m tokens; no slices: it does not
+// (few tokens, or rows or groups that its loads do not fit).
+struct MidPlan {
+  int slices, slice_k, slice_groups;
+  size_t bytes;
+};
+constexpr int kMidMin = 17;                     // tokens from which it pays
+constexpr size_t kMidGridBytes = 48 << 10;      // LDS for the scales and zero points
+static MidPlan mid_plan(int64_t m, const gptq_w4_weight* wa, const gptq_w4_weight* wb) {
+  MidPlan p{0, 0, 0, 0};
+  const int G = w4_group(wa);
+  if (m < kMidMin || m > kSkinnyMax || wa->d_in % 32 != 0 || G % 32 != 0) return p;
+  if (!aligned16(wa->packed) || (wb && !aligned16(wb->packed))) return p;
+  const int64_t blocks = (wa->d_out + (wb ? 64 : 128) - 1) / (wb ? 64 : 128);
+  // two workgroups a CU, four stages a slice at least, scales that fit LDS
+  int64_t k = ((int64_t)wa->d_in * blocks / 512 + kMidK - 1) / kMidK * kMidK;
+  const int64_t groups = kMidGridBytes / (16 * kMidWaves * sizeof(float2)) - 2;
+  k = std::max<int64_t>(k, 4 * kMidK);
+  k = std::min<int64_t>(k, std::max<int64_t>((groups - 1) * G / kMidK * kMidK, kMidK));
+  p.slice_k = (int)std::min<int64_t>(k, (wa->d_in + kMidK - 1) / kMidK * kMidK);
+  p.slices = (wa->d_in + p.slice_k - 1) / p.slice_k;
+  p.slice_groups = std::min(p.slice_k / G + 2, wa->n_groups);
+  p.bytes = align_up((size_t)p.slices * (wb ? 2 : 1) * m * ((wa->d_out + 3) & ~3) * sizeof(float));
+  return p;
+}
+
+template <typename T, typename Epi>
+static int launch_mid(const uint16_t* X, int64_t ldx, int64_t m, const gptq_w4_weight* wa, const gptq_w4_weight* wb,
+                      const MidPlan& p, const Epi& epi, float* part, hipStream_t s) {
+  constexpr int NMAT = Epi::kPlanes;
+  const int d_out = wa->d_out, rb = 128 / NMAT;
+  const dim3 grid((unsigned)((d_out + rb - 1) / rb), (unsigned)p.slices);
+  auto go = [&]<int NT>() {
+    const size_t lds = (size_t)kMidSlots * NT * 16 * 2 * kMidK + (size_t)kMidWaves * 16 * (p.slice_groups + 1) * sizeof(float2);
+    w4_mid_kernel<T, NT, NMAT><<<grid, 64 * kMidWaves, lds, s>>>(X, ldx, (int)m, dev_of(wa), dev_of(wb), d_out, wa->d_in,
+                                                                 w4_group(wa), wa->n_groups, p.slice_k, p.slice_groups, part);
+  };
+  if (m <= 32) go.template operator()<2>();
+  else go.template operator()<4>();
+  GPTQ_LAUNCH_CHECK();
+  w4_join_kernel<Epi><<<dim3((unsigned)((d_out + 1023) / 1024), (unsigned)m), 256, 0, s>>>(part, p.slices, (int)m, d_out, epi);
+  GPTQ_LAUNCH_CHECK();
+  return GPTQ_OK;
+}
+
 template <typename T, int NMAT, typename Epi>
 static int launch_skinny(const uint16_t* X, int64_t ldx, int64_t m, const gptq_w4_weight* wa, const gptq_w4_weight* wb,
                          const Epi& epi, hipStream_t s) {
   const int G = w4_group(wa), d_out = wa->d_out, d_in = wa->d_in, ng = wa->n_groups;
   const W4Dev a = dev_of(wa), b = dev_of(wb);
   const bool fast = (d_in % 32) == 0 && (G % 32) == 0 && aligned16(a.packed) && aligned16(b.packed);
-  auto go = [&]<int MT, int NT, bool FAST>() {
-    w4_skinny_kernel<T, MT, NT, NMAT, 8, FAST, Epi><<<(unsigned)((d_out + 16 * MT - 1) / (16 * MT)), 512, 0, s>>>(
+  // scales in LDS beside the sums of 8 waves (a workgroup may have 64 KB without further ado)
+  const size_t grid_bytes = (size_t)NMAT * 16 * (ng + 1) * sizeof(float2);
+  auto go = [&]<int NT, int GRID>() {
+    w4_skinny_kernel<T, NT, NMAT, 8, GRID, Epi><<<(unsigned)((d_out + 15) / 16), 512, GRID == 2 ? grid_bytes : 0, s>>>(
         X, ldx, (int)m, a, b, d_out, d_in, G, ng, epi);
   };
-  if (fast) {
-    if (m <= 16) go.template operator()<1, 1, true>();
-    else if (m <= 32) go.template operator()<1, 2, true>();
-    else go.template operator()<1, 4, true>();
+  if (m <= 16) {
+    if (fast && grid_bytes <= 40 * 1024) go.template operator()<1, 2>();
+    else if (fast) go.template operator()<1, 1>();
+    else go.template operator()<1, 0>();
+  } else if (m <= 32) {
+    go.template operator()<2, 0>();
   } else {
-    if (m <= 16) go.template operator()<1, 1, false>();
-    else if (m <= 32) go.template operator()<1, 2, false>();
-    else go.template operator()<1, 4, false>();
+    go.template operator()<4, 0>();
   }
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
@@ -391,7 +628,9 @@ static int forward(const void* X, int64_t ldx, int64_t m, const gptq_w4_weight* 
     x = xc;
     ldx = pad_k(wa->d_in);
   }
-  if (m <= kSkinnyMax) {
+  if (const MidPlan p = mid_plan(m, wa, wb); p.slices) {
+    return launch_mid<T>(x, ldx, m, wa, wb ? wb : wa, p, epi, reinterpret_cast<float*>(base + x_copy_bytes(m, wa->d_in)), s);
+  } else if (m <= kSkinnyMax) {
     return launch_skinny<T, Epi::kPlanes>(x, ldx, m, wa, wb ? wb : wa, epi, s);
   } else {
     uint16_t* w16 = reinterpret_cast<uint16_t*>(base + x_copy_bytes(m, wa->d_in));
@@ -404,11 +643,11 @@ static int forward(const void* X, int64_t ldx, int64_t m, const gptq_w4_weight* 
 
 static size_t forward_bytes(int64_t m, const gptq_w4_weight* wa, const gptq_w4_weight* wb) {
   const size_t rows = wb ? 2 * (size_t)((wa->d_out + 31) / 32 * 32) : (size_t)wa->d_out;
-  return x_copy_bytes(m, wa->d_in) + (m > kSkinnyMax ? align_up(rows * pad_k(wa->d_in) * 2) : 0);
+  return x_copy_bytes(m, wa->d_in) + (m > kSkinnyMax ? align_up(rows * pad_k(wa->d_in) * 2) : mid_plan(m, wa, wb).bytes);
 }
 // what this call touches of it
 static size_t forward_needs(const void* X, int64_t ldx, int64_t m, const gptq_w4_weight* wa, const gptq_w4_weight* wb) {
-  if (m <= kSkinnyMax && !copies_x(X, ldx, m, wa)) return 0;
+  if (m <= kSkinnyMax && !copies_x(X, ldx, m, wa) && !mid_plan(m, wa, wb).slices) return 0;
   return forward_bytes(m, wa, wb);
 }
 

@@ -53,6 +53,12 @@ LINEAR = [
     (32, 5, 640, 64, HF, HF, True, "none", True, False),
     (33, 64, 1000, 32, BF, BF, False, "silu", False, False),
     (64, 300, 256, 256, HF, F32, False, "none", True, True),
+    (17, 8, 32, 32, HF, HF, True, "none", True, False),
+    (24, 1000, 3008, 32, HF, F32, False, "none", True, True),
+    (29, 130, 7168, 128, BF, BF, True, "silu", True, False),
+    (40, 514, 1056, 96, BF, F32, False, "gelu", True, False),
+    (64, 129, 2080, -1, HF, BF, False, "none", False, False),
+    (16, 70, 14336, 32, BF, F32, False, "none", False, False),
     (65, 130, 264, 8, BF, BF, True, "relu", True, False),
     (129, 301, 288, 96, HF, HF, False, "gelu_tanh", True, False),
     (256, 512, 1024, 128, BF, F32, False, "none", False, True),
@@ -161,6 +167,8 @@ GATED = [
     (16, 512, 64, 128, BF, "silu", True, False),
     (30, 264, 33, 24, HF, "silu", False, True),
     (64, 384, 72, 128, BF, "gelu_tanh", True, False),
+    (20, 1312, 130, 32, BF, "silu", True, True),
+    (50, 2048, 67, 64, HF, "gelu_tanh", False, False),
     (66, 264, 97, 8, HF, "silu", True, False),
     (200, 320, 300, 64, BF, "gelu", True, True),
     (3100, 96, 2300, 32, BF, "silu", True, False),
