@@ -590,14 +590,16 @@ def _heads(t: torch.Tensor, name: str, index: int, heads: int, hd: int, dtype=No
     """[tokens, heads, hd], heads side by side inside a token's row."""
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != hd:
         raise ValueError(f"{name} must have shape (tokens, {heads}, {hd}), got {tuple(t.shape)}")
-    _on(t, name, index, dtype, rows=True)
-    if heads > 1 and t.stride(1) != hd:
+    if t.get_device() != index or (dtype is not None and t.dtype is not dtype):
+        _on(t, name, index, dtype, rows=True)
+    if not t.is_contiguous() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != hd)):
         raise ValueError(f"{name}'s heads must lie side by side")
 
 
 def _batch(cache: KV4Cache, q_start: torch.Tensor, kv_len: torch.Tensor) -> None:
-    _on(q_start, "q_start", cache.index, torch.int32); _shape(q_start, "q_start", (cache.n_seqs + 1,))
-    _on(kv_len, "kv_len", cache.index, torch.int32); _shape(kv_len, "kv_len", (cache.n_seqs,))
+    for t, n, name in ((q_start, cache.n_seqs + 1, "q_start"), (kv_len, cache.n_seqs, "kv_len")):
+        if t.dtype is not torch.int32 or t.get_device() != cache.index or t.numel() != n or not t.is_contiguous():
+            _on(t, name, cache.index, torch.int32); _shape(t, name, (n,))
 
 
 def gptq_kv4_append(cache: KV4Cache, K: torch.Tensor, V: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,

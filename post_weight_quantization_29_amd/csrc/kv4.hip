@@ -34,6 +34,12 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(KvDev c, KvBatch q, con
   const int lane = threadIdx.x & 63;
   const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (t >= q.n_tokens) return;
+  const void* src = blockIdx.y ? V : K;
+  const int64_t ld = blockIdx.y ? ldv : ldk;
+  // the first rows are on their way while their place is looked up (three
+  // loads, each on the one before)
+  float ahead[8];
+  load8<DT>(src, t * ld + (int64_t)min(lane / L, c.n_kv - 1) * HD + 8 * (lane % L), vec, ahead);
   const int b = seq_of_token(q.q_start, c.n_seqs, t);
   if (b < 0) return;
   int64_t t0;
@@ -42,8 +48,6 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(KvDev c, KvBatch q, con
   const int64_t p = (int64_t)q.kv_len[b] - n_q + (t - t0);
   const int64_t row0 = kv_row(c, b, 0, p);
   if (row0 < 0) return;
-  const void* src = blockIdx.y ? V : K;
-  const int64_t ld = blockIdx.y ? ldv : ldk;
   uint32_t* codes = blockIdx.y ? c.v_codes : c.k_codes;
   uint32_t* grid = blockIdx.y ? c.v_grid : c.k_grid;
   const int li = lane % L;
@@ -51,7 +55,9 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(KvDev c, KvBatch q, con
     const int h = h0 + lane / L;
     const bool in = h < c.n_kv;
     float x[8];
-    load8<DT>(src, t * ld + (int64_t)min(h, c.n_kv - 1) * HD + 8 * li, vec, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = ahead[e];
+    if (h0 + RPW < c.n_kv) load8<DT>(src, t * ld + (int64_t)min(h + RPW, c.n_kv - 1) * HD + 8 * li, vec, ahead);
     // values beyond fp16 count as its largest; fmin and fmax pass NaNs over
     float mn = kF16Max + 1.0f, mx = -kF16Max - 1.0f;
 #pragma unroll

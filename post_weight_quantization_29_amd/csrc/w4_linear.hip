@@ -215,7 +215,7 @@ __global__ __launch_bounds__(64 * NW) void w4_skinny_kernel(const uint16_t* __re
 // bytes a lane, three slots, two stages ahead), the codes go to registers two
 // stages ahead, the slice's scales and zero points to LDS first.  Slices'
 // sums go to the workspace and w4_join_kernel adds them in order and finishes
-// them.  Measured, 24 tokens, 28672 -> 8192: W4_MID_US against 129 us with
+// them.  Measured, 24 tokens, 28672 -> 8192: 51 us (and 5 to join) against 129 with
 // every 16 rows reading the activations themselves.
 // A token's row in LDS is 512 bytes; the 16-byte chunk c of its half y sits at
 // c ^ (token % 16): 16 tokens' reads of one chunk hit 16 columns of the banks.
@@ -224,7 +224,7 @@ constexpr int kMidSlots = 3;
 constexpr int kMidWaves = 8;
 
 template <typename T, int NT, int NMAT>
-__global__ __launch_bounds__(64 * kMidWaves, 2) void w4_mid_kernel(const uint16_t* __restrict__ X, int64_t ldx, int m, W4Dev wa,
+__global__ __launch_bounds__(64 * kMidWaves, NT == 2 ? 4 : 2) void w4_mid_kernel(const uint16_t* __restrict__ X, int64_t ldx, int m, W4Dev wa,
                                                                    W4Dev wb, int d_out, int d_in, int G, int ng, int slice_k,
                                                                    int slice_groups, float* __restrict__ part) {
   typedef typename T16<T>::v8 v8;
@@ -426,29 +426,36 @@ __global__ __launch_bounds__(256) void w4_dense_kernel(W4Dev wa, W4Dev wb, int d
 // The transposed 16-bit weights: out[channel c][k], row pitch 2 Fp, k = r for
 // the gate's row r and Fp + r for the up's; zeros from d_out to Fp.  Column q
 // of the packed layer goes to row perm[q].  A workgroup turns 64 rows x 16
-// words (128 columns) through LDS: 128-byte pieces out.
-constexpr int kTPitch = 64 + 8;
+// words (128 columns) through LDS, two rows to a 4-byte write: 128-byte pieces
+// out.  A column's eight 16-byte chunks (eight rows each) sit at chunk ^ (column
+// / 8) % 8, so the 16 words' writes spread over the banks.
 template <typename T>
 __global__ __launch_bounds__(256) void w4_dense_t_kernel(W4Dev wa, W4Dev wb, int d_out, int d_in, int G, int ng,
                                                          const int32_t* __restrict__ perm, int Fp, uint16_t* __restrict__ out) {
-  __shared__ __attribute__((aligned(16))) uint16_t tile[128 * kTPitch];
+  __shared__ __attribute__((aligned(16))) uint16_t tile[128 * 64];
   const W4Dev& w = blockIdx.z ? wb : wa;
   const int nw = d_in >> 3, tid = threadIdx.x;
-  const int q = blockIdx.x * 16 + (tid & 15);
+  const int ql = tid & 15, q = blockIdx.x * 16 + ql;
   const int gq = q < nw ? group_of(8 * q, G, 1.0f / (float)G) : 0;
   for (int rb = blockIdx.y; rb * 64 < Fp; rb += gridDim.y) {
     const int r0 = rb * 64;
+    uint32_t v[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int rl = (tid >> 4) + 16 * i, r = r0 + rl;
+      const int r = r0 + 2 * (tid >> 4) + 32 * (i >> 1) + (i & 1);
       const bool in = q < nw && r < d_out;
       const uint32_t p = in ? w.packed[(size_t)r * nw + q] : 0u;
       const float s = in ? w.scales[(size_t)r * ng + gq] : 0.0f, z = in ? (float)w.zeros[(size_t)r * ng + gq] : 0.0f;
-      uint32_t v[4];
-      dequant_word16<T>(p, s, z, v);
+      dequant_word16<T>(p, s, z, v[i]);
+    }
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        tile[(8 * (tid & 15) + e) * kTPitch + rl] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+    for (int i = 0; i < 2; ++i) {
+      const int rl = 2 * (tid >> 4) + 32 * i;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t two = __builtin_amdgcn_perm(v[2 * i + 1][e >> 1], v[2 * i][e >> 1], e & 1 ? 0x07060302u : 0x05040100u);
+        *reinterpret_cast<uint32_t*>(tile + (8 * ql + e) * 64 + (((rl >> 3) ^ (ql & 7)) << 3) + (rl & 7)) = two;
+      }
     }
     __syncthreads();
 #pragma unroll
@@ -457,7 +464,7 @@ __global__ __launch_bounds__(256) void w4_dense_t_kernel(W4Dev wa, W4Dev wb, int
       if (c < d_in && k < Fp) {
         const int ch = perm ? min(max(perm[c], 0), d_in - 1) : c;
         *reinterpret_cast<uint4*>(out + (size_t)ch * 2 * Fp + (size_t)blockIdx.z * Fp + k) =
-            *reinterpret_cast<const uint4*>(tile + cl * kTPitch + 8 * (tid & 7));
+            *reinterpret_cast<const uint4*>(tile + cl * 64 + (((tid & 7) ^ ((cl >> 3) & 7)) << 3));
       }
     }
     __syncthreads();
@@ -590,13 +597,15 @@ static int launch_skinny(const uint16_t* X, int64_t ldx, int64_t m, const gptq_w
 
 template <typename T, typename Epi>
 static int launch_gemm16(Gemm16Args g, const Epi& epi, hipStream_t s) {
-  auto tiles = [&](int tm, int tn) { return ((g.m + tm - 1) / tm) * (int64_t)((g.n + tn - 1) / tn); };
-  // A round of 256 large tiles takes 1, one of 512 small ones (two a CU) 2/3.
-  const int64_t r256 = (tiles(256, 256) + 255) / 256, r128 = (tiles(128, 128) + 511) / 512;
-  const bool big = 3 * r256 <= 2 * r128;
-  const int64_t t = big ? tiles(256, 256) : tiles(128, 128);
-  if (t > INT_MAX / 16) return GPTQ_ERR_INVALID_ARG;
+  auto tiles = [&](int64_t e) { return ((g.m + e - 1) / e) * ((g.n + e - 1) / e); };
+  // By rounds of the chip: 256 tiles of 256 x 256 take 1, 512 of 128 x 128 (two a
+  // CU) half the work at 3/4 of the rate, 2/3.  (256 x 192 tiles, one wave a
+  // SIMD, gained nothing where they fill the last round better: 577 x 5120 x
+  // 13824 149 us, as with 256 x 256.)
+  const bool big = 3 * ((tiles(256) + 255) / 256) <= 2 * ((tiles(128) + 511) / 512);
   const int e = big ? 256 : 128;
+  const int64_t t = tiles(e);
+  if (t > INT_MAX / 16) return GPTQ_ERR_INVALID_ARG;
   g.tiles_m = (int)((g.m + e - 1) / e);
   g.tiles_n = (g.n + e - 1) / e;
   const unsigned grid = (unsigned)(8 * ((t + 7) / 8));
