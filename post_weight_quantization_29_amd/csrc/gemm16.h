@@ -22,7 +22,9 @@
 //
 // The 256 x 256 tile (eight waves, two a SIMD) reads 6 KB of operands from LDS
 // per wave and 8 MFMAs; the 128 x 128 tile (four waves, two workgroups per CU)
-// serves products with too few large tiles for 256 CUs.
+// serves products with too few large tiles for 256 CUs.  Tiles past the last full
+// round may be split over k: their sums go to the workspace as they lie in
+// registers, and gemm16_join_kernel adds them in order and finishes them.
 #pragma once
 #include "w4.h"
 
@@ -40,6 +42,9 @@ struct Gemm16Args {
   int n;                // rows of B that exist
   int k0_pairs, n_pairs;
   int tiles_m, tiles_n;
+  int whole;            // tiles that one workgroup takes whole; the others' k is split
+  int slices, slice_pairs;
+  float* part;          // [slice][split tile][wave][block][4][lane] of four sums
 };
 
 constexpr int kGk = 64;          // k per pair of stages
@@ -79,17 +84,55 @@ GPTQ_DEV i32x4g_t tile_rsrc(uint64_t base, bool live) {
 }
 
 // Workgroups are dealt round-robin to the 8 XCDs, each with its own L2: XCD x
-// takes the x-th eighth of the tiles, in strips of four tile rows of A, so its
-// co-resident workgroups share panels of both operands.
-GPTQ_DEV bool tile_of(int wg, int tm, int tn, int& im, int& in) {
-  const int T = tm * tn, per = (T + 7) / 8;
-  const int idx = (wg & 7) * per + (wg >> 3);
-  if ((wg >> 3) >= per || idx >= T) return false;
+// takes the x-th eighth of the items, so its co-resident workgroups share panels
+// of both operands.  Tiles are counted in strips of four tile rows of A.
+GPTQ_DEV int item_of(int wg, int n) {
+  const int per = (n + 7) / 8, i = (wg & 7) * per + (wg >> 3);
+  return (wg >> 3) < per && i < n ? i : -1;
+}
+GPTQ_DEV void tile_of(int idx, int tm, int tn, int& im, int& in) {
   const int strip = idx / (4 * tn), rest = idx - strip * 4 * tn;
   const int h = min(4, tm - 4 * strip);
   im = 4 * strip + rest % h;
   in = rest / h;
-  return true;
+}
+
+// 32 tokens x 32 values (x kPlanes) go through the wave's own part of LDS, so
+// that a lane finishes eight neighbouring values of one token and stores 16
+// bytes.  Token tok0 + lane % 32 has values 8 q + 4 (lane / 32) + e in x[p][4 q + e].
+template <typename Epi>
+GPTQ_DEV void finish_block(const Epi& epi, float* ep, const f32x16_t (&x)[Epi::kPlanes], int64_t tok0, int64_t m, int col) {
+  constexpr int PL = Epi::kPlanes;
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int p = 0; p < PL; ++p)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      f32x4_t v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = x[p][4 * q + e];
+      *reinterpret_cast<f32x4_t*>(ep + (32 * p + (lane & 31)) * kEpPitch + 8 * q + 4 * (lane >> 5)) = v;
+    }
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+  for (int t = 0; t < 2; ++t) {
+    const int tok = 16 * t + (lane >> 2), c = 8 * (lane & 3);
+    if (tok0 + tok < m) {
+      float v[PL][8];
+#pragma unroll
+      for (int p = 0; p < PL; ++p) {
+        const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(ep + (32 * p + tok) * kEpPitch + c);
+        const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(ep + (32 * p + tok) * kEpPitch + c + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[p][e] = lo[e];
+          v[p][4 + e] = hi[e];
+        }
+      }
+      epi.template finish<8>(v, tok0 + tok, col + c);
+    }
+  }
+  __builtin_amdgcn_wave_barrier();
 }
 
 template <typename T, int MB, int NB, int WM, int WN, typename Epi>
@@ -105,8 +148,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm16_kernel(Gemm16Args g, E
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
+  // whole tiles first, then slice by slice the split ones
+  const int n_whole = (g.whole + 7) / 8 * 8, n_split = g.tiles_m * g.tiles_n - g.whole;
+  const bool split = (int)blockIdx.x >= n_whole;
+  const int item = split ? item_of(blockIdx.x - n_whole, n_split * g.slices) : item_of(blockIdx.x, g.whole);
+  if (item < 0) return;
+  const int slice = split ? item / n_split : 0;
   int im, in;
-  if (!tile_of(blockIdx.x, g.tiles_m, g.tiles_n, im, in)) return;
+  tile_of(split ? g.whole + item - slice * n_split : item, g.tiles_m, g.tiles_n, im, in);
+  const int p0 = slice * g.slice_pairs, np = split ? min(p0 + g.slice_pairs, g.n_pairs) : g.n_pairs;
   const int64_t m0 = (int64_t)im * TM;
   const int n0 = in * TN;
   const uint32_t lds = (uint32_t)(uintptr_t)(LDS_AS const char*)smem;
@@ -125,7 +175,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm16_kernel(Gemm16Args g, E
   }
   const uint64_t a0 = reinterpret_cast<uint64_t>(g.A0 + m0 * g.lda), a1 = reinterpret_cast<uint64_t>(g.A1 + m0 * g.lda);
   const uint64_t b0 = reinterpret_cast<uint64_t>(g.B + (int64_t)n0 * g.ldb);
-  const int np = g.n_pairs;
   // descriptors of a pair's first and second stages (an instruction offset
   // would move the LDS address as well)
   struct Pair {
@@ -162,8 +211,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm16_kernel(Gemm16Args g, E
 #pragma unroll
     for (int q = 0; q < kCopies; ++q) copy(r, s0, s1, q);
   };
-  copy_pair(0, 0, 1);
-  copy_pair(1, 2, 3);
+  copy_pair(p0, 0, 1);
+  copy_pair(p0 + 1, 2, 3);
   wait_copies<kCopies>();
   ring_barrier();
   v8 opA[2][MB], opB[2][NB];
@@ -221,7 +270,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm16_kernel(Gemm16Args g, E
     stage.template operator()<S + 1>(p);
   };
   static_assert(kSlots == 5, "ten stages to a turn");
-  int p = 0;
+  int p = p0;
   for (; p + 5 <= np; p += 5) {
     pair.template operator()<0>(p);
     pair.template operator()<2>(p + 1);
@@ -238,47 +287,67 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm16_kernel(Gemm16Args g, E
   wait_copies<0>();
   __syncthreads();
 
-  // Epilogue: blocks of 32 tokens x 32 values (x kPlanes) go through the wave's
-  // own part of LDS, so that a lane finishes eight neighbouring values of one
-  // token and stores 16 bytes.
-  float* ep = reinterpret_cast<float*>(smem) + wave * (kEpWave / 4);
-  constexpr int PL = Epi::kPlanes;
-  const int64_t mw = m0 + wm * 32 * MB;
+  if (split) {
+    f32x4_t* to = reinterpret_cast<f32x4_t*>(g.part) + ((int64_t)item * W + wave) * (NB * MB * 4 * 64) + lane;
 #pragma unroll
-  for (int ib = 0; ib < NB; ib += PL)
+    for (int i = 0; i < NB; ++i)
 #pragma unroll
-    for (int j = 0; j < MB; ++j) {
-#pragma unroll
-      for (int p = 0; p < PL; ++p)
+      for (int j = 0; j < MB; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           f32x4_t v;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = acc[ib + p][j][4 * q + e];
-          *reinterpret_cast<f32x4_t*>(ep + (32 * p + (lane & 31)) * kEpPitch + 8 * q + 4 * (lane >> 5)) = v;
+          for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e];
+          to[((i * MB + j) * 4 + q) * 64] = v;
         }
-      __builtin_amdgcn_wave_barrier();
-      const int nb = (n0 + wn * 32 * NB + 32 * ib) / PL;   // first output column of the block
-#pragma unroll 1
-      for (int t = 0; t < 2; ++t) {
-        const int tok = 16 * t + (lane >> 2), c = 8 * (lane & 3);
-        if (mw + 32 * j + tok < g.m) {
-          float v[PL][8];
+    return;
+  }
+  float* ep = reinterpret_cast<float*>(smem) + wave * (kEpWave / 4);
+  constexpr int PL = Epi::kPlanes;
 #pragma unroll
-          for (int p = 0; p < PL; ++p) {
-            const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(ep + (32 * p + tok) * kEpPitch + c);
-            const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(ep + (32 * p + tok) * kEpPitch + c + 4);
+  for (int ib = 0; ib < NB; ib += PL)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              v[p][e] = lo[e];
-              v[p][4 + e] = hi[e];
-            }
-          }
-          epi.template finish<8>(v, mw + 32 * j + tok, nb + c);
-        }
-      }
-      __builtin_amdgcn_wave_barrier();
+    for (int j = 0; j < MB; ++j) {
+      f32x16_t x[PL];
+#pragma unroll
+      for (int p = 0; p < PL; ++p) x[p] = acc[ib + p][j];
+      finish_block(epi, ep, x, m0 + wm * 32 * MB + 32 * j, g.m, (n0 + wn * 32 * NB + 32 * ib) / PL);
     }
+}
+
+// The split tiles: their slices' sums in order, and the epilogue, 32 tokens x 32
+// values (x kPlanes) per wave.
+template <int MB, int NB, int WM, int WN, typename Epi>
+__global__ __launch_bounds__(256) void gemm16_join_kernel(Gemm16Args g, Epi epi) {
+  constexpr int PL = Epi::kPlanes, W = WM * WN, BLOCKS = NB * MB / PL;   // blocks of a wave's accumulators
+  __shared__ __attribute__((aligned(16))) float smem[4 * 32 * kEpPitch * PL];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n_split = g.tiles_m * g.tiles_n - g.whole;
+  const int64_t id = (int64_t)blockIdx.x * 4 + wave;
+  const int b = (int)(id % BLOCKS), w = (int)(id / BLOCKS % W), tile = (int)(id / (BLOCKS * W));
+  if (tile >= n_split) return;
+  const int ib = b / MB * PL, j = b % MB;
+  f32x16_t x[PL];
+#pragma unroll
+  for (int p = 0; p < PL; ++p)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[p][e] = 0.0f;
+#pragma unroll 2
+  for (int s = 0; s < g.slices; ++s) {
+    const f32x4_t* from = reinterpret_cast<const f32x4_t*>(g.part) + (((int64_t)s * n_split + tile) * W + w) * (NB * MB * 4 * 64) + lane;
+#pragma unroll
+    for (int p = 0; p < PL; ++p)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x4_t v = from[(((ib + p) * MB + j) * 4 + q) * 64];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[p][4 * q + e] += v[e];
+      }
+  }
+  int im, in;
+  tile_of(g.whole + tile, g.tiles_m, g.tiles_n, im, in);
+  finish_block(epi, smem + wave * (32 * kEpPitch * PL), x, (int64_t)im * (32 * MB * WM) + (w / WN) * 32 * MB + 32 * j, g.m,
+               (in * (32 * NB * WN) + (w % WN) * 32 * NB + 32 * ib) / PL);
 }
 
 }  // namespace gptq

@@ -922,16 +922,20 @@ static int chunk_of(int64_t groups, int max_kv) {
 }
 
 // Many rows: the keys are split only where there are too few row tiles for the
-// 512 workgroups that the chip holds.
+// 256 workgroups that the chip holds.  Measured for 256 and 512 workgroups:
+// 192 rows of 8 sequences of 4096 positions 65, 76 us; of one of 32768 54, 66 us.
 static int tile_chunk_of(int64_t groups, int max_kv) {
   const int all = (max_kv + 63) / 64 * 64;
   if (groups >= 256) return all;
-  const int64_t want = ((int64_t)max_kv * groups / 512 + 63) / 64 * 64;
+  const int64_t want = ((int64_t)max_kv * groups / 256 + 63) / 64 * 64;
   return (int)std::min<int64_t>(all, std::max<int64_t>(want, 512));
 }
 
-// rows of a sequence and kv head from which the unpacked tiles pay
-constexpr int kTileRows = 33;
+// Rows of a sequence and kv head from which the unpacked tiles pay.  Measured,
+// 48 and 64 rows, 16 at a time against in tiles: 8 sequences of 4096 positions
+// 33 against 40, 41 against 41 us; 64 of 2048 116 against 114, 152 against 114;
+// one of 32768 27 against 37, 33 against 38.
+constexpr int kTileRows = 49;
 
 struct AttnPlan {
   int per;                   // rows per workgroup: 16, or the unpacked tiles' 192

@@ -4,9 +4,9 @@
 // practice page m.lqnn.cn/news/117696, section 4.3: at inference the 4-bit
 // weights are dequantized to a 16-bit type and then multiplied.
 //
-//  few tokens     w4_skinny_kernel (m < kMidMin), w4_mid_kernel (to kSkinnyMax):
-//                 packed words go straight into matrix-instruction operands;
-//                 bound by reading the codes
+//  few tokens     w4_skinny_kernel, w4_mid_kernel (to kMidMax): packed words go
+//                 straight into matrix-instruction operands; bound by reading
+//                 the codes
 //  more           w4_dense_kernel writes the 16-bit weight to the workspace
 //                 once, then gemm16_kernel; bound by the matrix pipe
 //  backward       dG, dU elementwise, the 16-bit weights transposed to the
@@ -208,15 +208,16 @@ __global__ __launch_bounds__(64 * NW) void w4_skinny_kernel(const uint16_t* __re
 }
 
 // ---------------------------------------------------------------- some tokens
-// 17 to 64 tokens: the activations no longer are a small part of what a CU
-// reads, so eight waves of 16 weight rows share them.  A workgroup takes 128
-// rows (64 of gate and 64 of up) against all tokens over a slice of k; stages
-// of 256 k of the activations are copied HBM -> LDS (buffer_load ... lds, 16
-// bytes a lane, three slots, two stages ahead), the codes go to registers two
-// stages ahead, the slice's scales and zero points to LDS first.  Slices'
-// sums go to the workspace and w4_join_kernel adds them in order and finishes
-// them.  Measured, 24 tokens, 28672 -> 8192: 51 us (and 5 to join) against 129 with
-// every 16 rows reading the activations themselves.
+// Up to 128 tokens (blocks of 64): the activations no longer are a small part
+// of what a CU reads, so eight waves of 16 weight rows share them.  A workgroup
+// takes 128 rows (64 of gate and 64 of up) against its block's tokens over a
+// slice of k; stages of 256 k of the activations are copied HBM -> LDS
+// (buffer_load ... lds, 16 bytes a lane, three slots, two stages ahead), the
+// codes go to registers two stages ahead, the slice's scales and zero points to
+// LDS first.  Slices' sums go to the workspace and w4_join_kernel adds them in
+// order and finishes them.  Bound by the codes from HBM and by what dequantizing
+// them costs; measured, 24 tokens, 28672 -> 8192: 48 us (and 5 to join) against
+// 129 us with every 16 rows reading the activations themselves.
 // A token's row in LDS is 512 bytes; the 16-byte chunk c of its half y sits at
 // c ^ (token % 16): 16 tokens' reads of one chunk hit 16 columns of the banks.
 constexpr int kMidK = 256;          // k per stage
@@ -224,7 +225,7 @@ constexpr int kMidSlots = 3;
 constexpr int kMidWaves = 8;
 
 template <typename T, int NT, int NMAT>
-__global__ __launch_bounds__(64 * kMidWaves, NT == 2 ? 4 : 2) void w4_mid_kernel(const uint16_t* __restrict__ X, int64_t ldx, int m, W4Dev wa,
+__global__ __launch_bounds__(64 * kMidWaves, NT <= 2 ? 4 : 2) void w4_mid_kernel(const uint16_t* __restrict__ X, int64_t ldx, int m, W4Dev wa,
                                                                    W4Dev wb, int d_out, int d_in, int G, int ng, int slice_k,
                                                                    int slice_groups, float* __restrict__ part) {
   typedef typename T16<T>::v8 v8;
@@ -241,6 +242,8 @@ __global__ __launch_bounds__(64 * kMidWaves, NT == 2 ? 4 : 2) void w4_mid_kernel
   const W4Dev& w = mat ? wb : wa;
   const int nw = d_in >> 3;
   const float invG = 1.0f / (float)G;
+  X += (int64_t)blockIdx.z * (16 * NT) * ldx;
+  const int t0 = blockIdx.z * 16 * NT, tokens = m - t0;
   const int k_lo = blockIdx.y * slice_k, k_hi = min(k_lo + slice_k, d_in);
   const int stages = (k_hi - k_lo + kMidK - 1) / kMidK;
   const int g_lo = group_of(k_lo, G, invG);
@@ -253,7 +256,7 @@ __global__ __launch_bounds__(64 * kMidWaves, NT == 2 ? 4 : 2) void w4_mid_kernel
     const int tl = 2 * wave + (lane >> 5);
     x_k = 128 * ((lane >> 4) & 1) + 8 * ((lane & 15) ^ (tl & 15));
 #pragma unroll
-    for (int i = 0; i < NT; ++i) x_off[i] = (int)(min(tl + 16 * i, m - 1) * ldx + x_k) * 2;
+    for (int i = 0; i < NT; ++i) x_off[i] = (int)(min(tl + 16 * i, tokens - 1) * ldx + x_k) * 2;
   }
   auto copy_x = [&](int st) {
     const int k0 = k_lo + st * kMidK;
@@ -343,8 +346,8 @@ __global__ __launch_bounds__(64 * kMidWaves, NT == 2 ? 4 : 2) void w4_mid_kernel
   if (r0 + 4 * lg < dp) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-      if (16 * n + lr < m)
-        *reinterpret_cast<f32x4_t*>(part + ((size_t)(blockIdx.y * NMAT + mat) * m + 16 * n + lr) * dp + r0 + 4 * lg) = acc[n];
+      if (16 * n + lr < tokens)
+        *reinterpret_cast<f32x4_t*>(part + ((size_t)(blockIdx.y * NMAT + mat) * m + t0 + 16 * n + lr) * dp + r0 + 4 * lg) = acc[n];
   }
 }
 
@@ -503,18 +506,17 @@ __global__ __launch_bounds__(256) void gated_slopes_kernel(const uint16_t* dM, c
 }
 
 // ---------------------------------------------------------------- host side
-// tokens up to which the packed words are multiplied directly
-constexpr int kSkinnyMax = 64;
+// Tokens up to which the packed words are multiplied directly, by the 16-row
+// waves and by w4_mid_kernel.  Measured, w4_mid_kernel and through memory, 65 and
+// 128 tokens: 4096 -> 4096 18 and 25, 19 and 26 us; 5120 -> 13824 62 and 61, 68 and
+// 64 us; 28672 -> 8192 141 and 245, 147 and 252 us; 192 tokens in three blocks 29 and
+// 31, 100 and 79, 217 and 261 us.
+constexpr int kSkinnyMax = 64, kMidMax = 128;
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 static int pad_k(int d) { return (d + kGk - 1) / kGk * kGk; }
 static unsigned grid_rows(int64_t rows) { return (unsigned)std::min<int64_t>(rows, 32768); }
 
-// X has to be copied (and brought into processing order)
-static bool copies_x(const void* X, int64_t ldx, int64_t m, const gptq_w4_weight* w) {
-  if (w->perm || !aligned16(X) || (ldx % 8) != 0 || ldx * 2 > kMaxRowBytes) return true;
-  return m > kSkinnyMax && w->d_in % kGk != 0;
-}
 static size_t x_copy_bytes(int64_t m, int d_in) { return align_up((size_t)m * pad_k(d_in) * 2); }
 
 static int order_x(const void* X, int64_t ldx, int64_t m, const gptq_w4_weight* w, uint16_t* out, hipStream_t s) {
@@ -531,12 +533,18 @@ struct MidPlan {
   int slices, slice_k, slice_groups;
   size_t bytes;
 };
-constexpr int kMidMin = 17;                     // tokens from which it pays
+// Tokens x d_in x d_out from which it pays with at most 16 tokens, too: what
+// the 16-row workgroups read of the activations outweighs the second launch.
+// Measured, 16-row and this, 8 and 16 tokens: 4096 -> 4096 7 and 11, 7 and 12 us;
+// 5120 -> 13824 19 and 19, 26 and 20 us; 28672 -> 8192 50 and 39, 68 and 40 us.
+// Two matrices share the reading: 4096 -> 2 x 11008 21 and 26, 22 and 26 us; 8192
+// -> 2 x 28672 81 and 79, 90 and 80 us.
+constexpr double kMidWork = 6.0e8;
 constexpr size_t kMidGridBytes = 48 << 10;      // LDS for the scales and zero points
 static MidPlan mid_plan(int64_t m, const gptq_w4_weight* wa, const gptq_w4_weight* wb) {
   MidPlan p{0, 0, 0, 0};
   const int G = w4_group(wa);
-  if (m < kMidMin || m > kSkinnyMax || wa->d_in % 32 != 0 || G % 32 != 0) return p;
+  if (m > kMidMax || (m <= 16 && (double)m * wa->d_in * wa->d_out < (wb ? 3.0 : 1.0) * kMidWork) || wa->d_in % 32 != 0 || G % 32 != 0) return p;
   if (!aligned16(wa->packed) || (wb && !aligned16(wb->packed))) return p;
   const int64_t blocks = (wa->d_out + (wb ? 64 : 128) - 1) / (wb ? 64 : 128);
   // two workgroups a CU, four stages a slice at least, scales that fit LDS
@@ -544,11 +552,24 @@ static MidPlan mid_plan(int64_t m, const gptq_w4_weight* wa, const gptq_w4_weigh
   const int64_t groups = kMidGridBytes / (16 * kMidWaves * sizeof(float2)) - 2;
   k = std::max<int64_t>(k, 4 * kMidK);
   k = std::min<int64_t>(k, std::max<int64_t>((groups - 1) * G / kMidK * kMidK, kMidK));
-  p.slice_k = (int)std::min<int64_t>(k, (wa->d_in + kMidK - 1) / kMidK * kMidK);
+  // as many slices of even length
+  const int64_t stages = (wa->d_in + kMidK - 1) / kMidK, n = (wa->d_in + k - 1) / k;
+  p.slice_k = (int)((stages + n - 1) / n * kMidK);
   p.slices = (wa->d_in + p.slice_k - 1) / p.slice_k;
   p.slice_groups = std::min(p.slice_k / G + 2, wa->n_groups);
   p.bytes = align_up((size_t)p.slices * (wb ? 2 : 1) * m * ((wa->d_out + 3) & ~3) * sizeof(float));
   return p;
+}
+
+// the 16-bit weight goes through memory
+static bool is_dense(int64_t m, const gptq_w4_weight* wa, const gptq_w4_weight* wb) {
+  return m > kSkinnyMax && !mid_plan(m, wa, wb).slices;
+}
+
+// X has to be copied (and brought into processing order)
+static bool copies_x(const void* X, int64_t ldx, int64_t m, const gptq_w4_weight* w, const gptq_w4_weight* wb) {
+  if (w->perm || !aligned16(X) || (ldx % 8) != 0 || ldx * 2 > kMaxRowBytes) return true;
+  return is_dense(m, w, wb) && w->d_in % kGk != 0;
 }
 
 template <typename T, typename Epi>
@@ -556,13 +577,14 @@ static int launch_mid(const uint16_t* X, int64_t ldx, int64_t m, const gptq_w4_w
                       const MidPlan& p, const Epi& epi, float* part, hipStream_t s) {
   constexpr int NMAT = Epi::kPlanes;
   const int d_out = wa->d_out, rb = 128 / NMAT;
-  const dim3 grid((unsigned)((d_out + rb - 1) / rb), (unsigned)p.slices);
   auto go = [&]<int NT>() {
+    const dim3 grid((unsigned)((d_out + rb - 1) / rb), (unsigned)p.slices, (unsigned)((m + 16 * NT - 1) / (16 * NT)));
     const size_t lds = (size_t)kMidSlots * NT * 16 * 2 * kMidK + (size_t)kMidWaves * 16 * (p.slice_groups + 1) * sizeof(float2);
     w4_mid_kernel<T, NT, NMAT><<<grid, 64 * kMidWaves, lds, s>>>(X, ldx, (int)m, dev_of(wa), dev_of(wb), d_out, wa->d_in,
                                                                  w4_group(wa), wa->n_groups, p.slice_k, p.slice_groups, part);
   };
-  if (m <= 32) go.template operator()<2>();
+  if (m <= 16) go.template operator()<1>();
+  else if (m <= 32) go.template operator()<2>();
   else go.template operator()<4>();
   GPTQ_LAUNCH_CHECK();
   w4_join_kernel<Epi><<<dim3((unsigned)((d_out + 1023) / 1024), (unsigned)m), 256, 0, s>>>(part, p.slices, (int)m, d_out, epi);
@@ -595,24 +617,68 @@ static int launch_skinny(const uint16_t* X, int64_t ldx, int64_t m, const gptq_w
   return GPTQ_OK;
 }
 
-template <typename T, typename Epi>
-static int launch_gemm16(Gemm16Args g, const Epi& epi, hipStream_t s) {
-  auto tiles = [&](int64_t e) { return ((g.m + e - 1) / e) * ((g.n + e - 1) / e); };
-  // By rounds of the chip: 256 tiles of 256 x 256 take 1, 512 of 128 x 128 (two a
-  // CU) half the work at 3/4 of the rate, 2/3.  (256 x 192 tiles, one wave a
-  // SIMD, gained nothing where they fill the last round better: 577 x 5120 x
-  // 13824 149 us, as with 256 x 256.)
-  const bool big = 3 * ((tiles(256) + 255) / 256) <= 2 * ((tiles(128) + 511) / 512);
-  const int e = big ? 256 : 128;
-  const int64_t t = tiles(e);
-  if (t > INT_MAX / 16) return GPTQ_ERR_INVALID_ARG;
-  g.tiles_m = (int)((g.m + e - 1) / e);
-  g.tiles_n = (g.n + e - 1) / e;
-  const unsigned grid = (unsigned)(8 * ((t + 7) / 8));
-  if (big) gemm16_kernel<T, 4, 2, 2, 4, Epi><<<grid, 512, 0, s>>>(g, epi);
-  else gemm16_kernel<T, 2, 2, 2, 2, Epi><<<grid, 256, 0, s>>>(g, epi);
+// Tiles of the large products.  256 workgroups of 256 x 256 tiles fill the chip,
+// or 512 of 128 x 128 (two a CU).  What is left after the full rounds leaves part
+// of it idle, so those tiles' k is split where that pays.  The model: a round of
+// large tiles takes 28 ns per k (1.18 PFLOP/s), of small ones 2/3 of that, and
+// slices' sums pass memory at a copy's rate.  Measured whole and split: 8192 x
+// 13824 x 5120 1050 and 982 us; 577 x 5120 x 13824 146 and 126 us; gated 4096 ->
+// 2 x 11008, 1024 tokens 239 and 216 us, 4096 tokens 700 and 692 us.
+struct GemmPlan {
+  int edge, whole, slices, slice_pairs;
+  size_t bytes;
+};
+constexpr int kMinSlicePairs = 4;
+static GemmPlan gemm_plan(int64_t m, int64_t n, int pairs) {
+  GemmPlan best{0, 0, 0, 0, 0};
+  double best_us = 0.0;
+  for (const int e : {256, 128}) {
+    const int64_t tiles = ((m + e - 1) / e) * ((n + e - 1) / e), slots = e == 256 ? 256 : 512;
+    const double round_us = pairs * kGk * (e == 256 ? 0.028 : 0.019);
+    const int64_t rest = tiles % slots;
+    for (int s = 1; s <= 8; ++s) {
+      if (s > 1 && (rest * s > slots || pairs < s * kMinSlicePairs)) break;
+      const int per = (pairs + s - 1) / s;
+      if (s > 1 && (pairs + per - 1) / per != s) continue;
+      const size_t bytes = s > 1 ? (size_t)rest * s * e * e * sizeof(float) : 0;
+      const double us = round_us * (double)(tiles / slots) + (rest ? round_us / s : 0.0) + (s > 1 ? 5.0 + 2.0 * (double)bytes / 4.9e6 : 0.0);
+      if (!best.edge || us < best_us) {
+        best = GemmPlan{e, (int)std::min<int64_t>(s > 1 ? tiles - rest : tiles, INT_MAX), s, per, align_up(bytes)};
+        best_us = us;
+      }
+      if (!rest) break;
+    }
+  }
+  return best;
+}
+
+template <typename T, int MB, int NB, int WM, int WN, typename Epi>
+static int launch_tiles(const Gemm16Args& g, const Epi& epi, hipStream_t s) {
+  const int64_t rest = (int64_t)g.tiles_m * g.tiles_n - g.whole;
+  const int64_t grid = ((int64_t)g.whole + 7) / 8 * 8 + (rest * g.slices + 7) / 8 * 8;
+  gemm16_kernel<T, MB, NB, WM, WN, Epi><<<(unsigned)grid, 64 * WM * WN, 0, s>>>(g, epi);
   GPTQ_LAUNCH_CHECK();
+  if (rest) {
+    const int64_t waves = rest * WM * WN * (NB * MB / Epi::kPlanes);
+    gemm16_join_kernel<MB, NB, WM, WN, Epi><<<(unsigned)((waves + 3) / 4), 256, 0, s>>>(g, epi);
+    GPTQ_LAUNCH_CHECK();
+  }
   return GPTQ_OK;
+}
+
+// part: gemm_plan(g.m, g.n, g.n_pairs).bytes
+template <typename T, typename Epi>
+static int launch_gemm16(Gemm16Args g, const Epi& epi, void* part, hipStream_t s) {
+  const GemmPlan p = gemm_plan(g.m, g.n, g.n_pairs);
+  const int64_t tm = (g.m + p.edge - 1) / p.edge, tn = (g.n + p.edge - 1) / p.edge;
+  if (tm * tn > INT_MAX / 16) return GPTQ_ERR_INVALID_ARG;
+  g.tiles_m = (int)tm;
+  g.tiles_n = (int)tn;
+  g.whole = p.whole;
+  g.slices = p.slices;
+  g.slice_pairs = p.slice_pairs;
+  g.part = static_cast<float*>(part);
+  return p.edge == 256 ? launch_tiles<T, 4, 2, 2, 4>(g, epi, s) : launch_tiles<T, 2, 2, 2, 2>(g, epi, s);
 }
 
 template <typename T>
@@ -624,13 +690,21 @@ static int launch_dense(const gptq_w4_weight* wa, const gptq_w4_weight* wb, uint
   return GPTQ_OK;
 }
 
+// rows of the 16-bit weight, both matrices' in blocks of 32
+static int weight_rows(const gptq_w4_weight* wa, const gptq_w4_weight* wb) {
+  return wb ? 2 * ((wa->d_out + 31) / 32 * 32) : wa->d_out;
+}
+static size_t dense_bytes(const gptq_w4_weight* wa, const gptq_w4_weight* wb) {
+  return align_up((size_t)weight_rows(wa, wb) * pad_k(wa->d_in) * 2);
+}
+
 // one or both products of X with packed weights, and the epilogue
 template <typename T, typename Epi>
 static int forward(const void* X, int64_t ldx, int64_t m, const gptq_w4_weight* wa, const gptq_w4_weight* wb, const Epi& epi,
                    void* ws, hipStream_t s) {
   char* base = static_cast<char*>(ws);
   const uint16_t* x = static_cast<const uint16_t*>(X);
-  if (copies_x(X, ldx, m, wa)) {
+  if (copies_x(X, ldx, m, wa, wb)) {
     uint16_t* xc = reinterpret_cast<uint16_t*>(base);
     const int st = order_x(X, ldx, m, wa, xc, s);
     if (st != GPTQ_OK) return st;
@@ -645,18 +719,20 @@ static int forward(const void* X, int64_t ldx, int64_t m, const gptq_w4_weight* 
     uint16_t* w16 = reinterpret_cast<uint16_t*>(base + x_copy_bytes(m, wa->d_in));
     const int st = launch_dense<T>(wa, wb, w16, s);
     if (st != GPTQ_OK) return st;
-    const int Kp = pad_k(wa->d_in), n = wb ? 2 * ((wa->d_out + 31) / 32 * 32) : wa->d_out;
-    return launch_gemm16<T>(Gemm16Args{x, x, ldx, w16, Kp, m, n, Kp / kGk, Kp / kGk, 0, 0}, epi, s);
+    const int Kp = pad_k(wa->d_in), n = weight_rows(wa, wb);
+    return launch_gemm16<T>(Gemm16Args{x, x, ldx, w16, Kp, m, n, Kp / kGk, Kp / kGk}, epi,
+                            base + x_copy_bytes(m, wa->d_in) + dense_bytes(wa, wb), s);
   }
 }
 
 static size_t forward_bytes(int64_t m, const gptq_w4_weight* wa, const gptq_w4_weight* wb) {
-  const size_t rows = wb ? 2 * (size_t)((wa->d_out + 31) / 32 * 32) : (size_t)wa->d_out;
-  return x_copy_bytes(m, wa->d_in) + (m > kSkinnyMax ? align_up(rows * pad_k(wa->d_in) * 2) : mid_plan(m, wa, wb).bytes);
+  if (!is_dense(m, wa, wb)) return x_copy_bytes(m, wa->d_in) + mid_plan(m, wa, wb).bytes;
+  return x_copy_bytes(m, wa->d_in) + dense_bytes(wa, wb) +
+         gemm_plan(m, weight_rows(wa, wb), pad_k(wa->d_in) / kGk).bytes;
 }
 // what this call touches of it
 static size_t forward_needs(const void* X, int64_t ldx, int64_t m, const gptq_w4_weight* wa, const gptq_w4_weight* wb) {
-  if (m <= kSkinnyMax && !copies_x(X, ldx, m, wa) && !mid_plan(m, wa, wb).slices) return 0;
+  if (!is_dense(m, wa, wb) && !copies_x(X, ldx, m, wa, wb) && !mid_plan(m, wa, wb).slices) return 0;
   return forward_bytes(m, wa, wb);
 }
 
@@ -669,7 +745,7 @@ static bool is_gate(gptq_act a) { return a == GPTQ_ACT_SILU || a == GPTQ_ACT_GEL
 static bool elem_ok(const void* p, gptq_dtype t) { return (reinterpret_cast<uintptr_t>(p) & (t == GPTQ_F32 ? 3 : 1)) == 0; }
 
 struct BackLayout {
-  size_t off_g, off_u, total;
+  size_t off_g, off_u, off_part, total;
   int Fp;
 };
 static BackLayout back_layout(int64_t m, const gptq_w4_weight* w) {
@@ -677,7 +753,8 @@ static BackLayout back_layout(int64_t m, const gptq_w4_weight* w) {
   L.Fp = pad_k(w->d_out);
   L.off_g = align_up((size_t)w->d_in * 2 * L.Fp * 2);
   L.off_u = L.off_g + align_up((size_t)m * L.Fp * 2);
-  L.total = L.off_u + align_up((size_t)m * L.Fp * 2);
+  L.off_part = L.off_u + align_up((size_t)m * L.Fp * 2);
+  L.total = L.off_part + gemm_plan(m, w->d_in, 2 * L.Fp / kGk).bytes;
   return L;
 }
 
@@ -703,7 +780,7 @@ static int backward(const void* dM, const void* G, const void* U, int64_t m, con
   const uint16_t* a0 = direct ? static_cast<const uint16_t*>(dG) : cg;
   const uint16_t* a1 = direct ? static_cast<const uint16_t*>(dU) : cu;
   const LinearEpi<T> epi{nullptr, nullptr, dX, 0, d, d, GPTQ_ACT_NONE, T16<T>::kType, (d % 8) == 0 && aligned16(dX)};
-  return launch_gemm16<T>(Gemm16Args{a0, a1, L.Fp, wt, 2 * L.Fp, m, d, L.Fp / kGk, 2 * L.Fp / kGk, 0, 0}, epi, s);
+  return launch_gemm16<T>(Gemm16Args{a0, a1, L.Fp, wt, 2 * L.Fp, m, d, L.Fp / kGk, 2 * L.Fp / kGk}, epi, base + L.off_part, s);
 }
 
 }  // namespace gptq
