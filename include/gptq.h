@@ -353,10 +353,12 @@ typedef enum {
  *  bias [d_out] of x_dtype, or NULL.  R [m x d_out] of y_dtype, row pitch ldr,
  *  or NULL; R may be Y itself (with ldr = ldy).  Y [m x d_out] of y_dtype
  *  (F32, F16 or BF16), row pitch ldy; elements between rows stay as they are.
- *  ws  scratch of gptq_w4_linear_workspace_size(m, w) bytes (the 16-bit weight
- *      of large products, X in processing order; 0 bytes for small ones
- *      without perm: ws may be NULL then).  X rows that are not 16-byte
- *      aligned are copied to the workspace: the query's size covers that.
+ *      Y overlaps neither X nor bias.
+ *  ws  scratch of gptq_w4_linear_workspace_size(m, w) bytes, 256-byte aligned:
+ *      X's copy (for perm, or rows that are not 16-byte aligned), and from 17
+ *      tokens on (with large weights from a few on) partial sums or the 16-bit
+ *      weight.  A call that needs none of these takes ws NULL.  Calls that may
+ *      run at the same time need workspaces of their own, as captured graphs do.
  *  m == 0 is a no-op.  INVALID_ARG: null pointers, bad sizes, types, pitches
  *  or group sizes. */
 size_t gptq_w4_linear_workspace_size(int64_t m, const gptq_w4_weight* w);
