@@ -353,7 +353,7 @@ typedef enum {
  *  bias [d_out] of x_dtype, or NULL.  R [m x d_out] of y_dtype, row pitch ldr,
  *  or NULL; R may be Y itself (with ldr = ldy).  Y [m x d_out] of y_dtype
  *  (F32, F16 or BF16), row pitch ldy; elements between rows stay as they are.
- *      Y overlaps neither X nor bias.
+ *  Y may overlap neither X nor bias.
  *  ws  scratch of gptq_w4_linear_workspace_size(m, w) bytes, 256-byte aligned:
  *      X's copy (for perm, or rows that are not 16-byte aligned), and from 17
  *      tokens on (with large weights from a few on) partial sums or the 16-bit
