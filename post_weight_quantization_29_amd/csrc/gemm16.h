@@ -198,6 +198,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm16_kernel(Gemm16Args g, E
   const uint32_t rdA = lds + wm * (32 * MB * kRow) + sw, rdB = lds + TM * kRow + wn * (32 * NB * kRow) + sw;
   auto rd = [&](uint32_t at) { return *(LDS_AS const v8*)(uintptr_t)at; };
 
+  // Of the two workgroups that share a CU (workgroups 256 apart, as they are
+  // dealt) one goes first at every pipe: the other's waits fall into its
+  // products.  Measured, 577 x 5120 x 13824: 166 us the whole call without, 160.
+  if constexpr (W == 4) {
+    if ((blockIdx.x >> 8) & 1) __builtin_amdgcn_s_setprio(1);
+  }
   f32x16_t acc[NB][MB];
 #pragma unroll
   for (int i = 0; i < NB; ++i)
