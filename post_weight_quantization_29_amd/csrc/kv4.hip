@@ -651,8 +651,11 @@ __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kern
         column.template operator()<3>();
       }
       if (lane < 16) {
+        // bf16: a row with a step or minimum that is no number reaches those that see
+        // it through its step alone, as 0 times such an operand would reach all
+        const bool number = kScaled || (fabsf(grid_step(gg)) < INFINITY && fabsf(grid_lo(gg)) < INFINITY);
         const float vr = grid_step(gg), vs = kScaled || vr != 0.0f ? vr : kNoStep;
-        grid(2) = vs;
+        grid(2) = number ? vs : NAN;
         if constexpr (kScaled) {
           grid(3) = fmaf(8.0f, vs, grid_lo(gg));
           float mx = vs;
@@ -662,7 +665,7 @@ __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kern
         } else {
           // three pieces each of lo / step - 16 and 1 / step: rows 0..5, this key's slot of its chunk
           const float inv = 1.0f / vs;
-          float x[2] = {grid_lo(gg) * inv - kCodeBase, inv};
+          float x[2] = {number ? grid_lo(gg) * inv - kCodeBase : 0.0f, number ? inv : 0.0f};
 #pragma unroll
           for (int y = 0; y < 2; ++y)
 #pragma unroll

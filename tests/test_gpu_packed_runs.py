@@ -386,3 +386,32 @@ def test_binding_refuses_tensors_that_do_not_fit(P):
     ):
         with pytest.raises(P.GPTQError):
             call()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("n_q", [1, 3, 60, 300])
+@pytest.mark.parametrize("what", ["v step", "v lo", "k step", "k lo"])
+def test_attention_a_row_that_is_no_number_reaches_only_those_that_see_it(P, dtype, n_q, what):
+    """A cached row whose step or minimum is NaN or infinite, in the middle of the new tokens: the tokens
+    before it are what they are without it, and it shows in itself and in those behind it.  Not to the bit:
+    rows that are computed together change their reference maximum together, so an infinite score of one
+    moves the others' roundings.  Both results are within the same bound of the exact one, half a step of p's
+    type on terms of at most 15 steps and half a step of the output, so they differ by twice that at most
+    (fp32's part, below 1e-4 here, beside it)."""
+    n_pages, table, start, kvl = plan([n_q, n_q], [n_q + 37, n_q], 16, 1)
+    c = random_cache(P, n_pages, 1, 16, 64, table, 2)
+    Q = acts(2 * n_q * 2, 64, dtype, 5).view(2 * n_q, 2, 64)
+    a, b = torch.empty_like(Q), torch.empty_like(Q)
+    P.gptq_kv4_attention(Q, c, start, kvl, n_q, n_q + 37, a)
+    grid = c.v_grid if what[0] == "v" else c.k_grid
+    for value in (float("nan"), float("inf")):
+        at = n_q // 2
+        p = 37 + at
+        grid[int(table[0, p // 16]), 0, p % 16, 0 if "step" in what else 1] = value
+        P.gptq_kv4_attention(Q, c, start, kvl, n_q, n_q + 37, b)
+        assert torch.equal(b[n_q:], a[n_q:])                       # another sequence shares nothing
+        x, y, eps = a[:at].double(), b[:at].double(), R.EPS[dtype]
+        assert torch.isfinite(y).all()
+        assert bool(((x - y).abs() <= 2 * eps * (15 * 0.4 + x.abs() * (1 + eps)) + 1e-4).all())
+        if what[0] == "v" or value != value:
+            assert not torch.isfinite(b[at:n_q]).any()
