@@ -372,7 +372,8 @@ int gptq_w4_linear(const void* X, gptq_dtype x_dtype, int64_t m, int64_t ldx, co
  *  same perm pointer (they share one Hessian, so one order).
  *  X [m x d_in], row pitch ldx.  M [m x d_out] of x_dtype, contiguous.  G and
  *  U (both or neither; NULL when no backward pass follows): [m x d_out] of
- *  x_dtype, contiguous.  act: SILU, GELU or GELU_TANH. */
+ *  x_dtype, contiguous.  act: SILU, GELU or GELU_TANH.  M, G and U overlap
+ *  neither X nor each other. */
 size_t gptq_w4_gated_workspace_size(int64_t m, const gptq_w4_weight* gate, const gptq_w4_weight* up);
 int gptq_w4_gated(const void* X, gptq_dtype x_dtype, int64_t m, int64_t ldx, const gptq_w4_weight* gate,
                   const gptq_w4_weight* up, gptq_act act, void* G, void* U, void* M, void* ws,
@@ -448,7 +449,7 @@ int gptq_kv4_read(const gptq_kv4_cache* cache, void* K, void* V, gptq_dtype dtyp
  *   out = softmax_j(scale * q . k_j) v_j,
  * sums and statistics in fp32.  A row that sees nothing is 0.
  *  Q: token t, head h at Q + t*ldq + h*head_dim (f16/bf16, 16-byte aligned
- *  rows); out likewise with ldo.
+ *  rows); out likewise with ldo, not overlapping Q.
  *  max_q_len, max_kv_len: host bounds on n_q and kv_len; tokens past
  *  max_q_len of a sequence are left alone, positions past max_kv_len unseen.
  *  ws  scratch of gptq_kv4_attention_workspace_size(...) bytes (partial

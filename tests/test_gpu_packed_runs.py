@@ -63,6 +63,20 @@ def test_linear_ways(P, m, d_out, d_in, G, xt, yt, perm):
     assert torch.equal(again, Y[:m])
 
 
+@pytest.mark.parametrize("m,d_in,G,shift", [(3, 32776, 8, 0), (3, 32768, 32, 1), (70, 264, 8, 1), (600, 136, 8, 3), (5000, 64, 32, 0)])
+def test_linear_act_order(P, m, d_in, G, shift):
+    """Rows that fit LDS and longer ones, aligned or not, brought into processing order."""
+    L = R.layer(24, d_in, G, 7, "cuda", perm=True)
+    X = acts(m, d_in + 8, BF, 1)[:, shift:shift + d_in]
+    Y = torch.full((m, 24), float("nan"), dtype=F32, device="cuda")
+    w = weight(P, L)
+    ws, behind = poisoned(P.gptq_w4_linear_workspace_size(m, w))
+    P.gptq_w4_linear(X, w, Y, ws=ws)
+    ref, err = linear_ref(X, L, None, "none", None)
+    close(Y, ref, err, F32)
+    assert bool((behind == 0xFF).all())
+
+
 @pytest.mark.parametrize("m,d,f,G,dtype", [
     (16, 8192, 13760, 128, BF), (70, 512, 100, 64, HF), (128, 1056, 70, 32, BF), (300, 1024, 200, 128, HF),
     (1100, 640, 1500, 64, BF)])
