@@ -636,6 +636,8 @@ def gptq_kv4_read(cache: KV4Cache, K: Optional[torch.Tensor], V: Optional[torch.
 
 def gptq_kv4_attention_workspace_size(n_tokens: int, n_heads: int, cache: KV4Cache, max_q_len: int,
                                       max_kv_len: int) -> int:
+    if max_q_len >> 31 or max_kv_len >> 31:
+        raise ValueError(f"max_q_len and max_kv_len must fit 32 bits, got {max_q_len} and {max_kv_len}")
     return int(lib().gptq_kv4_attention_workspace_size(n_tokens, n_heads, cache.ref, max_q_len, max_kv_len))
 
 
@@ -652,6 +654,8 @@ def gptq_kv4_attention(Q: torch.Tensor, cache: KV4Cache, q_start: torch.Tensor, 
     if out.shape[0] != T:
         raise ValueError(f"out must have {T} tokens, got {out.shape[0]}")
     qt = _dtype16(Q, "Q")
+    if max_q_len >> 31 or max_kv_len >> 31:
+        raise ValueError(f"max_q_len and max_kv_len must fit 32 bits, got {max_q_len} and {max_kv_len}")
     need = 0 if ws is not None else gptq_kv4_attention_workspace_size(T, n_heads, cache, max_q_len, max_kv_len)
     ws = _scratch(need, ws, dev, stream)
     _run("gptq_kv4_attention", dev, stream, Q.data_ptr(), qt, T, n_heads, _pitch(Q), cache.ref, q_start.data_ptr(),

@@ -386,6 +386,8 @@ def test_binding_refuses_tensors_that_do_not_fit(P):
         lambda: P.gptq_kv4_read(c, rows[:, :, :32], None, start, kvl),
         lambda: P.gptq_kv4_attention(rows.float(), c, start, kvl, 1, 16, rows),
         lambda: P.gptq_kv4_attention(rows, c, start, kvl, 1, 16, rows[:1]),
+        lambda: P.gptq_kv4_attention(rows, c, start, kvl, 1, (1 << 32) + 16, torch.empty_like(rows)),
+        lambda: P.gptq_kv4_attention_workspace_size(2, 1, c, 1 << 31, 16),
         lambda: P.KV4Cache(c.k_codes, c.v_codes, c.k_grid, c.v_grid[:, :, :8].contiguous(), c.page_table),
     ):
         with pytest.raises(ValueError):
