@@ -37,6 +37,25 @@ namespace gptq {
 constexpr size_t kAlign = 256;
 inline size_t align_up(size_t x, size_t a = kAlign) { return (x + a - 1) / a * a; }
 
+// Copies HBM -> LDS without registers: lane l's 16 (4) bytes at the
+// descriptor's base + voff go to LDS at lds_dst + 16 l (4 l).  From asm, so that
+// the compiler does not model an outstanding LDS write (it would otherwise
+// drain every copy in flight before each LDS read); the kernels wait for the
+// copies themselves with counted s_waitcnt vmcnt.  The compiler then does not
+// see the hazards either: the copy wants one wait state behind the write of M0
+// and five behind a vector instruction's write of its descriptor (a
+// readfirstlane, or a spilled register's return), which s_mov and s_nop give
+// wherever the asm lands.
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+#define GPTQ_COPY_TO_LDS(width)                                                     \
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_" width " %1, %2, 0 offen lds" \
+               :                                                                    \
+               : "s"(__builtin_amdgcn_readfirstlane((int)lds_dst)), "v"(voff), "s"(rsrc) \
+               : "memory", "m0")
+GPTQ_DEV void copy16_lds(uint32_t lds_dst, const i32x4_t& rsrc, int voff) { GPTQ_COPY_TO_LDS("dwordx4"); }
+GPTQ_DEV void copy4_lds(uint32_t lds_dst, const i32x4_t& rsrc, int voff) { GPTQ_COPY_TO_LDS("dword"); }
+#undef GPTQ_COPY_TO_LDS
+
 // Output layout of v_mfma_f32_32x32x{2f32,16bf16,16f16} (checked on gfx950):
 // lane l, accumulator register r holds C[row][col] with
 //   row = 8*(r/4) + 4*(l/32) + (r%4),  col = l%32.

@@ -32,8 +32,6 @@
 
 namespace gptq {
 
-typedef int i32x4g_t __attribute__((ext_vector_type(4)));
-
 struct Gemm16Args {
   const uint16_t* A0;   // pairs of stages [0, k0_pairs)
   const uint16_t* A1;   // pairs after them (a second matrix of A's shape, its k from 0)
@@ -53,18 +51,6 @@ constexpr int kGk = 64;          // k per pair of stages
 constexpr int kSlots = 5;        // stage slots
 constexpr int kEpPitch = 36;     // floats per token row of the epilogue's LDS tile
 
-GPTQ_DEV void copy16_lds(uint32_t lds_dst, const i32x4g_t& rsrc, int voff) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :
-               : "s"(__builtin_amdgcn_readfirstlane((int)lds_dst)), "v"(voff), "s"(rsrc)
-               : "memory", "m0");
-}
-GPTQ_DEV void copy4_lds(uint32_t lds_dst, const i32x4g_t& rsrc, int voff) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-               :
-               : "s"(__builtin_amdgcn_readfirstlane((int)lds_dst)), "v"(voff), "s"(rsrc)
-               : "memory", "m0");
-}
 template <int N> GPTQ_DEV void wait_copies() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
 }
@@ -76,8 +62,8 @@ GPTQ_DEV void ring_barrier() { asm volatile("s_barrier" ::: "memory"); }
 constexpr int kPastEnd = 0x7ffffff0;
 constexpr int64_t kMaxRowBytes = 0x7fff0000 / 256;   // a tile's row offsets stay below kPastEnd
 
-GPTQ_DEV i32x4g_t tile_rsrc(uint64_t base, bool live) {
-  i32x4g_t r;
+GPTQ_DEV i32x4_t tile_rsrc(uint64_t base, bool live) {
+  i32x4_t r;
   r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)base);
   r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32));
   r[2] = live ? 0x7fffff00 : 0;
@@ -180,7 +166,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm16_kernel(Gemm16Args g, E
   // descriptors of a pair's first and second stages (an instruction offset
   // would move the LDS address as well)
   struct Pair {
-    i32x4g_t a[2], b[2];
+    i32x4_t a[2], b[2];
   };
   auto rsrc_of = [&](int p) {
     const bool live = p < np;

@@ -94,26 +94,6 @@ constexpr int kSlots16 = 5;        // LDS ring slots
 constexpr int kRow16 = kT16;       // LDS row pitch in elements (512 bytes)
 constexpr int kStage16 = kK16 * kRow16;
 
-typedef int i32x4_t __attribute__((ext_vector_type(4)));
-
-// buffer_load_dwordx4 ... lds: each lane's 16 bytes go to LDS at M0 + 16*lane.
-// Issued from asm so that the compiler does not model an outstanding LDS write
-// (it would otherwise drain every copy in flight before each LDS read); the
-// kernel waits for the copies itself with counted s_waitcnt vmcnt.  All
-// operands are wave-uniform except the per-lane offset.
-GPTQ_DEV void dma16(i32x4_t rsrc, const void* lds_dst, int voff) {
-  const uint32_t m0v = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(LDS_AS const void*)lds_dst);
-  i32x4_t r;
-  r[0] = __builtin_amdgcn_readfirstlane(rsrc[0]);
-  r[1] = __builtin_amdgcn_readfirstlane(rsrc[1]);
-  r[2] = __builtin_amdgcn_readfirstlane(rsrc[2]);
-  r[3] = __builtin_amdgcn_readfirstlane(rsrc[3]);
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :
-               : "s"(m0v), "v"(voff), "s"(r)
-               : "memory", "m0");
-}
-
 // workgroup barrier that also stops the compiler from moving memory accesses
 // across it, without the fence's drain of outstanding global loads
 GPTQ_DEV void lds_barrier() { asm volatile("s_barrier" ::: "memory"); }
@@ -460,10 +440,7 @@ __global__ __launch_bounds__(256, 1) void syrk16_kernel(const T* __restrict__ X,
     const int i = n % NI;
     const uint32_t dst = ((n < NI) ? ldsA : ldsB) + (uint32_t)slot * kSlotBytes + 4096u * i + 1024u * wave;
     const int voff = (n < NI) ? voffA[i] : voffB[i];
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :
-                 : "s"(__builtin_amdgcn_readfirstlane(dst)), "v"(voff), "s"(r)
-                 : "memory", "m0");
+    copy16_lds(dst, r, voff);
   };
 
 

@@ -575,17 +575,17 @@ __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kern
       return tile_rsrc(reinterpret_cast<uint64_t>(p), true);
     };
     if (is_k) {
-      const i32x4g_t rs = from(c.k_codes + (size_t)r * RW);
+      const i32x4_t rs = from(c.k_codes + (size_t)r * RW);
       if (HD == 128 || lane < 32) copy16_lds(slot, rs, code_off);
     } else {
       const uint32_t ro = (uint32_t)max(__builtin_amdgcn_readlane(rows_o, nn - row_base), 0);
-      const i32x4g_t r0 = from(c.v_codes + (size_t)(u & 1 ? ro : r) * RW), r1 = from(c.v_codes + (size_t)(u & 1 ? r : ro) * RW);
+      const i32x4_t r0 = from(c.v_codes + (size_t)(u & 1 ? ro : r) * RW), r1 = from(c.v_codes + (size_t)(u & 1 ? r : ro) * RW);
       if (lane < 2 * HD / 8) {
         copy16_lds(slot, r0, code_off);
         copy16_lds(slot + 512, r1, code_off);
       }
     }
-    const i32x4g_t rg = from((is_k ? c.k_grid : c.v_grid) + r);
+    const i32x4_t rg = from((is_k ? c.k_grid : c.v_grid) + r);
     if (lane < 16) copy4_lds(slot + 1024, rg, 4 * lane);
   };
   // tile n into an unpacked buffer; `later` tiles' copies are still in flight

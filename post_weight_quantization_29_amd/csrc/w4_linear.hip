@@ -260,7 +260,7 @@ __global__ __launch_bounds__(64 * kMidWaves, NT <= 2 ? 4 : 2) void w4_mid_kernel
   }
   auto copy_x = [&](int st) {
     const int k0 = k_lo + st * kMidK;
-    const i32x4g_t rs = tile_rsrc(xb + (uint64_t)k0 * 2, st < stages);
+    const i32x4_t rs = tile_rsrc(xb + (uint64_t)k0 * 2, st < stages);
     const bool in = k0 + x_k < k_hi;
 #pragma unroll
     for (int i = 0; i < NT; ++i)
