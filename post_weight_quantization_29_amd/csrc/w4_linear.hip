@@ -297,9 +297,15 @@ __global__ __launch_bounds__(64 * kMidWaves, NT <= 2 ? 4 : 2) void w4_mid_kernel
   wait_copies<0>();
   __syncthreads();
 
-  auto stage = [&]<int S>(int st) {
-    load_p(st + 2, p[(S + 2) % 3]);
-    copy_x(st + 2);
+  // RING: stages follow whose copies and codes are to be issued.  The last one
+  // or two stages issue nothing and wait for everything: the codes that they
+  // would load nobody uses, so the compiler drops such loads, and a wait that
+  // counts them lets copies pass that the next stage reads.
+  auto stage = [&]<int S, bool RING>(int st) {
+    if constexpr (RING) {
+      load_p(st + 2, p[(S + 2) % 3]);
+      copy_x(st + 2);
+    }
     const uint32_t xs = lds + S * kSlot + lr * (2 * kMidK);
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
@@ -327,18 +333,19 @@ __global__ __launch_bounds__(64 * kMidWaves, NT <= 2 ? 4 : 2) void w4_mid_kernel
       }
     }
     // the next stage's copies are older than this stage's NT copies and two code loads
-    wait_copies<NT + 2>();
+    if constexpr (RING) wait_copies<NT + 2>();
+    else wait_copies<0>();
     wait_lds_reads();
     ring_barrier();
   };
   int st = 0;
   for (; st + 3 <= stages; st += 3) {
-    stage.template operator()<0>(st);
-    stage.template operator()<1>(st + 1);
-    stage.template operator()<2>(st + 2);
+    stage.template operator()<0, true>(st);
+    stage.template operator()<1, true>(st + 1);
+    stage.template operator()<2, true>(st + 2);
   }
-  if (st < stages) stage.template operator()<0>(st++);
-  if (st < stages) stage.template operator()<1>(st++);
+  if (st < stages) stage.template operator()<0, false>(st++);
+  if (st < stages) stage.template operator()<1, false>(st++);
   wait_copies<0>();                     // no copy may land after the workgroup's end
 
   // lane l: rows r0 + 4 (l / 16) + 0..3 of token 16 n + l % 16

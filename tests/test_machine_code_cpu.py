@@ -78,3 +78,31 @@ def test_copies_to_lds_keep_the_required_wait_states(kernels):
                 states += int(before.split()[1], 0) + 1 if before.startswith("s_nop") else 1
     assert copies > 100
     assert not bad, f"{len(bad)} of {copies}: {bad[:4]}"
+
+
+def is_memory(op):
+    return re.match(r"(buffer|global|flat|scratch)_(load|store|atomic)", op) is not None
+
+
+def test_a_stage_of_few_tokens_is_there_before_its_barrier(kernels):
+    """The product of some tokens reads a stage of activations behind a barrier, which has to wait for the copies
+    of all stages before the one whose own are in flight: no more operations may be outstanding than were issued
+    since the barrier before it.  (A load whose value nobody uses is not issued, whatever the source counts.)"""
+    barriers, bad = 0, []
+    for name, code in kernels.items():
+        if "w4_mid_kernel" not in name:
+            continue
+        issued, waits, first = 0, [], True
+        for at, op in code:
+            if is_memory(op):
+                issued += 1
+            elif m := re.match(r"s_waitcnt .*vmcnt\((\d+)\)", op):
+                waits.append((int(m.group(1)), issued))
+            elif op == "s_barrier":
+                barriers += 1
+                # the first one follows a wait for everything
+                if not any(left <= (0 if first else new) for left, new in waits):
+                    bad.append((name, hex(at), waits))
+                issued, waits, first = 0, [], False
+    assert barriers >= 12 * 4
+    assert not bad, f"{len(bad)} of {barriers}: {bad[:4]}"
