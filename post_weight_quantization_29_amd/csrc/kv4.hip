@@ -434,25 +434,23 @@ __global__ __launch_bounds__(256, 3) void kv4_rows_kernel(AttnArgs a, KvDev c, K
 
 // Many rows (prompts): a workgroup takes 192 rows, 16 to each of twelve waves,
 // and walks the keys in tiles of 64.  A tile's codes are unpacked once for the
-// twelve: keys as 16 + code rows (waves 0..3), values transposed (waves
-// 4..7; channel rows, the keys of a 16-byte chunk in the order in which the
-// softmax's registers hold them), both in the activations' type, double
-// buffered; the packed words come three tiles ahead.  Products
+// twelve: keys as 16 + code rows in the activations' type (waves 0..3), values
+// transposed in bf16 (waves 4..7; channel rows, the keys of a 16-byte chunk in
+// the order in which the softmax's registers hold them), double buffered; the packed words come three tiles ahead.  Products
 // and register layouts are those of kv4_rows_kernel.
 //
-// w_j = p_j step_j is rounded to the activations' type once, and what the
+// w_j = p_j step_j is rounded to bf16 (fp16 has not the range: steps may differ
+// by 2^37, and a scale that fits the widest row seen would leave the others few
+// bits), for bf16 inputs in one piece, for fp16 in two (16 bits), and what the
 // rounding is multiplied with has to be of the values' own size, not 16 + code:
-//   bf16  out = sum_j w_j ((16 + code_j) + lo_j / step_j - 16) / sum_j w_j / step_j
-//         with the rounded w_j in all three sums: its error is p's own, as if
-//         p had been rounded.  The last two sums are six more rows of V^T
-//         (lo / step - 16 and 1 / step, each in three bf16 pieces, 24 bits), so
-//         they cost two products a tile and no vector instructions; a step of
-//         0 counts as 1e-20.
-//   fp16  out = (sum_j w_j (code_j - 8) + sum_j p_j (lo_j + 8 step_j)) / sum_j p_j,
-//         the codes made signed by one packed addition (1 / step need not fit
-//         fp16).  The running maximum carries the exponent of the largest step
-//         seen, so w_j stays in [0, 2^9] whatever the steps are; bf16 has
-//         fp32's range and needs no such thing.
+//   out = sum_j w_j ((16 + code_j) + lo_j / step_j - 16) / sum_j w_j / step_j
+// with the rounded w_j in all three sums: the error is p's own, as if p had been
+// rounded.  The last two sums are six more rows of V^T (lo / step - 16 and 1 /
+// step, each in three bf16 pieces, 24 bits), so they cost two products a tile
+// and piece and no vector instructions; a step of 0 counts as 1e-20.  Measured,
+// the prompts below: bf16 231 us, fp16 with its second piece 278 us (241 us with
+// one fp16 piece and the widest step's exponent, which cost the rows next to a
+// wide one up to seven bits).
 //
 // 16-byte LDS accesses serve 16 lanes a cycle: the swizzles give 16 consecutive
 // rows of one chunk 16 different 16-byte columns of the 64 banks.
@@ -470,13 +468,14 @@ constexpr uint32_t kRawSlots = 4, kRawBytes = 1024 + 128;
 template <typename T, int HD>
 __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kernel(AttnArgs a, KvDev c, KvBatch q) {
   typedef typename T16<T>::v8 v8;
+  typedef typename T16<__bf16>::v8 b8;
   constexpr int RW = HD / 8;           // packed words per row
   constexpr int KS = HD / 32;          // k-slices of the first product
   constexpr int NJ = HD / 16;          // 16-channel blocks of the second
-  constexpr bool kScaled = T16<T>::kType == GPTQ_F16;
+  constexpr int kPieces = T16<T>::kType == GPTQ_F16 ? 2 : 1;     // of a weight
   constexpr int TR = 16 * kTileWaves;
-  // LDS: [buffer][keys 64 x HD | values HD x 64 | six rows x 64 | ks, kl, vs, vl | vmax, there]
-  constexpr uint32_t kOffV = 64 * HD * 2, kOffX = 2 * kOffV, kOffG = kOffX + 8 * 128, kBuf = kOffG + 5 * 256;
+  // LDS: [buffer][keys 64 x HD | values HD x 64 | six rows x 64 | ks, kl, vs | there]
+  constexpr uint32_t kOffV = 64 * HD * 2, kOffX = 2 * kOffV, kOffG = kOffX + 8 * 128, kOffThere = kOffG + 3 * 256, kBuf = kOffThere + 256;
   __shared__ __attribute__((aligned(1024))) char smem[2 * kBuf + 8 * kRawSlots * kRawBytes];
   const uint32_t lds = (uint32_t)(uintptr_t)(LDS_AS const char*)smem;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -617,7 +616,6 @@ __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kern
     // instead of being kept in two dozen registers through the loop
     uint32_t sa = buf + s_at, xa = buf + x_at, ga = buf + g_at;
     asm volatile("" : "+v"(sa), "+v"(xa), "+v"(ga));
-    LDS_AS float* tail = (LDS_AS float*)(uintptr_t)(buf + kOffG + 4 * 256);
     auto grid = [&](int plane) -> LDS_AS float& { return *(LDS_AS float*)(uintptr_t)(ga + 256 * plane); };
     if (is_k) {
       if (busy) {
@@ -628,7 +626,7 @@ __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kern
         const float ks = grid_step(gg);
         grid(0) = ks * a.scale2;
         grid(1) = fmaf(-kCodeBase, ks, grid_lo(gg));
-        if (lane == 0) ((LDS_AS int*)tail)[4 + u] = g_there;
+        if (lane == 0) ((LDS_AS int*)(uintptr_t)(buf + kOffThere))[u] = g_there;
       }
     } else {
       if (busy) {
@@ -638,13 +636,7 @@ __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kern
         auto column = [&]<int K>() {
           uint32_t w[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            w[e] = code_pair<T, K>(z[e]);
-            if constexpr (kScaled) {
-              const f16x2w_t off = {(_Float16)-24.0f, (_Float16)-24.0f};
-              w[e] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2w_t, w[e]) + off);
-            }
-          }
+          for (int e = 0; e < 4; ++e) w[e] = code_pair<__bf16, K>(z[e]);
           put((sa ^ ((K >> 1) << 4)) + 128 * K, make_uint4(w[0], w[1], w[2], w[3]));
         };
         column.template operator()<0>();
@@ -653,31 +645,23 @@ __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kern
         column.template operator()<3>();
       }
       if (lane < 16) {
-        // bf16: a row with a step or minimum that is no number reaches those that see
-        // it through its step alone, as 0 times such an operand would reach all
-        const bool number = kScaled || (fabsf(grid_step(gg)) < INFINITY && fabsf(grid_lo(gg)) < INFINITY);
-        const float vr = grid_step(gg), vs = kScaled || vr != 0.0f ? vr : kNoStep;
+        // a row with a step or minimum that is no number reaches those that see it
+        // through its step alone, as 0 times such an operand would reach all
+        const bool number = fabsf(grid_step(gg)) < INFINITY && fabsf(grid_lo(gg)) < INFINITY;
+        const float vr = grid_step(gg), vs = vr != 0.0f ? vr : kNoStep;
         grid(2) = number ? vs : NAN;
-        if constexpr (kScaled) {
-          grid(3) = fmaf(8.0f, vs, grid_lo(gg));
-          float mx = vs;
+        // three pieces each of lo / step - 16 and 1 / step: rows 0..5, this key's slot of its chunk
+        const float inv = 1.0f / vs;
+        float x[2] = {number ? grid_lo(gg) * inv - kCodeBase : 0.0f, number ? inv : 0.0f};
 #pragma unroll
-          for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o, 16));
-          if (lane == 0) tail[u] = mx;
-        } else {
-          // three pieces each of lo / step - 16 and 1 / step: rows 0..5, this key's slot of its chunk
-          const float inv = 1.0f / vs;
-          float x[2] = {number ? grid_lo(gg) * inv - kCodeBase : 0.0f, number ? inv : 0.0f};
+        for (int y = 0; y < 2; ++y)
 #pragma unroll
-          for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int p = 0; p < 3; ++p) {
-              const int rr = 3 * y + p;
-              const uint16_t bits = bits16<T>(x[y]);
-              x[y] -= (float)__builtin_bit_cast(T, bits);
-              *(LDS_AS uint16_t*)(uintptr_t)((xa ^ (rr << 4)) + 128 * rr) = bits;
-            }
-        }
+          for (int p = 0; p < 3; ++p) {
+            const int rr = 3 * y + p;
+            const uint16_t bits = bits16<__bf16>(x[y]);
+            x[y] -= (float)__builtin_bit_cast(__bf16, bits);
+            *(LDS_AS uint16_t*)(uintptr_t)((xa ^ (rr << 4)) + 128 * rr) = bits;
+          }
       }
     }
   };
@@ -689,9 +673,8 @@ __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kern
   const uint32_t v_rd = kOffV + i * 128 + ((g ^ swz_v(i)) << 4);
   const uint32_t x_rd = kOffX + (i & 7) * 128 + ((g ^ (i & 7)) << 4);
 
-  f32x4_t o[NJ], ox = {0.0f, 0.0f, 0.0f, 0.0f};   // ox: the sums of V^T's extra rows (bf16)
-  float m = kNoMax, l = 0.0f, base = 0.0f;
-  float top = kNoMax, ex = -24.0f;     // largest score seen (m follows it); exponent of the largest step (fp16)
+  f32x4_t o[NJ], ox = {0.0f, 0.0f, 0.0f, 0.0f};   // ox: the sums of V^T's extra rows
+  float m = kNoMax;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) o[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
@@ -704,7 +687,7 @@ __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kern
   __syncthreads();
   uint32_t buf = lds, other = lds + kBuf;
   int n = n0;
-  auto there = [&](int w) { return ((const LDS_AS int*)(uintptr_t)(buf + kOffG + 4 * 256 + 16))[w]; };
+  auto there = [&](int w) { return ((const LDS_AS int*)(uintptr_t)(buf + kOffThere))[w]; };
   auto next_tile = [&]() {
     if (n + 1 < n1) store(n + 1, other);
     __syncthreads();
@@ -721,9 +704,10 @@ __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kern
   auto tiles = [&]<bool WHOLE>(auto&& more) {
     for (;;) {
       bool grow = false;
-      float mt = top;
+      float mt = m;
       while (n < n1 && more()) {
         auto rd = [&](uint32_t at) { return *(LDS_AS const v8*)(uintptr_t)at; };
+        auto rdv = [&](uint32_t at) { return *(LDS_AS const b8*)(uintptr_t)at; };
         uint32_t kr = buf + k_rd, vr = buf + v_rd, xr = buf + x_rd, gr = buf + kOffG + 16 * g;
         asm volatile("" : "+v"(kr), "+v"(vr), "+v"(xr), "+v"(gr));
         // plane's values of keys 16 kt + 4 g + 0..3
@@ -735,7 +719,7 @@ __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kern
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
           for (int kt = 0; kt < 4; ++kt) s[kt] = T16<T>::mfma16(rd((kr ^ (ks << 6)) + kt * (32 * HD)), qv[ks], s[kt]);
-        mt = top;
+        mt = m;
 #pragma unroll
         for (int kt = 0; kt < 4; ++kt) {
           const f32x4_t ks = rd4(0, kt), kl = rd4(1, kt);
@@ -749,43 +733,42 @@ __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kern
         }
         mt = fmaxf(mt, __shfl_xor(mt, 16));
         mt = fmaxf(mt, __shfl_xor(mt, 32));
-        top = mt;
-        if constexpr (kScaled) {
-          const LDS_AS float* vmax = (const LDS_AS float*)(uintptr_t)(buf + kOffG + 4 * 256);
-          const float vm = fmaxf(fmaxf(vmax[0], vmax[1]), fmaxf(vmax[2], vmax[3]));
-          if (vm > 0.0f) ex = fmaxf(ex, (float)(__builtin_amdgcn_frexp_expf(vm) - 1));
-          mt = mt > kNoMax ? mt + ex : mt;
-        }
         grow = __any(mt > m + kLazy);
         if (grow) break;
         copy_tile(n + kRawSlots - 1);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          uint32_t pk[4];
+          uint32_t pk[kPieces][4];
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             const int kt = 2 * t + y;
             const f32x4_t vs = rd4(2, kt);
-            float p[4], w[4];
+            float w[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              p[r] = __builtin_amdgcn_exp2f(s[kt][r] - m);
+              const float p = __builtin_amdgcn_exp2f(s[kt][r] - m);
               // a key that this row does not see may hold anything
-              w[r] = !WHOLE && s[kt][r] == -INFINITY ? 0.0f : p[r] * vs[r];
+              w[r] = !WHOLE && s[kt][r] == -INFINITY ? 0.0f : p * vs[r];
             }
-            if constexpr (kScaled) {
-              const f32x4_t vl = rd4(3, kt);
-              l += (p[0] + p[1]) + (p[2] + p[3]);
 #pragma unroll
-              for (int r = 0; r < 4; ++r) base = fmaf(p[r], !WHOLE && s[kt][r] == -INFINITY ? 0.0f : vl[r], base);
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t hi = pack2<__bf16>(w[2 * x], w[2 * x + 1]);
+              pk[0][2 * y + x] = hi;
+              if constexpr (kPieces == 2) pk[kPieces - 1][2 * y + x] = pack2<__bf16>(w[2 * x] - lo16f<__bf16>(hi), w[2 * x + 1] - hi16f<__bf16>(hi));
             }
-            pk[2 * y] = pack2<T>(w[0], w[1]);
-            pk[2 * y + 1] = pack2<T>(w[2], w[3]);
           }
-          const v8 pv = __builtin_bit_cast(v8, make_uint4(pk[0], pk[1], pk[2], pk[3]));
+          b8 pv[kPieces];
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) o[j] = T16<T>::mfma16(rd((vr ^ (((4 * t) ^ (j & 7)) << 4)) + 2048 * j), pv, o[j]);
-          if constexpr (!kScaled) ox = T16<T>::mfma16(rd(xr ^ (t << 6)), pv, ox);
+          for (int x = 0; x < kPieces; ++x) pv[x] = __builtin_bit_cast(b8, make_uint4(pk[x][0], pk[x][1], pk[x][2], pk[x][3]));
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            const b8 vv = rdv((vr ^ (((4 * t) ^ (j & 7)) << 4)) + 2048 * j);
+#pragma unroll
+            for (int x = 0; x < kPieces; ++x) o[j] = T16<__bf16>::mfma16(vv, pv[x], o[j]);
+          }
+          const b8 xv = rdv(xr ^ (t << 6));
+#pragma unroll
+          for (int x = 0; x < kPieces; ++x) ox = T16<__bf16>::mfma16(xv, pv[x], ox);
         }
         next_tile();
       }
@@ -794,9 +777,7 @@ __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kern
       m = m_new;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) o[j] *= al;
-      if constexpr (!kScaled) ox *= al;
-      l *= al;
-      base *= al;
+      ox *= al;
     }
   };
   // one after the other (the waves of a workgroup may be in different ones,
@@ -809,16 +790,9 @@ __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kern
     next_tile();
   }
   wait_copies<0>();                      // no copy may land after the workgroup's end
-  if constexpr (kScaled) {
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
-    base += __shfl_xor(base, 16);
-    base += __shfl_xor(base, 32);
-  } else {
-    // rows 0..3 of the extra block are the registers of g = 0, 4 and 5 the first two of g = 1
-    base = __shfl(ox[0] + (ox[1] + ox[2]), i);
-    l = __shfl(ox[3], i) + __shfl(ox[0] + ox[1], 16 + i);
-  }
+  // rows 0..3 of the extra block are the registers of g = 0, 4 and 5 the first two of g = 1
+  const float base = __shfl(ox[0] + (ox[1] + ox[2]), i);
+  const float l = __shfl(ox[3], i) + __shfl(ox[0] + ox[1], 16 + i);
   if (row >= rows) return;
   const int64_t tok = t0 + row / a.rep;
   const int hq = h * a.rep + row % a.rep;
