@@ -52,12 +52,12 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(KvDev c, KvBatch q, con
   if (t >= q.n_tokens) return;
   const void* src = blockIdx.y ? V : K;
   const int64_t ld = blockIdx.y ? ldv : ldk;
-  // the first rows are on their way while their place is looked up (three
+  const int b = seq_of_token(q.q_start, c.n_seqs, t);
+  if (b < 0) return;                            // not the batch's: its row is not read either
+  // the first rows are on their way while their place is looked up (two more
   // loads, each on the one before)
   float ahead[8];
   load8<DT>(src, t * ld + (int64_t)min(lane / L, c.n_kv - 1) * HD + 8 * (lane % L), vec, ahead);
-  const int b = seq_of_token(q.q_start, c.n_seqs, t);
-  if (b < 0) return;
   int64_t t0;
   int n_q;
   q.span(b, t0, n_q);

@@ -106,3 +106,18 @@ def test_a_stage_of_few_tokens_is_there_before_its_barrier(kernels):
                 issued, waits, first = 0, [], False
     assert barriers >= 12 * 4
     assert not bad, f"{len(bad)} of {barriers}: {bad[:4]}"
+
+
+def test_append_reads_no_row_before_it_knows_that_the_batch_has_it(kernels):
+    """Rows outside the batch are not read: what another stream does with them is its own affair.  A token's
+    sequence is found by counting the starts up to it (s_bcnt1 of a ballot); rows are read by wide loads (12 or 16 bytes a lane)."""
+    found = 0
+    for name, code in kernels.items():
+        if "kv4_append_kernel" not in name:
+            continue
+        ops = [op for _, op in code]
+        row = next(n for n, op in enumerate(ops) if re.match(r"(global|flat)_load_dwordx[34] ", op))
+        count = next(n for n, op in enumerate(ops) if op.startswith("s_bcnt1_i32_b64"))
+        assert count < row, name
+        found += 1
+    assert found == 6
