@@ -324,7 +324,8 @@ int gptq_swiglu(const float* G, const float* U, int64_t n, float* M, hipStream_t
  *             packed column k belongs to channel perm[k].
  * The weight is W[r][perm[k]] = round16(scales[r][k/G] * (code[r][k] - zeros[r][k/G])),
  * the product in fp32, rounded (ties to even) to the activations' type, as in
- * gptq_w4a16_gemm.  d_in is a multiple of 8, at most 2^20.  Sums are fp32.
+ * gptq_w4a16_gemm.  d_in is a multiple of 8, at most 2^20; d_out is at most
+ * 2^27 - 32 (the backward pass: 2^20).  Sums are fp32.
  * The struct itself is host memory and is read before the call returns. */
 typedef struct {
   const uint32_t* packed;

@@ -149,10 +149,11 @@ template <typename F> GPTQ_DEV void with_act(int act, F&& f) {
 
 // ---------------------------------------------------------------- host checks
 constexpr int kW4MaxCols = 1 << 20;      // group_of() and the tiles' 32-bit row offsets hold to here
+constexpr int kW4MaxRows = (1 << 27) - 32;   // so many rows' threads, 32 a row at most, can be launched (2^32 - 1)
 
 inline bool w4_ok(const gptq_w4_weight* w) {
   if (!w || !w->packed || !w->scales || !w->zeros) return false;
-  if (w->d_out <= 0 || w->d_in <= 0 || (w->d_in % 8) != 0 || w->d_in > kW4MaxCols) return false;
+  if (w->d_out <= 0 || w->d_in <= 0 || (w->d_in % 8) != 0 || w->d_in > kW4MaxCols || w->d_out > kW4MaxRows) return false;
   const int G = w->group_size == -1 ? w->d_in : w->group_size;
   if (G <= 0 || (G % 8) != 0) return false;
   if (w->n_groups != (w->d_in + (int64_t)G - 1) / G) return false;

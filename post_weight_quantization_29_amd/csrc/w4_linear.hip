@@ -117,7 +117,7 @@ __global__ __launch_bounds__(64 * NW) void w4_skinny_kernel(const uint16_t* __re
 
   if (wave < pairs) load(wave, cur);
   if constexpr (GRID == 2) {
-    const int n = 16 * ng, have = min(n, (d_out - r0) * ng);
+    const int have = min(16, d_out - r0) * ng;
 #pragma unroll
     for (int a = 0; a < NMAT; ++a) {
       const W4Dev& w = a ? wb : wa;

@@ -1,0 +1,20 @@
+"""Sizes past the ends of the ranges of the packed layer's operators and the
+4-bit cache: refused on the host as arguments, not by the launch; no GPU."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+
+pytest.importorskip("torch")
+from post_weight_quantization_29_amd import _lib as M  # noqa: E402
+from test_packed_ops_cpu import L, backward, gated, i64, linear, weight  # noqa: E402, F401
+
+
+@pytest.mark.parametrize("d_out", [(1 << 27) - 31, 1 << 27, (1 << 31) - 1])
+def test_more_rows_than_can_be_launched(L, d_out):  # noqa: F811
+    w = weight(d_out=d_out)
+    for call in (lambda: linear(L, w, ldy=1 << 31), lambda: gated(L, w, w), lambda: backward(L, w, w)):
+        assert call() == M.ERR_INVALID_ARG
+    assert L.gptq_w4_linear_workspace_size(i64(100), ctypes.byref(w)) == 0
+    assert L.gptq_w4_gated_workspace_size(i64(100), ctypes.byref(w), ctypes.byref(w)) == 0
