@@ -485,9 +485,11 @@ __global__ __launch_bounds__(64 * kTileWaves, kTileWaves / 4) void kv4_tile_kern
   // heads shift by one from length to length: workgroups go to the XCDs in
   // turn, and 32 CUs of one XCD on one head's keys at the same time wait for
   // the same few lines of its L2 (369 us instead of 250).
-  const int ch = blockIdx.x % a.n_chunks;
-  int id = blockIdx.x / a.n_chunks;
+  const uint32_t wg = blockIdx.y * gridDim.x + blockIdx.x;
+  const int ch = wg % a.n_chunks;
   const int heads = c.n_kv * c.n_seqs;
+  if (wg / a.n_chunks >= (uint32_t)heads * a.row_tiles) return;    // the last of the launch's rows is not full
+  int id = wg / a.n_chunks;
   const int rt = a.row_tiles - 1 - id / heads;
   id = (id + rt) % heads;
   const int h = id % c.n_kv, b = id / c.n_kv;
@@ -825,8 +827,9 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(AttnArgs a, KvDev c, KvBa
   __shared__ f32x4_t sv[NG][L];
   __shared__ float sl[NG], sm[4];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int64_t tok = blockIdx.x / a.n_heads;
-  const int head = blockIdx.x % a.n_heads;
+  const int64_t wg = (int64_t)blockIdx.y * gridDim.x + blockIdx.x, tok = wg / a.n_heads;
+  const int head = (int)(wg % a.n_heads);
+  if (tok >= q.n_tokens) return;
   const int b = seq_of_token(q.q_start, c.n_seqs, tok);
   if (b < 0) return;
   int64_t t0;
@@ -935,6 +938,15 @@ static int tile_chunk_of(int64_t groups, int max_kv) {
 // one of 32768 27 against 37, 33 against 38.
 constexpr int kTileRows = 49;
 
+// A launch has fewer than 2^32 threads along x: more workgroups than this go on
+// along y (one long prompt beside many short sequences has that many, most of them
+// without rows).
+constexpr int64_t kGridX = 1 << 22;
+static dim3 grid_of(int64_t n) {
+  const int64_t x = std::min(n, kGridX);
+  return dim3((unsigned)x, (unsigned)((n + x - 1) / x));
+}
+
 struct AttnPlan {
   int per;                   // rows per workgroup: 16, or the unpacked tiles' 192
   int chunk, n_chunks, row_tiles;
@@ -955,6 +967,7 @@ static bool attn_plan(int64_t n_tokens, int n_heads, const gptq_kv4_cache* c, in
   p.n_chunks = (max_kv + p.chunk - 1) / p.chunk;
   p.grid = groups * p.n_chunks;
   if (p.grid > INT_MAX || n_tokens * n_heads > INT_MAX) return false;
+  if (p.per == 16 && p.grid / c->n_seqs > UINT32_MAX / 256) return false;     // sequences go along y
   const size_t n = p.n_chunks > 1 ? (size_t)p.n_chunks * n_tokens * n_heads : 0;
   p.off_ml = align_up(n * c->head_dim * sizeof(float));
   p.total = p.off_ml + align_up(n * sizeof(float2));
@@ -964,8 +977,8 @@ static bool attn_plan(int64_t n_tokens, int n_heads, const gptq_kv4_cache* c, in
 template <typename T>
 static int attend(const AttnArgs& a, const KvDev& c, const KvBatch& q, const AttnPlan& p, int hd, hipStream_t s) {
   if (p.per > 16) {
-    if (hd == 128) kv4_tile_kernel<T, 128><<<(unsigned)p.grid, 64 * kTileWaves, 0, s>>>(a, c, q);
-    else kv4_tile_kernel<T, 64><<<(unsigned)p.grid, 64 * kTileWaves, 0, s>>>(a, c, q);
+    if (hd == 128) kv4_tile_kernel<T, 128><<<grid_of(p.grid), 64 * kTileWaves, 0, s>>>(a, c, q);
+    else kv4_tile_kernel<T, 64><<<grid_of(p.grid), 64 * kTileWaves, 0, s>>>(a, c, q);
   } else {
     const dim3 grid((unsigned)(p.grid / c.n_seqs), (unsigned)std::min(c.n_seqs, 32768), (unsigned)((c.n_seqs + 32767) / 32768));
     if (hd == 128) kv4_rows_kernel<T, 128><<<grid, 256, 0, s>>>(a, c, q);
@@ -973,7 +986,7 @@ static int attend(const AttnArgs& a, const KvDev& c, const KvBatch& q, const Att
   }
   GPTQ_LAUNCH_CHECK();
   if (p.n_chunks > 1) {
-    const unsigned grid = (unsigned)(q.n_tokens * a.n_heads);
+    const dim3 grid = grid_of(q.n_tokens * a.n_heads);
     if (hd == 128) kv4_join_kernel<T, 128><<<grid, 256, 0, s>>>(a, c, q);
     else kv4_join_kernel<T, 64><<<grid, 256, 0, s>>>(a, c, q);
     GPTQ_LAUNCH_CHECK();

@@ -33,3 +33,42 @@ def test_linear_of_the_most_rows(P, m, d_in, group):
     for k in range(8):
         want += ((words >> (4 * k)) & 15).sum(1).float()
     assert bool((Y == want).all())
+
+
+def constant_cache(P, n_kv, hd, table):
+    """A cache whose values are all 1 (and keys): attention over any of it is 1, exactly."""
+    c = P.KV4Cache.empty(8, n_kv, 16, hd, table)
+    for codes, grid in ((c.k_codes, c.k_grid), (c.v_codes, c.v_grid)):
+        codes.zero_()
+        grid[..., 0], grid[..., 1] = 0.25, 1.0
+    return c
+
+
+@pytest.mark.parametrize("max_q", [131072, 40000])
+def test_attention_of_one_prompt_beside_many_sequences(P, max_q):
+    """1024 sequences under the bound of the longest one: 44 million workgroups, most without a row."""
+    n = 1024
+    c = constant_cache(P, 8, 128, torch.zeros((n, 4), dtype=torch.int32, device="cuda"))
+    lens = [0] * n
+    lens[0], lens[3], lens[-1] = 300, 1, 2
+    start = [0]
+    for k in lens:
+        start.append(start[-1] + k)
+    T = start[-1]
+    kvl = i32([64 if k else 0 for k in lens])
+    Q = torch.randn((T + 1, 64, 128), device="cuda").to(BF)
+    out = torch.full_like(Q, 5.0)
+    P.gptq_kv4_attention(Q, c, i32(start), kvl, max_q, 64, out)
+    # of 300 tokens at positions -236 .. 63 the first 236 see nothing
+    assert bool((out[:236] == 0).all()) and bool((out[236:T] == 1).all()) and bool((out[T] == 5).all())
+
+
+def test_attention_of_many_tokens_in_pieces(P):
+    """More than 2^24 (token, head) pairs whose pieces are joined."""
+    T, H = (1 << 18) + 8, 64
+    c = constant_cache(P, 2, 64, torch.zeros((3, 64), dtype=torch.int32, device="cuda"))
+    Q = torch.randn((T, H, 64), device="cuda").to(BF)
+    out = torch.full_like(Q, 5.0)
+    # the batch's tokens are the tensor's last ones; the others are left alone
+    P.gptq_kv4_attention(Q, c, i32([T - 3, T - 2, T - 1, T]), i32([1000, 3, 700]), 1, 1024, out)
+    assert bool((out[T - 3:] == 1).all()) and bool((out[:T - 3] == 5).all())

@@ -8,7 +8,7 @@ import pytest
 
 pytest.importorskip("torch")
 from post_weight_quantization_29_amd import _lib as M  # noqa: E402
-from test_packed_ops_cpu import L, backward, gated, i64, linear, weight  # noqa: E402, F401
+from test_packed_ops_cpu import L, attention, backward, cache, gated, i32, i64, linear, weight  # noqa: E402, F401
 
 
 @pytest.mark.parametrize("d_out", [(1 << 27) - 31, 1 << 27, (1 << 31) - 1])
@@ -18,3 +18,10 @@ def test_more_rows_than_can_be_launched(L, d_out):  # noqa: F811
         assert call() == M.ERR_INVALID_ARG
     assert L.gptq_w4_linear_workspace_size(i64(100), ctypes.byref(w)) == 0
     assert L.gptq_w4_gated_workspace_size(i64(100), ctypes.byref(w), ctypes.byref(w)) == 0
+
+
+def test_more_pieces_of_a_sequence_than_can_be_launched(L):  # noqa: F811
+    c = cache(n_pages=1, n_kv=64, max_pages=(1 << 27) - 4097)
+    assert attention(L, c, heads=64, ldq=64 * 128, ldo=64 * 128, mq=1, mk=(1 << 31) - 1) == M.ERR_INVALID_ARG
+    assert L.gptq_kv4_attention_workspace_size(i64(5), i32(64), ctypes.byref(c), i32(1), i32((1 << 31) - 1)) == 0
+    assert L.gptq_kv4_attention_workspace_size(i64(5), i32(64), ctypes.byref(c), i32(1), i32(1 << 29)) > 0
