@@ -451,7 +451,8 @@ int gptq_kv4_read(const gptq_kv4_cache* cache, void* K, void* V, gptq_dtype dtyp
  * sums and statistics in fp32.  A row that sees nothing is 0.
  *  Q: token t, head h at Q + t*ldq + h*head_dim (f16/bf16, 16-byte aligned
  *  rows); out likewise with ldo, not overlapping Q.
- *  max_q_len, max_kv_len: host bounds on n_q and kv_len; tokens past
+ *  max_q_len, max_kv_len: host bounds on n_q and kv_len, at least 1 (0 too
+ *  where n_tokens is 0, which is a no-op in every call here); tokens past
  *  max_q_len of a sequence are left alone, positions past max_kv_len unseen.
  *  ws  scratch of gptq_kv4_attention_workspace_size(...) bytes (partial
  *      results of long sequences, joined in a fixed order). */

@@ -1039,6 +1039,10 @@ extern "C" int gptq_kv4_attention(const void* Q, gptq_dtype dtype, int64_t n_tok
                                   int32_t max_q_len, int32_t max_kv_len, float scale, void* out, int64_t ldo, void* ws,
                                   size_t ws_bytes, hipStream_t s) {
   AttnPlan p;
+  if (n_tokens == 0) {                    // no tokens may have bounds of 0
+    max_q_len += max_q_len == 0;
+    max_kv_len += max_kv_len == 0;
+  }
   if (!attn_plan(n_tokens, n_heads, cache, max_q_len, max_kv_len, p) || !q_start || !kv_len) return GPTQ_ERR_INVALID_ARG;
   if (dtype != GPTQ_F16 && dtype != GPTQ_BF16) return GPTQ_ERR_INVALID_ARG;
   if (!(scale == scale) || std::isinf(scale)) return GPTQ_ERR_INVALID_ARG;

@@ -25,3 +25,12 @@ def test_more_pieces_of_a_sequence_than_can_be_launched(L):  # noqa: F811
     assert attention(L, c, heads=64, ldq=64 * 128, ldo=64 * 128, mq=1, mk=(1 << 31) - 1) == M.ERR_INVALID_ARG
     assert L.gptq_kv4_attention_workspace_size(i64(5), i32(64), ctypes.byref(c), i32(1), i32((1 << 31) - 1)) == 0
     assert L.gptq_kv4_attention_workspace_size(i64(5), i32(64), ctypes.byref(c), i32(1), i32(1 << 29)) > 0
+
+
+def test_attention_of_no_tokens_takes_bounds_of_0(L):  # noqa: F811
+    none = dict(n=0, Q=None, out=None, ws=None)
+    for mq, mk in ((0, 64), (5, 0), (0, 0)):
+        assert attention(L, **none, mq=mq, mk=mk) == M.OK
+    for kw in (dict(mq=-1), dict(mk=-1), dict(qs=None), dict(heads=3), dict(t=0), dict(scale=float("nan"))):
+        assert attention(L, **none, **kw) == M.ERR_INVALID_ARG, kw
+    assert attention(L, mq=0) == M.ERR_INVALID_ARG and attention(L, mk=0) == M.ERR_INVALID_ARG
