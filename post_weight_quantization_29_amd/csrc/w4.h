@@ -131,7 +131,8 @@ template <int ACT> GPTQ_DEV float act_slope(float x) {
     return 0.5f * erfcf(-x * 0.70710678118654752f) + x * expf(-0.5f * x * x) * 0.39894228040143268f;
   if constexpr (ACT == GPTQ_ACT_GELU_TANH) {
     const float sg = 1.0f / (1.0f + expf(-kGeluA * (x + kGeluB * x * x * x)));
-    return sg + x * sg * (1.0f - sg) * kGeluA * (1.0f + 3.0f * kGeluB * x * x);
+    // x^2 cut to where sg is 0 or 1 anyway: 0 times an overflow would be NaN
+    return sg + x * sg * (1.0f - sg) * kGeluA * (1.0f + 3.0f * kGeluB * fminf(x * x, 1.0e4f));
   }
   return 1.0f;
 }
