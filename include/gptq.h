@@ -386,7 +386,9 @@ int gptq_w4_gated(const void* X, gptq_dtype x_dtype, int64_t m, int64_t ldx, con
  * are rounded to that type (what an adapter's gradient needs; each may be
  * NULL), and dX's products take the rounded values: one rounding more than
  * exact, of the size of dX's own.  dX is written whole, in channel order.
- * dG may be G and dU may be U. */
+ * dG may be G (or dM, or U) and dU may be U (or dM, or G), whole; apart from that
+ * no output overlaps another array, and dX, dG and dU that overlap each other
+ * are refused. */
 size_t gptq_w4_gated_backward_workspace_size(int64_t m, const gptq_w4_weight* gate,
                                              const gptq_w4_weight* up);
 int gptq_w4_gated_backward(const void* dM, const void* G, const void* U, gptq_dtype dtype, int64_t m,

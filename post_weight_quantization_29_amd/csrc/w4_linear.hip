@@ -804,6 +804,12 @@ static bool is_gate(gptq_act a) { return a == GPTQ_ACT_SILU || a == GPTQ_ACT_GEL
 // 2-byte (4-byte for fp32) alignment of every element pointer
 static bool elem_ok(const void* p, gptq_dtype t) { return (reinterpret_cast<uintptr_t>(p) & (t == GPTQ_F32 ? 3 : 1)) == 0; }
 
+// two arrays (each may be NULL) share a byte
+static bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uint64_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + (uint64_t)b_bytes && y < x + (uint64_t)a_bytes;
+}
+
 struct BackLayout {
   size_t off_g, off_u, off_part, total;
   int Fp;
@@ -906,6 +912,9 @@ extern "C" int gptq_w4_gated_backward(const void* dM, const void* G, const void*
   if (!dM || !G || !U || !dX) return GPTQ_ERR_INVALID_ARG;
   for (const void* p : {dM, G, U, (const void*)dG, (const void*)dU, (const void*)dX})
     if (!elem_ok(p, dtype)) return GPTQ_ERR_INVALID_ARG;
+  // the product writes dX while it reads dG and dU
+  const int64_t xb = m * gate->d_in * 2, gb = m * gate->d_out * 2;
+  if (overlap(dX, xb, dG, gb) || overlap(dX, xb, dU, gb) || overlap(dG, gb, dU, gb)) return GPTQ_ERR_INVALID_ARG;
   if (!ws || ws_bytes < back_layout(m, gate).total || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return GPTQ_ERR_WORKSPACE;
   if (dtype == GPTQ_BF16) return backward<__bf16>(dM, G, U, m, gate, up, act, dG, dU, dX, ws, s);
   return backward<_Float16>(dM, G, U, m, gate, up, act, dG, dU, dX, ws, s);

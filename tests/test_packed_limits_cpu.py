@@ -8,7 +8,7 @@ import pytest
 
 pytest.importorskip("torch")
 from post_weight_quantization_29_amd import _lib as M  # noqa: E402
-from test_packed_ops_cpu import L, attention, backward, cache, gated, i32, i64, linear, weight  # noqa: E402, F401
+from test_packed_ops_cpu import FAKE, L, attention, backward, cache, gated, i32, i64, linear, weight  # noqa: E402, F401
 
 
 @pytest.mark.parametrize("d_out", [(1 << 27) - 31, 1 << 27, (1 << 31) - 1])
@@ -34,3 +34,15 @@ def test_attention_of_no_tokens_takes_bounds_of_0(L):  # noqa: F811
     for kw in (dict(mq=-1), dict(mk=-1), dict(qs=None), dict(heads=3), dict(t=0), dict(scale=float("nan"))):
         assert attention(L, **none, **kw) == M.ERR_INVALID_ARG, kw
     assert attention(L, mq=0) == M.ERR_INVALID_ARG and attention(L, mk=0) == M.ERR_INVALID_ARG
+
+
+def test_backward_refuses_outputs_that_overlap(L):  # noqa: F811
+    """dX is written while dG and dU are read (4 tokens of 64 and 256 channels: 512 and 2048 bytes)."""
+    far = dict(G=FAKE + (1 << 20), U=FAKE + (2 << 20), dM=FAKE + (3 << 20), ws=None)
+    for kw in (dict(dX=FAKE, dG=FAKE), dict(dX=FAKE, dG=FAKE + 2046), dict(dX=FAKE + 510, dG=FAKE), dict(dX=FAKE, dU=FAKE),
+               dict(dX=FAKE, dU=FAKE + 2046, dG=FAKE + 8192), dict(dX=FAKE + 8192, dG=FAKE, dU=FAKE), dict(dX=FAKE + 8192, dG=FAKE, dU=FAKE + 510)):
+        assert backward(L, **{**far, **kw}) == M.ERR_INVALID_ARG, kw
+    # side by side, and gradients over their own inputs, are fine (and then want a workspace)
+    for kw in (dict(dX=FAKE, dG=FAKE + 2048, dU=FAKE + 2560), dict(dX=FAKE + 512, dG=FAKE), dict(dX=FAKE, dG=far["G"], dU=far["U"]),
+               dict(dX=FAKE, dG=far["dM"])):
+        assert backward(L, **{**far, **kw}) == M.ERR_WORKSPACE, kw
