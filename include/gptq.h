@@ -450,7 +450,8 @@ int gptq_kv4_read(const gptq_kv4_cache* cache, void* K, void* V, gptq_dtype dtyp
  * sequence b, query head h, sees the positions j <= kv_len[b] - n_q + i of kv
  * head h / (n_heads / n_kv_heads):
  *   out = softmax_j(scale * q . k_j) v_j,
- * sums and statistics in fp32.  A row that sees nothing is 0.
+ * sums and statistics in fp32.  A row that sees nothing is 0.  |scale| is at
+ * most 1e8; a key whose q . k or score is below -1e30 counts as not seen.
  *  Q: token t, head h at Q + t*ldq + h*head_dim (f16/bf16, 16-byte aligned
  *  rows); out likewise with ldo, not overlapping Q.
  *  max_q_len, max_kv_len: host bounds on n_q and kv_len, at least 1 (0 too

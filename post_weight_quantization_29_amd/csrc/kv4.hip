@@ -161,6 +161,7 @@ struct AttnArgs {
 };
 
 constexpr float kNoMax = -1.0e30f;    // running maximum of a row that has seen nothing
+constexpr float kMaxScale = 1.0e8f;   // kNoMax times scale2 stays finite
 // A row's reference maximum follows the true one only when some row of the
 // wave has outgrown its own by 2^8: the terms stay below 2^8 (2^9 with fp16's
 // steps), and most tiles rescale nothing.
@@ -1045,7 +1046,7 @@ extern "C" int gptq_kv4_attention(const void* Q, gptq_dtype dtype, int64_t n_tok
   }
   if (!attn_plan(n_tokens, n_heads, cache, max_q_len, max_kv_len, p) || !q_start || !kv_len) return GPTQ_ERR_INVALID_ARG;
   if (dtype != GPTQ_F16 && dtype != GPTQ_BF16) return GPTQ_ERR_INVALID_ARG;
-  if (!(scale == scale) || std::isinf(scale)) return GPTQ_ERR_INVALID_ARG;
+  if (!(std::fabs(scale) <= kMaxScale)) return GPTQ_ERR_INVALID_ARG;      // nor NaN
   if (n_tokens == 0) return GPTQ_OK;
   const int64_t row = (int64_t)n_heads * cache->head_dim;
   if (!Q || !out || ldq < row || ldo < row || ldq % 8 != 0 || ldo % 8 != 0 || !al16(Q) || !al16(out)) return GPTQ_ERR_INVALID_ARG;

@@ -72,3 +72,14 @@ def test_attention_of_many_tokens_in_pieces(P):
     # the batch's tokens are the tensor's last ones; the others are left alone
     P.gptq_kv4_attention(Q, c, i32([T - 3, T - 2, T - 1, T]), i32([1000, 3, 700]), 1, 1024, out)
     assert bool((out[T - 3:] == 1).all()) and bool((out[:T - 3] == 5).all())
+
+
+@pytest.mark.parametrize("n_q", [3, 100])
+@pytest.mark.parametrize("scale", [1e8, -1e8])
+def test_attention_at_the_largest_scale(P, n_q, scale):
+    """One key takes all, and the rows that see nothing, next to others that do, are 0."""
+    c = constant_cache(P, 1, 64, torch.zeros((1, 8), dtype=torch.int32, device="cuda"))
+    Q = torch.randn((n_q, 2, 64), device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).to(BF)
+    out = torch.full_like(Q, 5.0)
+    P.gptq_kv4_attention(Q, c, i32([0, n_q]), i32([n_q - 2]), n_q, 128, out, scale=scale)
+    assert bool((out[:2] == 0).all()) and bool((out[2:] == 1).all())

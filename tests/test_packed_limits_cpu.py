@@ -46,3 +46,11 @@ def test_backward_refuses_outputs_that_overlap(L):  # noqa: F811
     for kw in (dict(dX=FAKE, dG=FAKE + 2048, dU=FAKE + 2560), dict(dX=FAKE + 512, dG=FAKE), dict(dX=FAKE, dG=far["G"], dU=far["U"]),
                dict(dX=FAKE, dG=far["dM"])):
         assert backward(L, **{**far, **kw}) == M.ERR_WORKSPACE, kw
+
+
+def test_attention_refuses_scales_that_leave_fp32(L):  # noqa: F811
+    """The reference of a row that has seen nothing, -1e30, times the scale has to stay finite: such a row is 0."""
+    for scale in (1.01e8, -2e8, 1e9, 3e38):
+        assert attention(L, scale=scale, n=0, Q=None, out=None, ws=None) == M.ERR_INVALID_ARG, scale
+    for scale in (1e8, -1e8, 0.0, 1e-30):
+        assert attention(L, scale=scale, n=0, Q=None, out=None, ws=None) == M.OK, scale
