@@ -197,7 +197,9 @@ int gptq_pack_dense(const uint8_t* codes, int64_t rows, int64_t cols, int32_t bi
  * Y = X W^T with W dequantized from the packed 4-bit layer (practice page
  * section 4.3: at inference the 4-bit weights are dequantized to a 16-bit type,
  * then multiplied).  W[r][c] = round16(scales[r][g] * (code[r][c] - zeros[r][g])),
- * the product taken in fp32 and rounded (ties to even) to x_dtype, with
+ * the product taken in fp32 and rounded (ties to even) to x_dtype (the weight of
+ * gptq_w4_linear too, which is the faster product where codes are packed in
+ * processing order), with
  * code[r][c] = (packed[r][c/8] >> 4(c%8)) & 15 and g = g_idx[c] (clamped to
  * [0, n_groups)), or, with g_idx NULL, g = c / group_size (group_size a
  * multiple of 8, or -1 for one group per row).  Products accumulate in fp32;
@@ -317,6 +319,8 @@ int gptq_swiglu(const float* G, const float* U, int64_t n, float* M, hipStream_t
  * bits.  They share one description of a packed weight:
  *  packed     [d_out x d_in/8] uint32, gptq_pack_int4's layout, columns in
  *             processing order (codes[:, perm] for desc_act, else as they are).
+ *             gptq_quantize_layer writes codes in channel order: a desc_act
+ *             layer's are brought into this order before they are packed.
  *  scales, zeros  [d_out x n_groups] fp32 / int32, as gptq_quantize_layer
  *             writes them; group_size a multiple of 8, or -1 for one group per
  *             row; n_groups = ceil(d_in / group_size).

@@ -462,7 +462,8 @@ def _scratch(nbytes: int, ws: Optional[torch.Tensor], index: int, stream) -> tor
 class W4Weight:
     """A packed 4-bit weight (gptq_w4_weight): packed [d_out, d_in/8] (gptq_pack_int4's words, columns in
     processing order), scales and zeros [d_out, n_groups], perm [d_in] or None.  Holds the tensors; they
-    may be rewritten in place between calls."""
+    may be rewritten in place between calls.  With perm the words are those of codes[:, perm]: a desc_act
+    layer's `packed`, which has its columns in channel order, is not; from_codes orders them."""
 
     def __init__(self, packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, group_size: int = 128,
                  perm: Optional[torch.Tensor] = None):
@@ -482,6 +483,24 @@ class W4Weight:
         self.c = gptq_w4_weight(_ptr(packed), _ptr(scales), _ptr(zeros), _ptr(perm), d_out, 8 * words, group_size,
                                 scales.shape[1])
         self.ref = ctypes.pointer(self.c)
+
+    @classmethod
+    def from_codes(cls, codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, group_size: int = 128,
+                   perm: Optional[torch.Tensor] = None) -> "W4Weight":
+        """The weight of a quantized layer: codes [d_out, d_in] uint8 in channel order, scales and zeros as
+        gptq_quantize_layer (or gptq_awq_quantize) writes them; perm: a desc_act layer's order, None for a layer
+        quantized from left to right.  Packs a copy of the codes, in that order."""
+        index = codes.device.index if codes.is_cuda else 0
+        _on(codes, "codes", index, torch.uint8)
+        _on(perm, "perm", index, torch.int32)
+        d_out, d_in = codes.shape
+        if d_in % 8:
+            raise ValueError(f"codes must have a multiple of 8 columns, got {d_in}")
+        _shape(perm, "perm", (d_in,))
+        ordered = codes if perm is None else codes.index_select(1, perm)
+        packed = torch.empty((d_out, d_in // 8), dtype=torch.int32, device=codes.device)
+        _run("gptq_pack_int4", index, None, ordered.data_ptr(), d_out, d_in, packed.data_ptr())
+        return cls(packed, scales, zeros, group_size, perm)
 
 
 def gptq_w4_linear_workspace_size(m: int, w: W4Weight) -> int:
