@@ -55,6 +55,16 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 GPTQ_DEV void copy16_lds(uint32_t lds_dst, const i32x4_t& rsrc, int voff) { GPTQ_COPY_TO_LDS("dwordx4"); }
 GPTQ_DEV void copy4_lds(uint32_t lds_dst, const i32x4_t& rsrc, int voff) { GPTQ_COPY_TO_LDS("dword"); }
 #undef GPTQ_COPY_TO_LDS
+// The same lanes' bytes of two descriptors: the wait states of the second are
+// the first's, but for M0's own.
+GPTQ_DEV void copy16_lds_two(uint32_t dst0, const i32x4_t& rsrc0, uint32_t dst1, const i32x4_t& rsrc1, int voff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds\n\t"
+               "s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %4, 0 offen lds"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane((int)dst0)), "s"(__builtin_amdgcn_readfirstlane((int)dst1)), "v"(voff),
+                 "s"(rsrc0), "s"(rsrc1)
+               : "memory", "m0");
+}
 
 // Output layout of v_mfma_f32_32x32x{2f32,16bf16,16f16} (checked on gfx950):
 // lane l, accumulator register r holds C[row][col] with

@@ -174,12 +174,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm16_kernel(Gemm16Args g, E
     const uint64_t pb = b0 + (uint64_t)p * (kGk * 2);
     return Pair{{tile_rsrc(pa, live), tile_rsrc(pa + 64, live)}, {tile_rsrc(pb, live), tile_rsrc(pb + 64, live)}};
   };
-  // copy q of a pair: half q % 2 of the lines of copy q / 2, into slots s0, s1
-  auto copy = [&](const Pair& r, int s0, int s1, int q) {
-    const int y = q >> 1;
-    const uint32_t slot = lds + ((q & 1) ? s1 : s0) * kSlot;
-    if (y < CA) copy16_lds(slot + 1024u * (W * y + wave), r.a[q & 1], voffA[y < CA ? y : 0]);
-    else copy16_lds(slot + TM * kRow + 1024u * (W * (y - CA) + wave), r.b[q & 1], voffB[y >= CA ? y - CA : 0]);
+  // copy y of a pair, both halves of its lines, into slots s0, s1
+  auto copy = [&](const Pair& r, int s0, int s1, int y) {
+    const uint32_t at = lds + 1024u * wave + (y < CA ? 1024u * W * y : TM * kRow + 1024u * W * (y - CA));
+    if (y < CA) copy16_lds_two(at + s0 * kSlot, r.a[0], at + s1 * kSlot, r.a[1], voffA[y < CA ? y : 0]);
+    else copy16_lds_two(at + s0 * kSlot, r.b[0], at + s1 * kSlot, r.b[1], voffB[y >= CA ? y - CA : 0]);
   };
   // operand reads: row lane % 32 of a 32-row block, k chunk 2 slice + lane / 32
   const uint32_t sw = (lane & 31) * kRow + (((lane >> 5) ^ ((lane >> 2) & 3)) << 4);
@@ -203,7 +202,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm16_kernel(Gemm16Args g, E
   auto copy_pair = [&](int p, int s0, int s1) {
     const Pair r = rsrc_of(p);
 #pragma unroll
-    for (int q = 0; q < kCopies; ++q) copy(r, s0, s1, q);
+    for (int y = 0; y < CA + CB; ++y) copy(r, s0, s1, y);
   };
   copy_pair(p0, 0, 1);
   copy_pair(p0 + 1, 2, 3);
@@ -253,7 +252,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm16_kernel(Gemm16Args g, E
         }
         if (last && even) {
 #pragma unroll
-          for (int f = q * kCopies / P; f < (q + 1) * kCopies / P; ++f) copy(r, SPARE, SLOT, f);
+          for (int f = q * kCopies / P; f < (q + 1) * kCopies / P; ++f)
+            if (f % 2 == 0) copy(r, SPARE, SLOT, f / 2);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
