@@ -13,8 +13,9 @@
 // one, three stages before it is needed.  Measured with no tile split (8192 x
 // 13824 x 5120, 4096 x 4096 x 22016, 4096 x 22016 x 4096): 1.11, 1.18, 1.26
 // PFLOP/s, a stage at a time 1.04, 1.08, 1.18; stages of 64 k in two slots the
-// same within 2 %.  Bound by the matrix pipe (60 % busy at the 1.87 GHz that the
-// chip's power leaves it) and the stages' barriers.
+// same within 2 %.  The matrix pipe is busy in 59-60 % of the cycles (at the 1.87
+// GHz that the chip's power leaves it) and the waves wait for a third of their
+// time: the two waves of a SIMD meet the same barriers.
 // A stage row is 64 bytes; its 16-byte chunk c sits at c ^ ((row / 4) % 4), so
 // the sixteen lanes that read sixteen consecutive rows of one chunk hit sixteen
 // different 16-byte columns of the 64 banks (the copy applies the swizzle by

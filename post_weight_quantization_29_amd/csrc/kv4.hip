@@ -185,10 +185,15 @@ constexpr float kLazy = 8.0f;
 // loads the packed words of its eight keys, pairs of words are zipped by
 // v_perm, and every code is then one shift and one and-or away.
 //
-// Bound by about 330 vector instructions per 32 keys and, next, by reading the
-// cache, 136 bytes per key (head_dim 128).  A step's loads are in flight while the
-// step before is computed.  Measured, 64 query heads on 8: one sequence of 131072
-// positions 37 us (3.8 TB/s), 48 of 1 to 8192 31 us.
+// A step of 32 keys is 322 vector instructions, 374 with masks, which a tile of
+// fewer than 16 rows always takes (its missing rows see nothing), and 4.3 KB of
+// cache (head_dim 128); its loads are in flight while the step before is
+// computed.  Measured, 64 query heads on 8: one sequence of 131072 positions 38 us
+// (3.8 TB/s), 48 of 1 to 8192 31 us.  Neither bound is reached: the counters show
+// 1.5 and 1.1 waves a SIMD on average, vector issue in 51 and 33 % of the cycles
+// and waves waiting for 42 and 35 % of their time.  What costs the rest are the
+// dependent loads in front of the first step (start, length, page, codes), a wave's
+// few steps (four of a chunk of 512), and a second, partly filled round.
 template <typename T, int HD>
 __global__ __launch_bounds__(256, 3) void kv4_rows_kernel(AttnArgs a, KvDev c, KvBatch q) {
   typedef typename T16<T>::v8 v8;
@@ -451,7 +456,8 @@ __global__ __launch_bounds__(256, 3) void kv4_rows_kernel(AttnArgs a, KvDev c, K
 // and piece and no vector instructions; a step of 0 counts as 1e-20.  Measured,
 // the prompts below: bf16 231 us, fp16 with its second piece 278 us (241 us with
 // one fp16 piece and the widest step's exponent, which cost the rows next to a
-// wide one up to seven bits).
+// wide one up to seven bits).  At head_dim 128 the 168 registers that three waves a
+// SIMD leave are all taken; the bf16 kernel spills two.
 //
 // 16-byte LDS accesses serve 16 lanes a cycle: the swizzles give 16 consecutive
 // rows of one chunk 16 different 16-byte columns of the 64 banks.
@@ -459,8 +465,10 @@ __global__ __launch_bounds__(256, 3) void kv4_rows_kernel(AttnArgs a, KvDev c, K
 // 32 rows a wave on the 32 x 32 products read LDS half as often, but their 96
 // accumulators leave two waves per SIMD, and the loop then waits for LDS more
 // than it computes (279 us against 230 for 2565 tokens of 32 heads over
-// 4613 positions); 16 rows fit three.  Bound by the vector work beside the
-// products: 0.46 PFLOP/s.
+// 4613 positions); 16 rows fit three.  0.46 PFLOP/s: the matrix pipe is busy in 19 %
+// of the cycles, vector issue (exponentials, rounding, unpacking again for every
+// 192 rows) fills 38 %, and the waves wait for 41 % of their time, as all twelve
+// meet at a tile's one barrier and eight of them unpack in front of it.
 constexpr float kNoStep = 1e-20f;
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 constexpr int kTileWaves = 12;

@@ -54,7 +54,8 @@ GPTQ_DEV uint32_t and_or(uint32_t v, uint32_t mask, uint32_t base) {
 // the exact integers code - zero (exact while |zero| <= kZeroFast).  A mixed
 // multiply reads an fp16 half as fp32, so a weight costs 2.9 vector
 // instructions instead of the 3.9 of byte conversion, subtraction and
-// multiplication; single-token products are bound by that count next to HBM.
+// multiplication; single-token products feel that count next to HBM (4096 -> 2 x
+// 11008, one token: vector issue in 42 % of the cycles).
 constexpr float kZeroFast = 1000.0f;
 
 // an fp16 half of n, as fp32, times s plus a: one mixed instruction.  (Left to

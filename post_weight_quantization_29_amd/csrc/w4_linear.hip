@@ -34,7 +34,9 @@ static W4Dev dev_of(const gptq_w4_weight* w) { return W4Dev{w->packed, w->scales
 // The NW waves of a workgroup split k in chunk pairs (256 k: one 128-byte line
 // per row), each with the next pair's loads in flight while one is multiplied,
 // and their sums are joined through LDS in wave order.
-// GRID 0: any layout.  1: rows allow 16-byte loads and a lane's 32 k share a
+// GRID 0: any layout (a (scale, zero) pair loaded for each word: 4104 -> 4096 in
+// groups of 24 12.4 us for one token, 13 for 16, 21 for 64, where 4096 -> 4096 in
+// groups of 128 takes 7.9, 7.8 and, by w4_mid_kernel, 17).  1: rows allow 16-byte loads and a lane's 32 k share a
 // group.  2: as 1, and the rows' scales and zero points fit LDS, where the
 // workgroup puts them first, in one coalesced sweep: loaded where they are
 // used, each touches 16 cache lines for 16 numbers, which cost more than the
@@ -215,9 +217,12 @@ __global__ __launch_bounds__(64 * NW) void w4_skinny_kernel(const uint16_t* __re
 // (buffer_load ... lds, 16 bytes a lane, three slots, two stages ahead), the
 // codes go to registers two stages ahead, the slice's scales and zero points to
 // LDS first.  Slices' sums go to the workspace and w4_join_kernel adds them in
-// order and finishes them.  Bound by the codes from HBM and by what dequantizing
-// them costs; measured, 24 tokens, 28672 -> 8192: 48 us (and 5 to join) against
-// 129 us with every 16 rows reading the activations themselves.
+// order and finishes them.  Measured, 24 tokens, 28672 -> 8192: 50 us (2.4 TB/s of
+// codes; and 5 to join) against 129 us with every 16 rows reading the activations
+// themselves.  Vector issue (dequantizing) fills half of the cycles, at 2.8 waves a
+// SIMD that wait for 46 % of their time: a barrier every 256 k, scales read from
+// LDS right before their use, and at up to 32 tokens five spilled registers (24
+// bytes a lane) for the 128 that let four waves share a SIMD.
 // A token's row in LDS is 512 bytes; the 16-byte chunk c of its half y sits at
 // c ^ (token % 16): 16 tokens' reads of one chunk hit 16 columns of the banks.
 constexpr int kMidK = 256;          // k per stage
@@ -559,7 +564,8 @@ __global__ __launch_bounds__(256) void gated_slopes_kernel(const uint16_t* dM, c
 // ---------------------------------------------------------------- host side
 // Tokens up to which the packed words are multiplied directly, by the 16-row
 // waves and by w4_mid_kernel.  Measured, w4_mid_kernel and through memory, 65 and
-// 128 tokens: 4096 -> 4096 18 and 25, 19 and 26 us; 5120 -> 13824 62 and 61, 68 and
+// 128 tokens (one layer, its codes in the last-level cache; from HBM 28672 ->
+// 8192 takes 157 and 163): 4096 -> 4096 18 and 25, 19 and 26 us; 5120 -> 13824 62 and 61, 68 and
 // 64 us; 28672 -> 8192 141 and 245, 147 and 252 us; 192 tokens in three blocks 29 and
 // 31, 100 and 79, 217 and 261 us.
 constexpr int kSkinnyMax = 64, kMidMax = 128;
