@@ -356,7 +356,7 @@ typedef enum {
  * fp32 sums, which are rounded once, to y_dtype.
  *  X [m x d_in] f16/bf16, row t at X + t*ldx elements (ldx >= d_in).
  *  bias [d_out] of x_dtype, or NULL.  R [m x d_out] of y_dtype, row pitch ldr,
- *  or NULL; R may be Y itself (with ldr = ldy).  Y [m x d_out] of y_dtype
+ *  or NULL; R may be Y itself (with ldr = ldy), else they do not overlap.  Y [m x d_out] of y_dtype
  *  (F32, F16 or BF16), row pitch ldy; elements between rows stay as they are.
  *  Y may overlap neither X nor bias.
  *  ws  scratch of gptq_w4_linear_workspace_size(m, w) bytes, 256-byte aligned:

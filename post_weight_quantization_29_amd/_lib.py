@@ -489,7 +489,8 @@ class W4Weight:
                    perm: Optional[torch.Tensor] = None) -> "W4Weight":
         """The weight of a quantized layer: codes [d_out, d_in] uint8 in channel order, scales and zeros as
         gptq_quantize_layer (or gptq_awq_quantize) writes them; perm: a desc_act layer's order, None for a layer
-        quantized from left to right.  Packs a copy of the codes, in that order."""
+        quantized from left to right (entries outside it count as the nearest, as in the kernels).  Packs a copy
+        of the codes, in that order."""
         index = codes.device.index if codes.is_cuda else 0
         _on(codes, "codes", index, torch.uint8)
         _on(perm, "perm", index, torch.int32)
@@ -497,7 +498,7 @@ class W4Weight:
         if d_in % 8:
             raise ValueError(f"codes must have a multiple of 8 columns, got {d_in}")
         _shape(perm, "perm", (d_in,))
-        ordered = codes if perm is None else codes.index_select(1, perm)
+        ordered = codes if perm is None else codes.index_select(1, perm.clamp(0, d_in - 1))
         packed = torch.empty((d_out, d_in // 8), dtype=torch.int32, device=codes.device)
         _run("gptq_pack_int4", index, None, ordered.data_ptr(), d_out, d_in, packed.data_ptr())
         return cls(packed, scales, zeros, group_size, perm)

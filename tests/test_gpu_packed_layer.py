@@ -75,3 +75,15 @@ def test_from_codes_refuses(P):
         with pytest.raises(ValueError):
             call()
     P.W4Weight.from_codes(codes, s, z, -1, order)
+
+
+def test_an_order_with_entries_outside_it(P):
+    """No read outside the codes: such entries count as the nearest channel."""
+    codes = torch.arange(64, device="cuda").remainder(16).to(torch.uint8).repeat(8, 1)
+    s, z = torch.ones((8, 1), device="cuda"), torch.zeros((8, 1), dtype=torch.int32, device="cuda")
+    order = torch.arange(64, dtype=torch.int32, device="cuda").flip(0).contiguous()
+    order[0], order[1], order[2] = -5, 64, 1 << 30
+    w = P.W4Weight.from_codes(codes, s, z, -1, order)
+    want = torch.empty_like(w.packed)
+    P.gptq_pack_int4(codes[:, order.clamp(0, 63).long()].contiguous(), want)
+    assert torch.equal(w.packed, want)
