@@ -399,6 +399,114 @@ int gptq_w4_gated_backward(const void* dM, const void* G, const void* U, gptq_dt
                            const gptq_w4_weight* gate, const gptq_w4_weight* up, gptq_act act, void* dG,
                            void* dU, void* dX, void* ws, size_t ws_bytes, hipStream_t s);
 
+/* dX = dY W + R, the product's gradient through the frozen packed weight (a
+ * bias's and an activation's are the caller's).
+ *  dY [m x d_out] f16/bf16, row pitch lddy.  dX [m x d_in] of x_dtype (F32, F16 or
+ *  BF16), row pitch lddx, in channel order, written whole.  R [m x d_in] of
+ *  x_dtype, row pitch ldr, or NULL: what reaches X from elsewhere (the other
+ *  projections of the same input, an adapter); R may be dX itself (with ldr = lddx),
+ *  else they do not overlap, nor do dX and dY.
+ *  The weight counts as rounded to dtype.  d_out is at most 2^20.
+ *  ws  scratch of gptq_w4_linear_backward_workspace_size(m, w) bytes (the
+ *      transposed 16-bit weight, dY's copy, partial sums). */
+size_t gptq_w4_linear_backward_workspace_size(int64_t m, const gptq_w4_weight* w);
+int gptq_w4_linear_backward(const void* dY, gptq_dtype dtype, int64_t m, int64_t lddy, const gptq_w4_weight* w,
+                            const void* R, int64_t ldr, void* dX, gptq_dtype x_dtype, int64_t lddx, void* ws,
+                            size_t ws_bytes, hipStream_t s);
+
+/* ---------------------------------------------------------------- adapters
+ * Low-rank adapters of many requests beside a shared projection
+ * (gptq_w4_linear's): a set holds n_adapters pairs of matrices of one 16-bit type,
+ *  A      [n_adapters x rank x d_in], B [n_adapters x d_out x rank], contiguous,
+ *  scale  [n_adapters] fp32,
+ * rank 1..128 (a smaller one's rows and columns are filled with zeros), d_in and
+ * d_out up to 2^20, channels in the layer's own order (whatever its perm).
+ * A batch is described on the device: sequence b's tokens are rows q_start[b] ..
+ * q_start[b+1]-1 ([n_seqs + 1] int32, not decreasing) and go through adapter[b]
+ * ([n_seqs] int32; a number outside [0, n_adapters): through none).  Rows outside
+ * [q_start[0], q_start[n_seqs]) are neither read nor written.
+ * The struct itself is host memory and is read before the call returns. */
+typedef struct {
+  const void* A;
+  const void* B;
+  const float* scale;
+  int32_t n_adapters;
+  int32_t rank;
+  int32_t d_in;
+  int32_t d_out;
+} gptq_lora_set;
+
+/* Y = R + scale_a (X A_a^T) B_a^T; a token without an adapter has Y = R.
+ *  X [m x d_in] of the set's type, row pitch ldx.  R [m x d_out] of y_dtype, row
+ *  pitch ldr, or NULL (0); R may be Y itself (with ldr = ldy: the adapters are
+ *  added to the shared projection's output), else they do not overlap.  Y [m x d_out]
+ *  of y_dtype (F32, F16 or BF16), row pitch ldy, rounded once.
+ *  S [m x rank] fp32, contiguous, or NULL: X A_a^T, for the backward pass (0 for a
+ *  token without an adapter).  Sums are fp32; X A_a^T enters the second product in
+ *  two 16-bit pieces (16 bits for bf16, 22 for fp16).
+ *  Y and S overlap neither X nor each other.  m is at most 2^24.
+ *  ws  scratch of gptq_lora_workspace_size(m, set) bytes. */
+size_t gptq_lora_workspace_size(int64_t m, const gptq_lora_set* set);
+int gptq_lora(const void* X, gptq_dtype x_dtype, int64_t m, int64_t ldx, const gptq_lora_set* set,
+              const int32_t* q_start, const int32_t* adapter, int32_t n_seqs, const void* R, int64_t ldr,
+              void* Y, gptq_dtype y_dtype, int64_t ldy, float* S, void* ws, size_t ws_bytes, hipStream_t s);
+
+/* Its backward pass, from dY, X and the forward pass's S, with dS = dY B_a:
+ *   dX = R + scale_a dS A_a,  dA_a = scale_a sum_t dS_t^T X_t,
+ *   dB_a = scale_a sum_t dY_t^T S_t,
+ * the sums over all of an adapter's tokens (0 for one without any; both are
+ * written whole).  Each of dX, dA and dB may be NULL; X is needed for dA, S for dB.
+ *  dY [m x d_out] and X [m x d_in] of dtype, the set's; dX [m x d_in] and R (NULL:
+ *  0; or dX itself) of x_dtype (F32, F16 or BF16): the shared projection's dX, say.
+ *  dA [n_adapters x rank x d_in], dB [n_adapters x d_out x rank] fp32.
+ *  Sums are fp32, added in a fixed order; dS and S enter the products in two
+ *  16-bit pieces.  Outputs overlap neither inputs nor each other.
+ *  ws  scratch of gptq_lora_backward_workspace_size(m, set) bytes (NULL if m is 0). */
+size_t gptq_lora_backward_workspace_size(int64_t m, const gptq_lora_set* set);
+int gptq_lora_backward(const void* dY, gptq_dtype dtype, int64_t m, int64_t lddy, const void* X, int64_t ldx,
+                       const float* S, const gptq_lora_set* set, const int32_t* q_start, const int32_t* adapter,
+                       int32_t n_seqs, const void* R, int64_t ldr, void* dX, gptq_dtype x_dtype, int64_t lddx,
+                       float* dA, float* dB, void* ws, size_t ws_bytes, hipStream_t s);
+
+/* ---------------------------------------------------------------- the residual stream and its norms
+ * What stands between two sub-layers, in one pass:
+ *   b = B, or with post_gamma its norm: unit(B) * post_gamma,
+ *   H = R + alpha * gate * b,   Y = unit(H) * gamma,
+ * unit(x) = x / sqrt(mean_j x_j^2 + eps).  Y is the norm of the unrounded H.
+ *  R, H   [m x d] of h_dtype, row pitches ldr, ldh: the stream before and after.
+ *         H may be R (with ldh = ldr).
+ *  B, Y   [m x d] of dtype, row pitches ldb, ldy.  h_dtype is dtype or F32.
+ *         B NULL: H = R, only Y is written (post_gamma, gate and H are NULL).
+ *         Y or H may be NULL; either may be B (same type and pitch).
+ *  post_gamma, gate, gamma  [d] fp32, each NULL for 1 (post_gamma NULL: no norm).
+ * Outputs overlap nothing else.  d is at most 16384.  Statistics are fp32. */
+int gptq_residual_rmsnorm(const void* R, gptq_dtype h_dtype, int64_t ldr, const void* B, gptq_dtype dtype,
+                          int64_t ldb, int64_t m, int32_t d, const float* post_gamma, const float* gate,
+                          float alpha, const float* gamma, float eps, void* H, int64_t ldh, void* Y, int64_t ldy,
+                          hipStream_t s);
+
+/* Its backward pass, at the stored stream H: with n = unit(H),
+ *   dh = dH + (dY gamma - n mean(dY gamma n)) / sqrt(mean H^2 + eps),
+ *   dR = dh,   dB = alpha gate dh, through unit(B) post_gamma where there is one,
+ *   dgamma = sum_t dY n,   dgate = alpha sum_t dh b,
+ *   dpost_gamma = sum_t alpha gate dh unit(B).
+ *  dH  [m x d] of h_dtype, what reaches the stream behind the norm, or NULL (0).
+ *  B   as in the forward pass; read only with post_gamma or gate (else it may be
+ *      NULL).  dR of h_dtype, dB of dtype, dgamma, dpost_gamma and dgate [d] fp32:
+ *      each may be NULL.  The sums are written, not added to (0 if m is 0), and do not
+ *      depend on timing.
+ *  dR and dB may each be one of dY, H, dH, B whole (same type and pitch); they overlap
+ *  nothing else, nor each other.
+ *  ws  scratch of gptq_residual_rmsnorm_backward_workspace_size(m, d) bytes (NULL
+ *      without dgamma, dpost_gamma and dgate). */
+size_t gptq_residual_rmsnorm_backward_workspace_size(int64_t m, int32_t d);
+int gptq_residual_rmsnorm_backward(const void* dY, gptq_dtype dtype, int64_t lddy, const void* H,
+                                   gptq_dtype h_dtype, int64_t ldh, const void* dH, int64_t lddh, const void* B,
+                                   int64_t ldb, int64_t m, int32_t d, const float* post_gamma, const float* gate,
+                                   float alpha, const float* gamma, float eps, void* dR, int64_t lddr, void* dB,
+                                   int64_t lddb, float* dgamma, float* dpost_gamma, float* dgate, void* ws,
+                                   size_t ws_bytes, hipStream_t s);
+
 /* ---------------------------------------------------------------- a cache held in 4 bits
  * Keys and values of a decoder block in pages of 4-bit rows.  A row is one
  * token's head_dim values of one kv head, on its own min-max grid:
@@ -469,6 +577,50 @@ int gptq_kv4_attention(const void* Q, gptq_dtype dtype, int64_t n_tokens, int32_
                        const gptq_kv4_cache* cache, const int32_t* q_start, const int32_t* kv_len,
                        int32_t max_q_len, int32_t max_kv_len, float scale, void* out, int64_t ldo,
                        void* ws, size_t ws_bytes, hipStream_t s);
+
+/* ---------------------------------------------------------------- whole prompts
+ * Causal attention of whole sequences packed one behind the other, before their
+ * keys and values go into a cache, or in training: token i of a sequence, query
+ * head h, sees the sequence's tokens j <= i of kv head h / (n_heads / n_kv_heads):
+ *   out = softmax_j(scale * q . k_j) v_j,   lse = log sum_j exp(scale * q . k_j).
+ *  Q, out  token t, head h at Q + t*ldq + h*head_dim elements; K, V likewise with
+ *          n_kv_heads heads: rows of a fused projection as they are.  f16 or bf16,
+ *          rows 16-byte aligned; pitches below 2^22 elements.  head_dim 64 or 128;
+ *          n_heads a multiple of n_kv_heads.  out overlaps no input.
+ *  q_start [n_seqs + 1] int32 (device, not decreasing): sequence b is rows
+ *          q_start[b] .. q_start[b+1]-1.  Rows outside [q_start[0], q_start[n_seqs])
+ *          are left as they are, and so are a sequence's tokens past max_len
+ *          (a host bound on the lengths, at least 1), which nobody sees.
+ *  lse     [n_tokens x n_heads] fp32, or NULL: what the backward pass needs.
+ * Scores and statistics are fp32; the probabilities are rounded to 16 bits for the
+ * second product.  What a token does not see, infinities and NaN too, does not
+ * reach it.  |scale| is at most 1e8; a key whose score is below -1e30 counts as
+ * not seen, and a row that sees nothing is 0 (its lse -inf); a score above 1e38 may
+ * count as infinite (the row is then no number). */
+int gptq_prompt_attention(const void* Q, const void* K, const void* V, gptq_dtype dtype, int64_t n_tokens,
+                          int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int64_t ldq, int64_t ldk,
+                          int64_t ldv, const int32_t* q_start, int32_t n_seqs, int32_t max_len, float scale,
+                          void* out, int64_t ldo, float* lse, hipStream_t s);
+
+/* Its backward pass, from dOut and the forward pass's out and lse: with
+ * p_ij = exp(scale q_i . k_j - lse_i) and ds_ij = p_ij (dout_i . v_j - dout_i . out_i),
+ *   dV_j = sum p_ij dout_i,  dK_j = scale sum ds_ij q_i,  dQ_i = scale sum_j ds_ij k_j,
+ * the sums over i >= j and over the query heads of a kv head.  (lse is fp32: p is
+ * off by up to 2^-23 |lse| relatively.)
+ *  dOut, out and dQ are laid out as Q, dK and dV as K and V, each with its own
+ *  pitch (gradients of one fused row are written in place).  p and ds are rounded
+ *  to 16 bits for the products (fp16: below a power of two that follows ds); sums are
+ *  fp32, in a fixed order.
+ *  dQ, dK and dV overlap no input and, row by row, not each other.
+ *  ws  scratch of gptq_prompt_attention_backward_workspace_size(n_tokens, n_heads)
+ *      bytes. */
+size_t gptq_prompt_attention_backward_workspace_size(int64_t n_tokens, int32_t n_heads);
+int gptq_prompt_attention_backward(const void* dOut, int64_t lddo, const void* Q, const void* K, const void* V,
+                                   gptq_dtype dtype, int64_t n_tokens, int32_t n_heads, int32_t n_kv_heads,
+                                   int32_t head_dim, int64_t ldq, int64_t ldk, int64_t ldv, const void* out,
+                                   int64_t ldo, const float* lse, const int32_t* q_start, int32_t n_seqs,
+                                   int32_t max_len, float scale, void* dQ, int64_t lddq, void* dK, int64_t lddk,
+                                   void* dV, int64_t lddv, void* ws, size_t ws_bytes, hipStream_t s);
 
 /* ---------------------------------------------------------------- misc */
 const char* gptq_status_string(int status);

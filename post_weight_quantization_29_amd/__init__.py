@@ -17,7 +17,10 @@ from ._lib import (  # noqa: F401
     gptq_swiglu, GPTQ_ACTS, KV4Cache, W4Weight, gptq_kv4_append, gptq_kv4_attention,
     gptq_kv4_attention_workspace_size, gptq_kv4_read, gptq_w4_gated, gptq_w4_gated_backward,
     gptq_w4_gated_backward_workspace_size, gptq_w4_gated_workspace_size, gptq_w4_linear,
-    gptq_w4_linear_workspace_size,
+    gptq_w4_linear_workspace_size, gptq_w4_linear_backward, gptq_w4_linear_backward_workspace_size, LoRASet, gptq_lora,
+    gptq_lora_backward, gptq_lora_backward_workspace_size, gptq_lora_workspace_size, gptq_prompt_attention,
+    gptq_prompt_attention_backward, gptq_prompt_attention_backward_workspace_size, gptq_residual_rmsnorm,
+    gptq_residual_rmsnorm_backward, gptq_residual_rmsnorm_backward_workspace_size,
     gptq_prepare_hinv_workspace_size, gptq_quantize_layer, gptq_quantize_workspace_size,
     gptq_status_string, lib, make_config,
 )

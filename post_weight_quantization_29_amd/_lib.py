@@ -45,6 +45,12 @@ class gptq_w4_weight(ctypes.Structure):
                 ("group_size", ctypes.c_int32), ("n_groups", ctypes.c_int32)]
 
 
+class gptq_lora_set(ctypes.Structure):
+    _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("n_adapters", ctypes.c_int32), ("rank", ctypes.c_int32), ("d_in", ctypes.c_int32),
+                ("d_out", ctypes.c_int32)]
+
+
 class gptq_kv4_cache(ctypes.Structure):
     _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_grid", ctypes.c_void_p),
                 ("v_grid", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("n_pages", ctypes.c_int32),
@@ -63,7 +69,8 @@ def lib() -> ctypes.CDLL:
                               f"`python -m post_weight_quantization_29_amd.build_lib`")
         L = ctypes.CDLL(LIB_PATH)
         vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
-        wt, kv = ctypes.POINTER(gptq_w4_weight), ctypes.POINTER(gptq_kv4_cache)
+        wt, kv, lr = ctypes.POINTER(gptq_w4_weight), ctypes.POINTER(gptq_kv4_cache), ctypes.POINTER(gptq_lora_set)
+        dt, f32 = ctypes.c_int, ctypes.c_float
         sig = {
             "gptq_hessian_workspace_size": (sz, [i64, i32]),
             "gptq_hessian_accumulate": (ctypes.c_int, [vp, vp, vp, ctypes.c_int, i64, i32, vp, sz, vp]),
@@ -108,6 +115,24 @@ def lib() -> ctypes.CDLL:
             "gptq_kv4_attention_workspace_size": (sz, [i64, i32, kv, i32, i32]),
             "gptq_kv4_attention": (ctypes.c_int, [vp, ctypes.c_int, i64, i32, i64, kv, vp, vp, i32, i32,
                                                   ctypes.c_float, vp, i64, vp, sz, vp]),
+            "gptq_w4_linear_backward_workspace_size": (sz, [i64, wt]),
+            "gptq_w4_linear_backward": (ctypes.c_int, [vp, dt, i64, i64, wt, vp, i64, vp, dt, i64, vp, sz, vp]),
+            "gptq_lora_workspace_size": (sz, [i64, lr]),
+            "gptq_lora": (ctypes.c_int, [vp, dt, i64, i64, lr, vp, vp, i32, vp, i64, vp, dt, i64, vp, vp, sz, vp]),
+            "gptq_lora_backward_workspace_size": (sz, [i64, lr]),
+            "gptq_lora_backward": (ctypes.c_int, [vp, dt, i64, i64, vp, i64, vp, lr, vp, vp, i32, vp, i64, vp, dt, i64, vp,
+                                                  vp, vp, sz, vp]),
+            "gptq_residual_rmsnorm": (ctypes.c_int, [vp, dt, i64, vp, dt, i64, i64, i32, vp, vp, f32, vp, f32, vp, i64, vp,
+                                                     i64, vp]),
+            "gptq_residual_rmsnorm_backward_workspace_size": (sz, [i64, i32]),
+            "gptq_residual_rmsnorm_backward": (ctypes.c_int, [vp, dt, i64, vp, dt, i64, vp, i64, vp, i64, i64, i32, vp, vp,
+                                                              f32, vp, f32, vp, i64, vp, i64, vp, vp, vp, vp, sz, vp]),
+            "gptq_prompt_attention": (ctypes.c_int, [vp, vp, vp, dt, i64, i32, i32, i32, i64, i64, i64, vp, i32, i32, f32,
+                                                     vp, i64, vp, vp]),
+            "gptq_prompt_attention_backward_workspace_size": (sz, [i64, i32]),
+            "gptq_prompt_attention_backward": (ctypes.c_int, [vp, i64, vp, vp, vp, dt, i64, i32, i32, i32, i64, i64, i64,
+                                                              vp, i64, vp, vp, i32, i32, f32, vp, i64, vp, i64, vp, i64, vp,
+                                                              sz, vp]),
             "gptq_layer_error_workspace_size": (sz, [i32, i32]),
             "gptq_layer_error": (ctypes.c_int, [vp, vp, ctypes.c_int, vp, i32, i32,
                                                 ctypes.POINTER(ctypes.c_double), vp, sz, vp]),
@@ -132,7 +157,11 @@ EXPORTED = ("gptq_hessian_workspace_size", "gptq_hessian_accumulate",
             "gptq_w4_linear_workspace_size", "gptq_w4_linear", "gptq_w4_gated_workspace_size",
             "gptq_w4_gated", "gptq_w4_gated_backward_workspace_size", "gptq_w4_gated_backward",
             "gptq_kv4_append", "gptq_kv4_read", "gptq_kv4_attention_workspace_size",
-            "gptq_kv4_attention",
+            "gptq_kv4_attention", "gptq_w4_linear_backward_workspace_size", "gptq_w4_linear_backward",
+            "gptq_lora_workspace_size", "gptq_lora", "gptq_lora_backward_workspace_size", "gptq_lora_backward",
+            "gptq_residual_rmsnorm", "gptq_residual_rmsnorm_backward_workspace_size",
+            "gptq_residual_rmsnorm_backward", "gptq_prompt_attention",
+            "gptq_prompt_attention_backward_workspace_size", "gptq_prompt_attention_backward",
             "gptq_layer_error_workspace_size", "gptq_layer_error", "gptq_status_string",
             "gptq_abi_version")
 
@@ -572,6 +601,172 @@ def gptq_w4_gated_backward(dM: torch.Tensor, G: torch.Tensor, U: torch.Tensor, g
          _act(act), _ptr(dG), _ptr(dU), dX.data_ptr(), ws.data_ptr(), ws.nbytes)
 
 
+def gptq_w4_linear_backward_workspace_size(m: int, w: W4Weight) -> int:
+    return int(lib().gptq_w4_linear_backward_workspace_size(m, w.ref))
+
+
+def gptq_w4_linear_backward(dY: torch.Tensor, w: W4Weight, dX: torch.Tensor, R: Optional[torch.Tensor] = None,
+                            ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """dX [m, d_in] = dY W + R.  dY, dX and R may have pitched rows; R may be dX."""
+    dev, m = w.index, dY.shape[0]
+    _on(dY, "dY", dev, rows=True); _on(dX, "dX", dev, rows=True)
+    _shape(dY, "dY", (m, w.d_out)); _shape(dX, "dX", (m, w.d_in))
+    if R is not None:
+        _on(R, "R", dev, dX.dtype, rows=True); _shape(R, "R", (m, w.d_in))
+    yt = _dtype16(dY, "dY")
+    if dX.dtype not in _DTYPE:
+        raise ValueError(f"dX must be float32, float16 or bfloat16, got {dX.dtype}")
+    ws = _scratch(0 if ws is not None else gptq_w4_linear_backward_workspace_size(m, w), ws, dev, stream)
+    _run("gptq_w4_linear_backward", dev, stream, dY.data_ptr(), yt, m, _pitch(dY), w.ref, _ptr(R),
+         0 if R is None else _pitch(R), dX.data_ptr(), _DTYPE[dX.dtype], _pitch(dX), ws.data_ptr(), ws.nbytes)
+
+
+# ---------------------------------------------------------------- adapters
+
+class LoRASet:
+    """Low-rank adapters (gptq_lora_set): A [n_adapters, rank, d_in] and B [n_adapters, d_out, rank] of one 16-bit type,
+    scale [n_adapters] float32.  Holds the tensors; they may be rewritten in place between calls."""
+
+    def __init__(self, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor):
+        index = A.device.index if A.is_cuda else 0
+        _on(A, "A", index); _on(B, "B", index, A.dtype); _on(scale, "scale", index, torch.float32)
+        _dtype16(A, "A")
+        if A.dim() != 3:
+            raise ValueError(f"A must have shape (adapters, rank, d_in), got {tuple(A.shape)}")
+        n, rank, d_in = A.shape
+        if B.dim() != 3:
+            raise ValueError(f"B must have shape (adapters, d_out, rank), got {tuple(B.shape)}")
+        _shape(B, "B", (n, B.shape[1], rank)); _shape(scale, "scale", (n,))
+        if not 1 <= rank <= 128:
+            raise ValueError(f"rank must be 1 to 128, got {rank}")
+        self.A, self.B, self.scale = A, B, scale
+        self.n_adapters, self.rank, self.d_in, self.d_out, self.index, self.dtype = n, rank, d_in, B.shape[1], index, A.dtype
+        self.c = gptq_lora_set(_ptr(A), _ptr(B), _ptr(scale), n, rank, d_in, B.shape[1])
+        self.ref = ctypes.pointer(self.c)
+
+
+def _requests(q_start: torch.Tensor, adapter: torch.Tensor, index: int) -> int:
+    n = adapter.numel()
+    _on(q_start, "q_start", index, torch.int32); _on(adapter, "adapter", index, torch.int32)
+    _shape(adapter, "adapter", (n,)); _shape(q_start, "q_start", (n + 1,))
+    return n
+
+
+def _rows16(t: Optional[torch.Tensor], name: str, index: int, shape: tuple, dtype=None) -> None:
+    """Rows that may be pitched, of `dtype` or any of the three types."""
+    if t is None:
+        return
+    _on(t, name, index, dtype, rows=True); _shape(t, name, shape)
+    if t.dtype not in _DTYPE:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+
+
+def _row_pitch(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else _pitch(t)
+
+
+def gptq_lora_workspace_size(m: int, adapters: LoRASet) -> int:
+    return int(lib().gptq_lora_workspace_size(m, adapters.ref))
+
+
+def gptq_lora(X: torch.Tensor, adapters: LoRASet, q_start: torch.Tensor, adapter: torch.Tensor, Y: torch.Tensor,
+              R: Optional[torch.Tensor] = None, S: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+              stream=None) -> None:
+    """Y [m, d_out] = R + scale (X A^T) B^T with each token's adapter: sequence b (rows q_start[b] .. q_start[b+1]-1) goes
+    through adapter[b], or none (-1).  R None counts as 0 and may be Y; S [m, rank] float32 takes X A^T for the backward pass."""
+    dev, m = adapters.index, X.shape[0]
+    n = _requests(q_start, adapter, dev)
+    _rows16(X, "X", dev, (m, adapters.d_in), adapters.dtype)
+    _rows16(Y, "Y", dev, (m, adapters.d_out)); _rows16(R, "R", dev, (m, adapters.d_out), Y.dtype)
+    _on(S, "S", dev, torch.float32); _shape(S, "S", (m, adapters.rank))
+    ws = _scratch(0 if ws is not None else gptq_lora_workspace_size(m, adapters), ws, dev, stream)
+    _run("gptq_lora", dev, stream, X.data_ptr(), _DTYPE[X.dtype], m, _pitch(X), adapters.ref, q_start.data_ptr(),
+         adapter.data_ptr(), n, _ptr(R), _row_pitch(R), Y.data_ptr(), _DTYPE[Y.dtype], _pitch(Y), _ptr(S), ws.data_ptr(),
+         ws.nbytes)
+
+
+def gptq_lora_backward_workspace_size(m: int, adapters: LoRASet) -> int:
+    return int(lib().gptq_lora_backward_workspace_size(m, adapters.ref))
+
+
+def gptq_lora_backward(dY: torch.Tensor, X: Optional[torch.Tensor], S: Optional[torch.Tensor], adapters: LoRASet,
+                       q_start: torch.Tensor, adapter: torch.Tensor, dX: Optional[torch.Tensor] = None,
+                       R: Optional[torch.Tensor] = None, dA: Optional[torch.Tensor] = None,
+                       dB: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """dX [m, d_in] = R + scale (dY B) A, dA and dB (float32, the shapes of A and B) the sums over each adapter's tokens;
+    each may be None.  X is needed for dA, the forward pass's S for dB; R may be dX."""
+    dev, m = adapters.index, dY.shape[0]
+    n = _requests(q_start, adapter, dev)
+    _rows16(dY, "dY", dev, (m, adapters.d_out), adapters.dtype); _rows16(X, "X", dev, (m, adapters.d_in), adapters.dtype)
+    _on(S, "S", dev, torch.float32); _shape(S, "S", (m, adapters.rank))
+    _rows16(dX, "dX", dev, (m, adapters.d_in))
+    if R is not None:
+        if dX is None:
+            raise ValueError("R is added to dX, which is None")
+        _rows16(R, "R", dev, (m, adapters.d_in), dX.dtype)
+    for t, name, like in ((dA, "dA", adapters.A), (dB, "dB", adapters.B)):
+        _on(t, name, dev, torch.float32); _shape(t, name, tuple(like.shape))
+    ws = _scratch(0 if ws is not None else gptq_lora_backward_workspace_size(m, adapters), ws, dev, stream)
+    _run("gptq_lora_backward", dev, stream, dY.data_ptr(), _DTYPE[dY.dtype], m, _pitch(dY), _ptr(X), _row_pitch(X), _ptr(S),
+         adapters.ref, q_start.data_ptr(), adapter.data_ptr(), n, _ptr(R), _row_pitch(R), _ptr(dX),
+         _DTYPE[dY.dtype if dX is None else dX.dtype], _row_pitch(dX), _ptr(dA), _ptr(dB), ws.data_ptr(), ws.nbytes)
+
+
+# ---------------------------------------------------------------- the residual stream and its norms
+
+def _vectors(index: int, d: int, **vectors) -> None:
+    for name, t in vectors.items():
+        _on(t, name, index, torch.float32); _shape(t, name, (d,))
+
+
+def gptq_residual_rmsnorm(R: torch.Tensor, Y: Optional[torch.Tensor], B: Optional[torch.Tensor] = None,
+                          H: Optional[torch.Tensor] = None, gamma: Optional[torch.Tensor] = None,
+                          post_gamma: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                          alpha: float = 1.0, eps: float = 1e-6, stream=None) -> None:
+    """H = R + alpha * gate * b with b = B, or its norm times post_gamma, and Y = norm(H) * gamma; all [m, d], gamma,
+    post_gamma and gate [d] float32.  R and H have one type, Y and B one (R's, or 16-bit ones beside a float32 stream).
+    H may be R.  Without B, Y = norm(R) * gamma."""
+    dev, (m, d) = R.get_device(), R.shape
+    if dev < 0:
+        raise ValueError(f"R must be on a GPU, got {R.device}")
+    some = Y if Y is not None else B
+    if some is None:
+        raise ValueError("Y or B must be given")
+    _rows16(R, "R", dev, (m, d)); _rows16(H, "H", dev, (m, d), R.dtype)
+    _rows16(Y, "Y", dev, (m, d), some.dtype); _rows16(B, "B", dev, (m, d), some.dtype)
+    _vectors(dev, d, gamma=gamma, post_gamma=post_gamma, gate=gate)
+    _run("gptq_residual_rmsnorm", dev, stream, R.data_ptr(), _DTYPE[R.dtype], _pitch(R), _ptr(B), _DTYPE[some.dtype],
+         _row_pitch(B), m, d, _ptr(post_gamma), _ptr(gate), float(alpha), _ptr(gamma), float(eps), _ptr(H), _row_pitch(H),
+         _ptr(Y), _row_pitch(Y))
+
+
+def gptq_residual_rmsnorm_backward_workspace_size(m: int, d: int) -> int:
+    return int(lib().gptq_residual_rmsnorm_backward_workspace_size(m, d))
+
+
+def gptq_residual_rmsnorm_backward(dY: torch.Tensor, H: torch.Tensor, dR: Optional[torch.Tensor],
+                                   dH: Optional[torch.Tensor] = None, B: Optional[torch.Tensor] = None,
+                                   dB: Optional[torch.Tensor] = None, gamma: Optional[torch.Tensor] = None,
+                                   post_gamma: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                                   alpha: float = 1.0, eps: float = 1e-6, dgamma: Optional[torch.Tensor] = None,
+                                   dpost_gamma: Optional[torch.Tensor] = None, dgate: Optional[torch.Tensor] = None,
+                                   ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """dR (and, with a branch, dB) [m, d], dgamma, dpost_gamma and dgate [d] float32 from dY, the stored stream H and dH,
+    what reaches it from behind the norm (None: nothing).  B is read only with post_gamma or gate."""
+    dev, (m, d) = H.get_device(), H.shape
+    if dev < 0:
+        raise ValueError(f"H must be on a GPU, got {H.device}")
+    _rows16(H, "H", dev, (m, d)); _rows16(dY, "dY", dev, (m, d))
+    _rows16(dH, "dH", dev, (m, d), H.dtype); _rows16(dR, "dR", dev, (m, d), H.dtype)
+    _rows16(B, "B", dev, (m, d), dY.dtype); _rows16(dB, "dB", dev, (m, d), dY.dtype)
+    _vectors(dev, d, gamma=gamma, post_gamma=post_gamma, gate=gate, dgamma=dgamma, dpost_gamma=dpost_gamma, dgate=dgate)
+    ws = _scratch(0 if ws is not None else gptq_residual_rmsnorm_backward_workspace_size(m, d), ws, dev, stream)
+    _run("gptq_residual_rmsnorm_backward", dev, stream, dY.data_ptr(), _DTYPE[dY.dtype], _pitch(dY), H.data_ptr(),
+         _DTYPE[H.dtype], _pitch(H), _ptr(dH), _row_pitch(dH), _ptr(B), _row_pitch(B), m, d, _ptr(post_gamma), _ptr(gate),
+         float(alpha), _ptr(gamma), float(eps), _ptr(dR), _row_pitch(dR), _ptr(dB), _row_pitch(dB), _ptr(dgamma),
+         _ptr(dpost_gamma), _ptr(dgate), ws.data_ptr(), ws.nbytes)
+
+
 # ---------------------------------------------------------------- a cache held in 4 bits
 
 class KV4Cache:
@@ -681,6 +876,67 @@ def gptq_kv4_attention(Q: torch.Tensor, cache: KV4Cache, q_start: torch.Tensor, 
     _run("gptq_kv4_attention", dev, stream, Q.data_ptr(), qt, T, n_heads, _pitch(Q), cache.ref, q_start.data_ptr(),
          kv_len.data_ptr(), max_q_len, max_kv_len, hd ** -0.5 if scale is None else float(scale), out.data_ptr(),
          _pitch(out), ws.data_ptr(), ws.nbytes)
+
+
+# ---------------------------------------------------------------- whole prompts
+
+def _prompt(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, q_start: torch.Tensor, max_len: int) -> tuple:
+    dev = Q.get_device()
+    if dev < 0:
+        raise ValueError(f"Q must be on a GPU, got {Q.device}")
+    if Q.dim() != 3 or K.dim() != 3:
+        raise ValueError(f"Q and K must have shape (tokens, heads, head_dim), got {tuple(Q.shape)} and {tuple(K.shape)}")
+    (T, H, hd), n_kv = Q.shape, K.shape[1]
+    _dtype16(Q, "Q")
+    _heads(Q, "Q", dev, H, hd); _heads(K, "K", dev, n_kv, hd, Q.dtype); _heads(V, "V", dev, n_kv, hd, Q.dtype)
+    if K.shape[0] != T or V.shape[0] != T:
+        raise ValueError(f"K and V must have {T} tokens, got {K.shape[0]} and {V.shape[0]}")
+    _on(q_start, "q_start", dev, torch.int32)
+    if q_start.dim() != 1 or q_start.numel() < 2:
+        raise ValueError(f"q_start must have shape (sequences + 1,), got {tuple(q_start.shape)}")
+    if max_len >> 31:
+        raise ValueError(f"max_len must fit 32 bits, got {max_len}")
+    return dev, T, H, n_kv, hd
+
+
+def _like(t: torch.Tensor, name: str, other: torch.Tensor, index: int) -> None:
+    _heads(t, name, index, other.shape[1], other.shape[2], other.dtype)
+    if t.shape[0] != other.shape[0]:
+        raise ValueError(f"{name} must have {other.shape[0]} tokens, got {t.shape[0]}")
+
+
+def gptq_prompt_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, q_start: torch.Tensor, max_len: int,
+                          out: torch.Tensor, lse: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                          stream=None) -> None:
+    """out [tokens, n_heads, head_dim] = causal attention of whole sequences packed one behind the other (rows q_start[b] ..
+    q_start[b+1]-1, at most max_len each), K and V [tokens, n_kv_heads, head_dim]; lse [tokens, n_heads] float32 for the
+    backward pass (scale None: 1/sqrt(head_dim))."""
+    dev, T, H, n_kv, hd = _prompt(Q, K, V, q_start, max_len)
+    _like(out, "out", Q, dev)
+    _on(lse, "lse", dev, torch.float32); _shape(lse, "lse", (T, H))
+    _run("gptq_prompt_attention", dev, stream, Q.data_ptr(), K.data_ptr(), V.data_ptr(), _DTYPE[Q.dtype], T, H, n_kv, hd,
+         _pitch(Q), _pitch(K), _pitch(V), q_start.data_ptr(), q_start.numel() - 1, max_len,
+         hd ** -0.5 if scale is None else float(scale), out.data_ptr(), _pitch(out), _ptr(lse))
+
+
+def gptq_prompt_attention_backward_workspace_size(n_tokens: int, n_heads: int) -> int:
+    return int(lib().gptq_prompt_attention_backward_workspace_size(n_tokens, n_heads))
+
+
+def gptq_prompt_attention_backward(dOut: torch.Tensor, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, out: torch.Tensor,
+                                   lse: torch.Tensor, q_start: torch.Tensor, max_len: int, dQ: torch.Tensor, dK: torch.Tensor,
+                                   dV: torch.Tensor, scale: Optional[float] = None, ws: Optional[torch.Tensor] = None,
+                                   stream=None) -> None:
+    """dQ, dK and dV (laid out as Q, K and V, each with a pitch of its own) from dOut and the forward pass's out and lse."""
+    dev, T, H, n_kv, hd = _prompt(Q, K, V, q_start, max_len)
+    for t, name, like in ((dOut, "dOut", Q), (out, "out", Q), (dQ, "dQ", Q), (dK, "dK", K), (dV, "dV", V)):
+        _like(t, name, like, dev)
+    _on(lse, "lse", dev, torch.float32); _shape(lse, "lse", (T, H))
+    ws = _scratch(0 if ws is not None else gptq_prompt_attention_backward_workspace_size(T, H), ws, dev, stream)
+    _run("gptq_prompt_attention_backward", dev, stream, dOut.data_ptr(), _pitch(dOut), Q.data_ptr(), K.data_ptr(), V.data_ptr(),
+         _DTYPE[Q.dtype], T, H, n_kv, hd, _pitch(Q), _pitch(K), _pitch(V), out.data_ptr(), _pitch(out), lse.data_ptr(),
+         q_start.data_ptr(), q_start.numel() - 1, max_len, hd ** -0.5 if scale is None else float(scale), dQ.data_ptr(),
+         _pitch(dQ), dK.data_ptr(), _pitch(dK), dV.data_ptr(), _pitch(dV), ws.data_ptr(), ws.nbytes)
 
 
 def gptq_layer_error_workspace_size(d_out: int, d_in: int) -> int:

@@ -35,6 +35,11 @@ namespace gptq {
   } while (0)
 
 constexpr size_t kAlign = 256;
+// bytes from the first to behind the last of m rows of d elements, pitch ld (2^62 where that is more)
+inline uint64_t rows_bytes(int64_t m, int64_t ld, int64_t d, int64_t elem) {
+  const __int128 n = ((__int128)(m - 1) * ld + d) * elem;
+  return n > ((__int128)1 << 62) ? (uint64_t)1 << 62 : (uint64_t)n;
+}
 inline size_t align_up(size_t x, size_t a = kAlign) { return (x + a - 1) / a * a; }
 
 // Copies HBM -> LDS without registers: lane l's 16 (4) bytes at the

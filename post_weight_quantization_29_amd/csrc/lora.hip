@@ -1,0 +1,762 @@
+// Low-rank adapters of many requests beside a shared projection, forward and
+// backward.  Token t of a sequence with adapter a:
+//
+//   s_t = A_a x_t                              [rank]
+//   y_t = r_t + scale_a B_a s_t                [d_out]
+//   dS_t = B_a' dy_t (unscaled),  dx_t = r_t + scale_a A_a' dS_t
+//   dA_a = scale_a sum_t dS_t x_t',  dB_a = scale_a sum_t dy_t s_t'
+//
+// A batch mixes adapters token by token (a decode step) or in long runs
+// (prompts), so the kernels go by blocks of 16 tokens and, inside one, by the
+// adapters that occur in it: a product with one adapter's matrix is made for all
+// 16 columns of the matrix instruction, and each token keeps the one of its own
+// adapter (kept by selection, not by zeros: another request's infinities do not
+// reach it).
+//
+// s and dS are fp32.  Where they are an operand of a matrix instruction they go in
+// two pieces of the operands' 16-bit type (16 bits for bf16, 22 for fp16).
+#include "w4_epilogue.h"
+
+#include <climits>
+#include <utility>
+
+namespace gptq {
+
+constexpr int kLoraMaxRank = 128, kLoraMaxDim = 1 << 20, kLoraMaxSets = 65535;
+constexpr int kLowWaves = 4, kUpWaves = 4;
+
+struct LoraBatch {
+  const int32_t* q_start;
+  const int32_t* adapter;
+  int n_seqs, n_adapters;
+  int64_t m;
+};
+
+constexpr int kNoAdapter = -1, kNoToken = -2;
+
+// The adapters of tokens t0 .. t0 + 15 (lane i: token i % 16's): a token's
+// sequence is the number of starts up to it, less one, so sequences without
+// tokens are passed over.
+GPTQ_DEV int adapter_of(const LoraBatch& b, int64_t t0) {
+  const int lane = threadIdx.x & 63;
+  int count = 0;
+  for (int i0 = 0; i0 <= b.n_seqs; i0 += 64) {
+    const int64_t v = i0 + lane <= b.n_seqs ? (int64_t)b.q_start[i0 + lane] : INT64_MAX;
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      c = __popcll(__ballot(v <= t0 + i));
+      if ((lane & 15) == i) count += c;
+    }
+    if (c < 64) break;
+  }
+  if (count < 1 || count > b.n_seqs || t0 + (lane & 15) >= b.m) return kNoToken;
+  const int a = b.adapter[count - 1];
+  return a >= 0 && a < b.n_adapters ? a : kNoAdapter;
+}
+
+// the first of the adapters (or kNoAdapter) among the lanes of `left`, which loses its lanes
+GPTQ_DEV int next_adapter(int id, uint64_t& left) {
+  const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+  left &= ~__ballot(id == a);
+  return a;
+}
+
+// eight 16-bit values at p; VEC: 16-byte loads, all eight or none
+template <bool VEC> GPTQ_DEV uint4 load_chunk(const uint16_t* p, int have) {
+  if constexpr (VEC) return have > 0 ? *reinterpret_cast<const uint4*>(p) : make_uint4(0u, 0u, 0u, 0u);
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    w[e] = (2 * e < have ? p[2 * e] : 0u) | (2 * e + 1 < have ? (uint32_t)p[2 * e + 1] << 16 : 0u);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+struct LowArgs {
+  const uint16_t* X;      // [m x K], pitch ldx
+  const uint16_t* A;      // [adapters][rank x K], row pitch lda
+  int64_t ldx, lda, set;  // set: from one adapter's matrix to the next's
+  int K, rank, slice_k;   // a workgroup's share of k, a multiple of 64 kLowWaves
+  float* part;            // [slice][m][16 NB]
+  int32_t* ids;           // [m], written by the first slice
+};
+
+// Partial sums of X A^T: 16 MT tokens by all ranks (16 NB) a workgroup, k dealt to
+// its waves by 64 and joined through LDS in order.  A is the first operand, so that
+// a lane has four neighbouring ranks of one token.  blockIdx.z takes every
+// gridDim.z-th adapter of the tile: in a decode step each token may have its own,
+// and one after the other they would be a chain of memory latencies.
+template <typename T, int NB, int MT, bool VEC>
+__global__ __launch_bounds__(64 * kLowWaves) void lora_low_kernel(LowArgs p, LoraBatch batch) {
+  typedef typename T16<T>::v8 v8;
+  __shared__ f32x4_t red[kLowWaves][MT][NB][64];
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t0 = (int64_t)blockIdx.x * (16 * MT);
+  int id[MT];
+  const uint16_t* x[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    id[j] = adapter_of(batch, t0 + 16 * j);
+    x[j] = p.X + min(t0 + 16 * j + i, batch.m - 1) * p.ldx;
+    if (blockIdx.y == 0 && blockIdx.z == 0 && wave == 0 && lane < 16 && t0 + 16 * j + i < batch.m) p.ids[t0 + 16 * j + i] = id[j];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) red[wave][j][n][lane] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  const int k_lo = blockIdx.y * p.slice_k, k_hi = min(k_lo + p.slice_k, p.K);
+  uint64_t left[MT];
+  bool mine[MT];           // this workgroup writes the lane's token
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    left[j] = __ballot(lane < 16 && id[j] >= 0);
+    mine[j] = id[j] < 0 && blockIdx.z == 0;
+  }
+  for (int n_set = 0;; ++n_set) {
+    int a = -1;
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+      if (a < 0 && left[j]) a = __builtin_amdgcn_readlane(id[j], __builtin_ctzll(left[j]));
+    if (a < 0) break;
+    bool some[MT];
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      const uint64_t same = __ballot(lane < 16 && id[j] == a);
+      some[j] = same != 0;
+      left[j] &= ~same;
+    }
+    if (n_set % gridDim.z != blockIdx.z) continue;
+    const uint16_t* A = p.A + a * p.set;
+    f32x4_t acc[MT][NB];
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int n = 0; n < NB; ++n) acc[j][n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    uint4 xv[MT][2], av[NB][2];
+    auto load = [&](int k0) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = k0 + 32 * h + 8 * g, have = k_hi - k;
+#pragma unroll
+        for (int j = 0; j < MT; ++j) xv[j][h] = load_chunk<VEC>(x[j] + k, have);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          const int r = 16 * n + i;
+          av[n][h] = load_chunk<VEC>(A + r * p.lda + k, r < p.rank ? have : 0);
+        }
+      }
+    };
+    int k0 = k_lo + 64 * wave;
+    if (k0 < k_hi) load(k0);
+    for (; k0 < k_hi; k0 += 64 * kLowWaves) {
+      v8 xo[MT][2], ao[NB][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int j = 0; j < MT; ++j) xo[j][h] = __builtin_bit_cast(v8, xv[j][h]);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) ao[n][h] = __builtin_bit_cast(v8, av[n][h]);
+      }
+      if (k0 + 64 * kLowWaves < k_hi) load(k0 + 64 * kLowWaves);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+          for (int n = 0; n < NB; ++n) acc[j][n] = T16<T>::mfma16(ao[n][h], xo[j][h], acc[j][n]);
+    }
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+      if (some[j] && id[j] == a) {
+        mine[j] = true;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) red[wave][j][n][lane] = acc[j][n];
+      }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < MT * NB; ++u) {
+    const int j = u / NB, n = u % NB;
+    if (u % kLowWaves != wave || !mine[j]) continue;
+    f32x4_t s = red[0][j][n][lane];
+#pragma unroll
+    for (int w = 1; w < kLowWaves; ++w) s += red[w][j][n][lane];
+    const int64_t t = t0 + 16 * j + i;
+    if (t < batch.m) *reinterpret_cast<f32x4_t*>(p.part + ((int64_t)blockIdx.y * batch.m + t) * (16 * NB) + 16 * n + 4 * g) = s;
+  }
+}
+
+struct UpArgs {
+  const float* part;      // [slices][m][16 NB]
+  const int32_t* ids;
+  const uint16_t* B;      // [adapters][d x rank], row pitch ldb
+  const float* scale;
+  const void* R;          // [m x d] of y_type, or NULL
+  void* Y;                // or NULL: only S
+  float* S;               // [m x rank], or NULL
+  int64_t ldb, set, ldr, ldy;
+  int64_t m;
+  int slices, rank, d;
+  int y_type;
+  bool vec;               // rows of Y and R allow 16-byte accesses
+  int blocks;             // token blocks of a workgroup
+  int unit_waves;         // waves that share a channel group's units; the others take further channel groups
+};
+
+// Y = R + scale S B^T: a wave has 64 channels; a unit is a block of 16 tokens and
+// one of the adapters in it.  In a run of one adapter B's operands stay in
+// registers; in a decode step, where every unit has its own, the waves share one
+// channel group's units.  Row 4 g + r of matrix block b stands for channel 16 g + 4 b
+// + r, so a lane ends with 16 neighbouring channels of one token.
+// s comes in two pieces of T below its row's power of two (fp16 has not the
+// range): k of the products is [hi ranks | lo ranks].
+template <typename T, int NB, bool VEC>
+__global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(UpArgs p) {
+  typedef typename T16<T>::v8 v8;
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int share = wave % p.unit_waves;
+  const int per = kUpWaves / p.unit_waves, groups = ((p.d + 63) / 64 + per - 1) / per;
+  const int64_t tile = blockIdx.x / groups;
+  const int c0 = 64 * (int)((blockIdx.x - tile * groups) * per + wave / p.unit_waves);
+  if (c0 >= p.d) return;
+  const bool writes_s = p.S && c0 == 0 && share == 0;
+  v8 bo[4][NB];
+  float scale = 0.0f;
+  int have_set = kNoToken, unit = 0;
+  for (int tb = 0; tb < p.blocks; ++tb) {
+    const int64_t t = (tile * p.blocks + tb) * 16 + i;
+    if (t - i >= p.m) break;
+    const int id = t < p.m ? p.ids[t] : kNoToken;
+    uint64_t left = __ballot(id != kNoToken && lane < 16);
+    bool have_s = false;
+    v8 so[NB];
+    float row = 1.0f;
+    // s of this lane's token, ranks 8 q .. 8 q + 7 of the chunks it needs, in its piece
+    auto make_s = [&]() {
+      have_s = true;
+      float s[NB][8], top = 0.0f;
+#pragma unroll
+      for (int kb = 0; kb < NB; ++kb) {
+        const int rc = (4 * kb + g) % (2 * NB);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[kb][e] = 0.0f;
+        if (id != kNoToken) {
+          for (int z = 0; z < p.slices; ++z) {
+            const f32x4_t* from = reinterpret_cast<const f32x4_t*>(p.part + ((int64_t)z * p.m + t) * (16 * NB) + 8 * rc);
+            const f32x4_t lo = from[0], hi = from[1];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              s[kb][e] += lo[e];
+              s[kb][4 + e] += hi[e];
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(s[kb][e]));
+      }
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      int ex = (int)(__builtin_bit_cast(uint32_t, top) >> 23);
+      ex = ex == 255 || ex == 0 ? 127 : min(ex, 252);
+      row = __builtin_bit_cast(float, (uint32_t)ex << 23);
+      const float inv = __builtin_bit_cast(float, (uint32_t)(254 - ex) << 23);
+#pragma unroll
+      for (int kb = 0; kb < NB; ++kb) {
+        const bool low = (4 * kb + g) / (2 * NB) != 0;
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float a0 = s[kb][2 * e] * inv, a1 = s[kb][2 * e + 1] * inv;
+          w[e] = pack2<T>(a0, a1);
+          if (low) {
+            const float h0 = lo16f<T>(w[e]), h1 = hi16f<T>(w[e]);
+            w[e] = pack2<T>(fabsf(h0) < INFINITY ? a0 - h0 : 0.0f, fabsf(h1) < INFINITY ? a1 - h1 : 0.0f);
+          }
+        }
+        so[kb] = __builtin_bit_cast(v8, make_uint4(w[0], w[1], w[2], w[3]));
+        if (writes_s && !low && id != kNoToken) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int r = 8 * ((4 * kb + g) % (2 * NB)) + e;
+            if (r < p.rank) p.S[t * p.rank + r] = s[kb][e];
+          }
+        }
+      }
+    };
+    if (writes_s) make_s();
+    while (p.Y && left) {
+      const int a = next_adapter(id, left);
+      if (unit++ % p.unit_waves != share) continue;
+      if (!have_s) make_s();
+      f32x4_t acc[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) acc[b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      if (a >= 0) {
+        if (a != have_set) {
+          have_set = a;
+          scale = p.scale[a];
+          const uint16_t* B = p.B + a * p.set;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const int c = c0 + 16 * (i >> 2) + 4 * b + (i & 3);
+#pragma unroll
+            for (int kb = 0; kb < NB; ++kb) {
+              const int r = 8 * ((4 * kb + g) % (2 * NB));
+              bo[b][kb] = __builtin_bit_cast(v8, load_chunk<VEC>(B + c * p.ldb + r, c < p.d ? p.rank - r : 0));
+            }
+          }
+        }
+#pragma unroll
+        for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) acc[b] = T16<T>::mfma16(bo[b][kb], so[kb], acc[b]);
+      }
+      if (id != a) continue;
+      const float f = a >= 0 ? scale * row : 0.0f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = c0 + 16 * g + 8 * h, have = p.d - c;
+        if (have <= 0) continue;
+        const bool full = p.vec && have >= 8;
+        float r[8], y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[e] = 0.0f;
+        if (p.R) {
+          if (p.y_type == GPTQ_F32) load_f32<8>(static_cast<const float*>(p.R) + t * p.ldr + c, full, have, r);
+          else if (p.y_type == GPTQ_BF16) load_n<__bf16, 8>(static_cast<const uint16_t*>(p.R) + t * p.ldr + c, full, have, r);
+          else load_n<_Float16, 8>(static_cast<const uint16_t*>(p.R) + t * p.ldr + c, full, have, r);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = a >= 0 ? fmaf(f, acc[2 * h + (e >> 2)][e & 3], r[e]) : r[e];
+        if (p.y_type == GPTQ_F32) store_f32<8>(static_cast<float*>(p.Y) + t * p.ldy + c, full, have, y);
+        else if (p.y_type == GPTQ_BF16) store_n<__bf16, 8>(static_cast<uint16_t*>(p.Y) + t * p.ldy + c, full, have, y);
+        else store_n<_Float16, 8>(static_cast<uint16_t*>(p.Y) + t * p.ldy + c, full, have, y);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- backward
+
+// [n][rows x cols] -> [n][cols x rows], row pitch `pitch` (a multiple of 8, zeros from rows on): 64 x 64 tiles through LDS
+__global__ __launch_bounds__(256) void lora_transpose_kernel(const uint16_t* __restrict__ in, int rows, int cols, int pitch,
+                                                             uint16_t* __restrict__ out) {
+  __shared__ uint16_t tile[64][66];
+  const int64_t set = blockIdx.z;
+  const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
+  const uint16_t* from = in + set * rows * cols;
+  uint16_t* to = out + set * cols * pitch;
+  for (int u = threadIdx.x; u < 64 * 64; u += 256) {
+    const int r = r0 + (u >> 6), c = c0 + (u & 63);
+    tile[u >> 6][u & 63] = r < rows && c < cols ? from[(int64_t)r * cols + c] : (uint16_t)0;
+  }
+  __syncthreads();
+  for (int u = threadIdx.x; u < 64 * 64; u += 256) {
+    const int c = c0 + (u >> 6), r = r0 + (u & 63);
+    if (c < cols && r < pitch) to[(int64_t)c * pitch + r] = tile[u & 63][u >> 6];
+  }
+}
+
+// One of the two products over tokens: dA (X: the inputs, S: dS) or dB (X: dY, S: s)
+struct OuterSide {
+  const uint16_t* X;
+  const float* S;         // [m x rank]
+  int64_t ldx;
+  float* out;             // [adapters][rank x d] or [adapters][d x rank]; with splits the first one's part
+  int64_t split;          // from one split's part to the next's
+  int d, tiles;           // tiles of 128 channels
+  bool vec;
+};
+struct OuterArgs {
+  OuterSide side[2];
+  const int32_t* ids;
+  const float* scale;
+  int64_t m, slice;       // tokens of a split, a multiple of 32
+  int rank;
+};
+
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+// Four rows of 16 channels of 16-bit values become four values of one channel a
+// lane: in each group of 16 lanes, lane l names 8 bytes of row l / 4 (channels 4 (l %
+// 4) ..), and gets channel l of the four rows.
+GPTQ_DEV uint2 read_transposed(uint32_t at) {
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS i16x4_t*)(uintptr_t)at));
+}
+
+// scale sum_t X[t][c] S[t][r] over one adapter's tokens: 128 channels by all ranks
+// a workgroup, 32 tokens a step.  Both operands want the tokens next to each
+// other: X goes to LDS as it lies and is read transposed, S in bf16 pieces (two: 16
+// bits) with tokens innermost.  fp16 channels are two bf16 values exactly.
+template <typename T, int NB>
+__global__ __launch_bounds__(256) void lora_outer_kernel(OuterArgs p) {
+  typedef typename T16<__bf16>::v8 b8;
+  constexpr bool kSplitX = T16<T>::kType == GPTQ_F16;
+  constexpr int kPitch = 40;                         // tokens of a rank's row in LDS: 80 bytes
+  __shared__ __attribute__((aligned(1024))) uint16_t xs[32 * 128];
+  __shared__ __attribute__((aligned(16))) uint16_t ss[2][16 * NB * kPitch];
+  const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const bool is_b = (int)blockIdx.x >= p.side[0].tiles;
+  const OuterSide& o = p.side[is_b];
+  const int c0 = 128 * ((int)blockIdx.x - (is_b ? p.side[0].tiles : 0)), a = blockIdx.z;
+  const int64_t t_lo = blockIdx.y * p.slice, t_hi = min(t_lo + p.slice, p.m);
+  const float scale = p.scale[a];
+  const uint32_t xl = (uint32_t)(uintptr_t)(LDS_AS const char*)(const char*)xs;
+  // 32-byte pairs of chunks of row t sit at pair ^ (t % 4 + 4 (t / 8 % 2)): the rows that a read takes differ in it
+  auto swz = [](int t) { return (t & 3) | ((t >> 1) & 4); };
+  f32x4_t acc[2][NB];
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int n = 0; n < NB; ++n) acc[b][n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int64_t t0 = t_lo; t0 < t_hi; t0 += 32) {
+    const int64_t mine_t = t0 + (lane & 31);
+    const bool mine = mine_t < t_hi && p.ids[mine_t] == a;
+    const uint64_t some = __ballot(mine);
+    if (!some) continue;
+    // another adapter's tokens count as zeros, whatever they hold
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t = (tid >> 4) + 16 * h, ch = tid & 15, c = c0 + 8 * ch;
+      const int have = (some >> t) & 1 ? o.d - c : 0;
+      const uint16_t* x = o.X + (t0 + t) * o.ldx + c;
+      const uint4 v = o.vec && have >= 8 ? load_chunk<true>(x, have) : load_chunk<false>(x, have);
+      *reinterpret_cast<uint4*>(xs + t * 128 + (((ch >> 1) ^ swz(t)) << 4) + 8 * (ch & 1)) = v;
+    }
+    for (int u = tid; u < 32 * 16 * NB; u += 256) {
+      const int t = u / (16 * NB), r = u % (16 * NB);
+      const float v = ((some >> t) & 1) && r < p.rank ? scale * o.S[(t0 + t) * p.rank + r] : 0.0f;
+      const uint16_t hi = bits16<__bf16>(v);
+      const float rest = v - (float)__builtin_bit_cast(__bf16, hi);
+      ss[0][r * kPitch + t] = hi;
+      ss[1][r * kPitch + t] = bits16<__bf16>(fabsf((float)__builtin_bit_cast(__bf16, hi)) < INFINITY ? rest : 0.0f);
+    }
+    __syncthreads();
+    b8 xo[2][kSplitX ? 2 : 1];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      uint32_t w[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int t = 8 * g + 4 * h + (i >> 2), pair = 2 * wave + b;
+        const uint2 v = read_transposed(xl + t * 256 + ((pair ^ swz(t)) << 5) + 8 * (i & 3));
+        w[2 * h] = v.x;
+        w[2 * h + 1] = v.y;
+      }
+      if constexpr (kSplitX) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float f0 = lo16f<_Float16>(w[e]), f1 = hi16f<_Float16>(w[e]);
+          hi[e] = pack2<__bf16>(f0, f1);
+          const float h0 = lo16f<__bf16>(hi[e]), h1 = hi16f<__bf16>(hi[e]);
+          lo[e] = pack2<__bf16>(fabsf(h0) < INFINITY ? f0 - h0 : 0.0f, fabsf(h1) < INFINITY ? f1 - h1 : 0.0f);
+        }
+        xo[b][0] = __builtin_bit_cast(b8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        xo[b][kSplitX ? 1 : 0] = __builtin_bit_cast(b8, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      } else {
+        xo[b][0] = __builtin_bit_cast(b8, make_uint4(w[0], w[1], w[2], w[3]));
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      b8 so[2];
+#pragma unroll
+      for (int z = 0; z < 2; ++z) so[z] = *reinterpret_cast<const b8*>(ss[z] + (16 * n + i) * kPitch + 8 * g);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        auto product = [&](const b8& x, const b8& s) {
+          // dA: rows are channels, so that a lane has four channels of one rank; dB: four ranks of one channel
+          acc[b][n] = is_b ? T16<__bf16>::mfma16(s, x, acc[b][n]) : T16<__bf16>::mfma16(x, s, acc[b][n]);
+        };
+        product(xo[b][0], so[0]);
+        product(xo[b][0], so[1]);
+        if constexpr (kSplitX) {
+          product(xo[b][kSplitX ? 1 : 0], so[0]);
+          product(xo[b][kSplitX ? 1 : 0], so[1]);
+        }
+      }
+    }
+    __syncthreads();
+  }
+  float* out = o.out + blockIdx.y * o.split + (int64_t)a * p.rank * o.d;
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const int c = c0 + 16 * (2 * wave + b) + (is_b ? i : 4 * g), r = 16 * n + (is_b ? 4 * g : i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int ce = is_b ? c : c + e, re = is_b ? r + e : r;
+        if (ce < o.d && re < p.rank) out[is_b ? (int64_t)ce * p.rank + re : (int64_t)re * o.d + ce] = acc[b][n][e];
+      }
+    }
+}
+
+// out = the splits' parts in order
+__global__ __launch_bounds__(256) void lora_join_kernel(const float* __restrict__ part, int64_t split, int splits, int64_t n,
+                                                        float* __restrict__ out) {
+  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < n; u += (int64_t)gridDim.x * 256) {
+    float v = 0.0f;
+    for (int z = 0; z < splits; ++z) v += part[z * split + u];
+    out[u] = v;
+  }
+}
+
+// ---------------------------------------------------------------- host side
+static bool at16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+static int rank_blocks(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
+
+static bool lora_ok(const gptq_lora_set* a) {
+  if (!a || !a->A || !a->B || !a->scale) return false;
+  if (a->n_adapters <= 0 || a->n_adapters > kLoraMaxSets || a->rank <= 0 || a->rank > kLoraMaxRank) return false;
+  if (a->d_in <= 0 || a->d_in > kLoraMaxDim || a->d_out <= 0 || a->d_out > kLoraMaxDim) return false;
+  return ((reinterpret_cast<uintptr_t>(a->A) | reinterpret_cast<uintptr_t>(a->B)) & 1) == 0 && (reinterpret_cast<uintptr_t>(a->scale) & 3) == 0;
+}
+constexpr int64_t kLoraMaxTokens = 1 << 24;
+
+// How X A^T is dealt out: 16 MT tokens a workgroup, k in slices, until there are
+// four workgroups a CU; the adapters of a tile over `shares`.
+struct LowPlan {
+  int mt, tiles, slices, slice_k, shares;
+};
+static bool mixed(int64_t m, int n_seqs) { return m < 16 * (int64_t)n_seqs; }     // a block of tokens has several adapters
+static LowPlan low_plan(int64_t m, int n_seqs, int K, int nb) {
+  LowPlan p;
+  const bool mix = mixed(m, n_seqs);
+  p.mt = mix || m <= 32 ? 1 : nb == 8 ? 2 : 4;
+  p.tiles = (int)((m + 16 * p.mt - 1) / (16 * p.mt));
+  p.shares = mix ? 4 : 1;
+  const int step = 64 * kLowWaves, most = (K + step - 1) / step;
+  const int64_t want = 1024 / ((int64_t)p.tiles * p.shares);
+  int n = (int)std::max<int64_t>(1, std::min<int64_t>(want, std::min(most, 32)));
+  p.slice_k = (most + n - 1) / n * step;
+  p.slices = (K + p.slice_k - 1) / p.slice_k;
+  return p;
+}
+// room for every plan of m tokens, whatever the sequences
+static size_t part_bytes(int64_t m, int K, int nb) {
+  int slices = 1;
+  for (int n_seqs : {1, (int)std::min<int64_t>(m, INT_MAX - 1) / 16 + 1}) slices = std::max(slices, low_plan(m, n_seqs, K, nb).slices);
+  return align_up((size_t)slices * m * 16 * nb * sizeof(float));
+}
+
+template <typename T>
+static int launch_low(const LowPlan& p, int nb, bool vec, const LowArgs& a, const LoraBatch& b, hipStream_t s) {
+  const dim3 grid((unsigned)p.tiles, (unsigned)p.slices, (unsigned)p.shares);
+  auto go = [&]<int NB, int MT>() {
+    if (vec) lora_low_kernel<T, NB, MT, true><<<grid, 64 * kLowWaves, 0, s>>>(a, b);
+    else lora_low_kernel<T, NB, MT, false><<<grid, 64 * kLowWaves, 0, s>>>(a, b);
+  };
+  if (nb == 1) p.mt == 1 ? go.template operator()<1, 1>() : go.template operator()<1, 4>();
+  else if (nb == 2) p.mt == 1 ? go.template operator()<2, 1>() : go.template operator()<2, 4>();
+  else if (nb == 4) p.mt == 1 ? go.template operator()<4, 1>() : go.template operator()<4, 4>();
+  else p.mt == 1 ? go.template operator()<8, 1>() : go.template operator()<8, 2>();
+  GPTQ_LAUNCH_CHECK();
+  return GPTQ_OK;
+}
+
+template <typename T>
+static int launch_up(UpArgs a, int nb, bool mix, hipStream_t s) {
+  a.unit_waves = mix ? kUpWaves : 1;
+  const int per = kUpWaves / a.unit_waves;
+  const int64_t groups = a.Y ? ((a.d + 63) / 64 + per - 1) / per : 1;
+  // as many token blocks a workgroup (B's operands serve them all) as leave two workgroups a CU
+  a.blocks = mix ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(8, (a.m + 15) / 16 * groups / 512));
+  const int64_t tiles = (a.m + 16 * a.blocks - 1) / (16 * a.blocks);
+  if (!a.Y) a.d = 1;
+  const bool vec = at16(a.B) && a.rank % 8 == 0 && a.ldb % 8 == 0 && a.set % 8 == 0;
+  if (tiles * groups > (1 << 24) - 1) return GPTQ_ERR_INVALID_ARG;
+  auto go = [&]<int NB>() {
+    if (vec) lora_up_kernel<T, NB, true><<<(unsigned)(tiles * groups), 64 * kUpWaves, 0, s>>>(a);
+    else lora_up_kernel<T, NB, false><<<(unsigned)(tiles * groups), 64 * kUpWaves, 0, s>>>(a);
+  };
+  if (nb == 1) go.template operator()<1>();
+  else if (nb == 2) go.template operator()<2>();
+  else if (nb == 4) go.template operator()<4>();
+  else go.template operator()<8>();
+  GPTQ_LAUNCH_CHECK();
+  return GPTQ_OK;
+}
+
+static bool is_16(gptq_dtype t) { return t == GPTQ_F16 || t == GPTQ_BF16; }
+static bool elem_at(const void* p, gptq_dtype t) { return (reinterpret_cast<uintptr_t>(p) & (t == GPTQ_F32 ? 3 : 1)) == 0; }
+static bool share_bytes(const void* a, uint64_t na, const void* b, uint64_t nb) {
+  const uint64_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+static bool rows_vec(const void* p, int64_t ld, gptq_dtype t) { return !p || (at16(p) && ld % (t == GPTQ_F32 ? 4 : 8) == 0); }
+
+struct LoraBackLayout {
+  size_t off_part, off_ds, off_at, off_bt, off_outer, total;
+  int nb, splits;
+  int64_t slice, out_pitch;
+};
+static LoraBackLayout lora_back_layout(int64_t m, const gptq_lora_set* a) {
+  LoraBackLayout L;
+  L.nb = rank_blocks(a->rank);
+  const int64_t sets = a->n_adapters, r = a->rank, pitch = (r + 7) & ~7;
+  L.off_part = align_up((size_t)m * 4);
+  L.off_ds = L.off_part + part_bytes(m, a->d_out, L.nb);
+  L.off_at = L.off_ds + align_up((size_t)m * r * 4);
+  L.off_bt = L.off_at + align_up((size_t)sets * a->d_in * pitch * 2);
+  L.off_outer = L.off_bt + align_up((size_t)sets * r * ((a->d_out + 7) & ~7) * 2);
+  // splits of the tokens until there are four workgroups a CU, 64 tokens each at least
+  const int64_t tiles = ((a->d_in + 127) / 128 + (a->d_out + 127) / 128) * sets;
+  int64_t n = std::max<int64_t>(1, std::min<int64_t>({1024 / tiles, (m + 63) / 64, 16}));
+  L.slice = ((m + n - 1) / n + 31) / 32 * 32;
+  L.splits = (int)((m + L.slice - 1) / L.slice);
+  L.out_pitch = sets * r * (a->d_in + a->d_out);
+  L.total = L.off_outer + (L.splits > 1 ? align_up((size_t)L.splits * L.out_pitch * 4) : 0);
+  return L;
+}
+
+template <typename T>
+static int lora_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, const float* S, const gptq_lora_set* a,
+                         const LoraBatch& b, const void* R, int64_t ldr, void* dX, gptq_dtype x_dtype, int64_t lddx, float* dA,
+                         float* dB, char* base, hipStream_t s) {
+  const LoraBackLayout L = lora_back_layout(b.m, a);
+  const int sets = a->n_adapters, r = a->rank, pitch = (r + 7) & ~7, kp = (a->d_out + 7) & ~7;
+  int32_t* ids = reinterpret_cast<int32_t*>(base);
+  float *part = reinterpret_cast<float*>(base + L.off_part), *ds = reinterpret_cast<float*>(base + L.off_ds);
+  uint16_t *at = reinterpret_cast<uint16_t*>(base + L.off_at), *bt = reinterpret_cast<uint16_t*>(base + L.off_bt);
+  const uint16_t *A = static_cast<const uint16_t*>(a->A), *B = static_cast<const uint16_t*>(a->B);
+  lora_transpose_kernel<<<dim3((unsigned)((r + 63) / 64), (unsigned)((kp + 63) / 64), (unsigned)sets), 256, 0, s>>>(B, a->d_out, r, kp, bt);
+  GPTQ_LAUNCH_CHECK();
+  if (dX) {
+    lora_transpose_kernel<<<dim3((unsigned)((a->d_in + 63) / 64), (unsigned)((pitch + 63) / 64), (unsigned)sets), 256, 0, s>>>(A, r, a->d_in,
+                                                                                                                         pitch, at);
+    GPTQ_LAUNCH_CHECK();
+  }
+  const LowPlan lp = low_plan(b.m, b.n_seqs, a->d_out, L.nb);
+  const bool vec = rows_vec(dY, lddy, GPTQ_BF16) && a->d_out % 8 == 0;
+  int st = launch_low<T>(lp, L.nb, vec, LowArgs{static_cast<const uint16_t*>(dY), bt, lddy, kp, (int64_t)r * kp, a->d_out, r, lp.slice_k, part, ids}, b, s);
+  if (st != GPTQ_OK) return st;
+  UpArgs u{part, ids, at, a->scale, R, dX, dA ? ds : nullptr, pitch, (int64_t)a->d_in * pitch, ldr, lddx, b.m, lp.slices, r, a->d_in, x_dtype,
+           rows_vec(R, ldr, x_dtype) && rows_vec(dX, lddx, x_dtype), 1, 1};
+  if (dX || dA) {
+    st = launch_up<T>(u, L.nb, mixed(b.m, b.n_seqs), s);
+    if (st != GPTQ_OK) return st;
+  }
+  if (!dA && !dB) return GPTQ_OK;
+  float* outer = reinterpret_cast<float*>(base + L.off_outer);
+  const int64_t na = (int64_t)sets * r * a->d_in, nb = (int64_t)sets * r * a->d_out;
+  const bool split = L.splits > 1;
+  OuterArgs o{};
+  o.side[0] = OuterSide{static_cast<const uint16_t*>(X), ds, ldx, split ? outer : dA, split ? L.out_pitch : 0, a->d_in,
+                        dA ? (a->d_in + 127) / 128 : 0, rows_vec(X, ldx, GPTQ_BF16)};
+  o.side[1] = OuterSide{static_cast<const uint16_t*>(dY), S, lddy, split ? outer + na : dB, split ? L.out_pitch : 0, a->d_out,
+                        dB ? (a->d_out + 127) / 128 : 0, rows_vec(dY, lddy, GPTQ_BF16)};
+  o.ids = ids;
+  o.scale = a->scale;
+  o.m = b.m;
+  o.slice = L.slice;
+  o.rank = r;
+  const dim3 grid((unsigned)(o.side[0].tiles + o.side[1].tiles), (unsigned)L.splits, (unsigned)sets);
+  if (L.nb == 1) lora_outer_kernel<T, 1><<<grid, 256, 0, s>>>(o);
+  else if (L.nb == 2) lora_outer_kernel<T, 2><<<grid, 256, 0, s>>>(o);
+  else if (L.nb == 4) lora_outer_kernel<T, 4><<<grid, 256, 0, s>>>(o);
+  else lora_outer_kernel<T, 8><<<grid, 256, 0, s>>>(o);
+  GPTQ_LAUNCH_CHECK();
+  if (split) {
+    auto join = [&](const float* from, int64_t n, float* to) {
+      lora_join_kernel<<<(unsigned)std::min<int64_t>((n + 255) / 256, 4096), 256, 0, s>>>(from, L.out_pitch, L.splits, n, to);
+    };
+    if (dA) join(outer, na, dA);
+    if (dB) join(outer + na, nb, dB);
+    GPTQ_LAUNCH_CHECK();
+  }
+  return GPTQ_OK;
+}
+
+}  // namespace gptq
+
+using namespace gptq;
+
+extern "C" size_t gptq_lora_workspace_size(int64_t m, const gptq_lora_set* a) {
+  if (m <= 0 || m > kLoraMaxTokens || !lora_ok(a)) return 0;
+  return align_up((size_t)m * 4) + part_bytes(m, a->d_in, rank_blocks(a->rank));
+}
+
+extern "C" int gptq_lora(const void* X, gptq_dtype x_dtype, int64_t m, int64_t ldx, const gptq_lora_set* a, const int32_t* q_start,
+                         const int32_t* adapter, int32_t n_seqs, const void* R, int64_t ldr, void* Y, gptq_dtype y_dtype, int64_t ldy,
+                         float* S, void* ws, size_t ws_bytes, hipStream_t s) {
+  if (!lora_ok(a) || m < 0 || m > kLoraMaxTokens || n_seqs <= 0 || n_seqs == INT_MAX || !is_16(x_dtype)) return GPTQ_ERR_INVALID_ARG;
+  if (y_dtype != GPTQ_F32 && !is_16(y_dtype)) return GPTQ_ERR_INVALID_ARG;
+  if (m == 0) return GPTQ_OK;
+  if (!X || !Y || !q_start || !adapter || ldx < a->d_in || ldy < a->d_out || (R && ldr < a->d_out)) return GPTQ_ERR_INVALID_ARG;
+  if (!elem_at(X, x_dtype) || !elem_at(R, y_dtype) || !elem_at(Y, y_dtype) || !elem_at(S, GPTQ_F32) || !elem_at(q_start, GPTQ_F32) ||
+      !elem_at(adapter, GPTQ_F32)) return GPTQ_ERR_INVALID_ARG;
+  const uint64_t e = y_dtype == GPTQ_F32 ? 4 : 2, yb = rows_bytes(m, ldy, a->d_out, e), xb = rows_bytes(m, ldx, a->d_in, 2), sb = (uint64_t)m * a->rank * 4;
+  if (share_bytes(Y, yb, X, xb) || share_bytes(Y, yb, S, sb) || share_bytes(S, sb, X, xb)) return GPTQ_ERR_INVALID_ARG;
+  if (R && !(R == Y && ldr == ldy) && share_bytes(Y, yb, R, rows_bytes(m, ldr, a->d_out, e))) return GPTQ_ERR_INVALID_ARG;
+  if (R && share_bytes(S, sb, R, rows_bytes(m, ldr, a->d_out, e))) return GPTQ_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < gptq_lora_workspace_size(m, a) || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return GPTQ_ERR_WORKSPACE;
+  const int nb = rank_blocks(a->rank);
+  const LowPlan lp = low_plan(m, n_seqs, a->d_in, nb);
+  const LoraBatch b{q_start, adapter, n_seqs, a->n_adapters, m};
+  char* base = static_cast<char*>(ws);
+  int32_t* ids = reinterpret_cast<int32_t*>(base);
+  float* part = reinterpret_cast<float*>(base + align_up((size_t)m * 4));
+  const bool vec = rows_vec(X, ldx, x_dtype) && at16(a->A) && a->d_in % 8 == 0;
+  const LowArgs low{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(a->A), ldx, a->d_in, (int64_t)a->rank * a->d_in, a->d_in,
+                    a->rank, lp.slice_k, part, ids};
+  const UpArgs up{part, ids, static_cast<const uint16_t*>(a->B), a->scale, R, Y, S, a->rank, (int64_t)a->d_out * a->rank, ldr, ldy, m,
+                  lp.slices, a->rank, a->d_out, y_dtype, rows_vec(R, ldr, y_dtype) && rows_vec(Y, ldy, y_dtype), 1, 1};
+  const bool mix = mixed(m, n_seqs);
+  if (x_dtype == GPTQ_BF16) {
+    const int st = launch_low<__bf16>(lp, nb, vec, low, b, s);
+    return st != GPTQ_OK ? st : launch_up<__bf16>(up, nb, mix, s);
+  }
+  const int st = launch_low<_Float16>(lp, nb, vec, low, b, s);
+  return st != GPTQ_OK ? st : launch_up<_Float16>(up, nb, mix, s);
+}
+
+extern "C" size_t gptq_lora_backward_workspace_size(int64_t m, const gptq_lora_set* a) {
+  if (m <= 0 || m > kLoraMaxTokens || !lora_ok(a)) return 0;
+  return lora_back_layout(m, a).total;
+}
+
+extern "C" int gptq_lora_backward(const void* dY, gptq_dtype dtype, int64_t m, int64_t lddy, const void* X, int64_t ldx, const float* S,
+                                  const gptq_lora_set* a, const int32_t* q_start, const int32_t* adapter, int32_t n_seqs,
+                                  const void* R, int64_t ldr, void* dX, gptq_dtype x_dtype, int64_t lddx, float* dA, float* dB,
+                                  void* ws, size_t ws_bytes, hipStream_t s) {
+  if (!lora_ok(a) || m < 0 || m > kLoraMaxTokens || n_seqs <= 0 || n_seqs == INT_MAX || !is_16(dtype)) return GPTQ_ERR_INVALID_ARG;
+  if (x_dtype != GPTQ_F32 && !is_16(x_dtype)) return GPTQ_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(dA) | reinterpret_cast<uintptr_t>(dB)) & 3) return GPTQ_ERR_INVALID_ARG;
+  const uint64_t na = (uint64_t)a->n_adapters * a->rank * a->d_in * 4, nb = (uint64_t)a->n_adapters * a->rank * a->d_out * 4;
+  if (share_bytes(dA, na, dB, nb)) return GPTQ_ERR_INVALID_ARG;
+  if (m == 0) {
+    // sums over no tokens
+    for (auto [out, n] : {std::pair{dA, na / 4}, std::pair{dB, nb / 4}}) {
+      if (!out) continue;
+      lora_join_kernel<<<(unsigned)std::min<uint64_t>((n + 255) / 256, 4096), 256, 0, s>>>(nullptr, 0, 0, n, out);
+      GPTQ_LAUNCH_CHECK();
+    }
+    return GPTQ_OK;
+  }
+  if (!dY || !q_start || !adapter || (!dX && !dA && !dB) || (R && !dX) || (dA && !X) || (dB && !S)) return GPTQ_ERR_INVALID_ARG;
+  if (lddy < a->d_out || (dA && ldx < a->d_in) || (dX && lddx < a->d_in) || (R && ldr < a->d_in)) return GPTQ_ERR_INVALID_ARG;
+  if (!elem_at(dY, dtype) || !elem_at(X, dtype) || !elem_at(R, x_dtype) || !elem_at(dX, x_dtype) || !elem_at(S, GPTQ_F32) ||
+      !elem_at(q_start, GPTQ_F32) || !elem_at(adapter, GPTQ_F32)) return GPTQ_ERR_INVALID_ARG;
+  const uint64_t e = x_dtype == GPTQ_F32 ? 4 : 2, dxb = rows_bytes(m, lddx, a->d_in, e), dyb = rows_bytes(m, lddy, a->d_out, 2);
+  const uint64_t xb = dA ? rows_bytes(m, ldx, a->d_in, 2) : 0, sb = (uint64_t)m * a->rank * 4;
+  const struct {
+    const void* p;
+    uint64_t n;
+  } outs[] = {{dX, dxb}, {dA, na}, {dB, nb}}, ins[] = {{dY, dyb}, {dA ? X : nullptr, xb}, {dB ? S : nullptr, sb}};
+  for (const auto& o : outs)
+    for (const auto& i : ins)
+      if (share_bytes(o.p, o.n, i.p, i.n)) return GPTQ_ERR_INVALID_ARG;
+  if (share_bytes(dX, dxb, dA, na) || share_bytes(dX, dxb, dB, nb)) return GPTQ_ERR_INVALID_ARG;
+  if (R) {
+    const uint64_t rb = rows_bytes(m, ldr, a->d_in, e);
+    if (!(R == dX && ldr == lddx) && share_bytes(dX, dxb, R, rb)) return GPTQ_ERR_INVALID_ARG;
+    if (share_bytes(dA, na, R, rb) || share_bytes(dB, nb, R, rb)) return GPTQ_ERR_INVALID_ARG;
+  }
+  if (!ws || ws_bytes < lora_back_layout(m, a).total || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return GPTQ_ERR_WORKSPACE;
+  const LoraBatch b{q_start, adapter, n_seqs, a->n_adapters, m};
+  char* base = static_cast<char*>(ws);
+  if (dtype == GPTQ_BF16) return lora_backward<__bf16>(dY, lddy, X, ldx, S, a, b, R, ldr, dX, x_dtype, lddx, dA, dB, base, s);
+  return lora_backward<_Float16>(dY, lddy, X, ldx, S, a, b, R, ldr, dX, x_dtype, lddx, dA, dB, base, s);
+}

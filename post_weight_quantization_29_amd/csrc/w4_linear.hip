@@ -480,8 +480,8 @@ __global__ __launch_bounds__(256) void w4_dense_kernel(W4Dev wa, W4Dev wb, int d
   }
 }
 
-// The transposed 16-bit weights: out[channel c][k], row pitch 2 Fp, k = r for
-// the gate's row r and Fp + r for the up's; zeros from d_out to Fp.  Column q
+// The transposed 16-bit weights: out[channel c][k], row pitch Fp for each matrix, k = r for
+// the first's row r and Fp + r for the second's; zeros from d_out to Fp.  Column q
 // of the packed layer goes to row perm[q].  A workgroup turns 64 rows x 16
 // words (128 columns) through LDS, two rows to a 4-byte write: 128-byte pieces
 // out.  A column's eight 16-byte chunks (eight rows each) sit at chunk ^ (column
@@ -521,7 +521,7 @@ __global__ __launch_bounds__(256) void w4_dense_t_kernel(W4Dev wa, W4Dev wb, int
       const int cl = (tid >> 3) + 32 * i, c = 128 * blockIdx.x + cl, k = r0 + 8 * (tid & 7);
       if (c < d_in && k < Fp) {
         const int ch = perm ? min(max(perm[c], 0), d_in - 1) : c;
-        *reinterpret_cast<uint4*>(out + (size_t)ch * 2 * Fp + (size_t)blockIdx.z * Fp + k) =
+        *reinterpret_cast<uint4*>(out + ((size_t)ch * gridDim.z + blockIdx.z) * Fp + k) =
             *reinterpret_cast<const uint4*>(tile + cl * 64 + (((tid & 7) ^ ((cl >> 3) & 7)) << 3));
       }
     }
@@ -576,19 +576,20 @@ static unsigned grid_rows(int64_t rows) { return (unsigned)std::min<int64_t>(row
 
 static size_t x_copy_bytes(int64_t m, int d_in) { return align_up((size_t)m * pad_k(d_in) * 2); }
 
-static int order_x(const void* X, int64_t ldx, int64_t m, const gptq_w4_weight* w, uint16_t* out, hipStream_t s) {
-  const int Kp = pad_k(w->d_in);
-  if (w->perm && w->d_in <= kGatherMax) {
+// X's rows in the order perm (NULL: as they are), padded to whole stages
+static int order_x(const void* X, int64_t ldx, int64_t m, int d_in, const int32_t* perm, uint16_t* out, hipStream_t s) {
+  const int Kp = pad_k(d_in);
+  if (perm && d_in <= kGatherMax) {
     const bool vec = aligned16(X) && ldx % 8 == 0;
     // every share of a row loads all of it: as many as fill the chip
     const int64_t shares = std::min<int64_t>(std::max<int64_t>(512 / m, 1), (Kp / 8 + 255) / 256);
-    x_gather_kernel<<<dim3((unsigned)shares, (unsigned)std::min<int64_t>(m, 4096)), 256, (size_t)w->d_in * 2, s>>>(
-        static_cast<const uint16_t*>(X), ldx, m, w->d_in, w->perm, Kp, vec, aligned16(w->perm), out);
+    x_gather_kernel<<<dim3((unsigned)shares, (unsigned)std::min<int64_t>(m, 4096)), 256, (size_t)d_in * 2, s>>>(
+        static_cast<const uint16_t*>(X), ldx, m, d_in, perm, Kp, vec, aligned16(perm), out);
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
   }
   x_order_kernel<<<dim3((unsigned)((Kp / 8 + 255) / 256), grid_rows(m)), 256, 0, s>>>(
-      static_cast<const uint16_t*>(X), ldx, m, w->d_in, w->perm, Kp, out);
+      static_cast<const uint16_t*>(X), ldx, m, d_in, perm, Kp, out);
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
 }
@@ -772,7 +773,7 @@ static int forward(const void* X, int64_t ldx, int64_t m, const gptq_w4_weight* 
   const uint16_t* x = static_cast<const uint16_t*>(X);
   if (copies_x(X, ldx, m, wa, wb)) {
     uint16_t* xc = reinterpret_cast<uint16_t*>(base);
-    const int st = order_x(X, ldx, m, wa, xc, s);
+    const int st = order_x(X, ldx, m, wa->d_in, wa->perm, xc, s);
     if (st != GPTQ_OK) return st;
     x = xc;
     ldx = pad_k(wa->d_in);
@@ -855,6 +856,40 @@ static int backward(const void* dM, const void* G, const void* U, int64_t m, con
   return launch_gemm16<T>(Gemm16Args{a0, a1, L.Fp, wt, 2 * L.Fp, m, d, L.Fp / kGk, 2 * L.Fp / kGk}, epi, base + L.off_part, s);
 }
 
+struct LinearBackLayout {
+  size_t off_y, off_part, total;
+  int Fp;
+};
+static LinearBackLayout linear_back_layout(int64_t m, const gptq_w4_weight* w) {
+  LinearBackLayout L;
+  L.Fp = pad_k(w->d_out);
+  L.off_y = align_up((size_t)w->d_in * L.Fp * 2);
+  L.off_part = L.off_y + align_up((size_t)m * L.Fp * 2);
+  L.total = L.off_part + gemm_plan(m, w->d_in, L.Fp / kGk).bytes;
+  return L;
+}
+
+// dX = dY W + R: the product takes dY from where it is if its rows fit its stages
+template <typename T>
+static int linear_backward(const void* dY, int64_t lddy, int64_t m, const gptq_w4_weight* w, const LinearEpi<T>& epi, void* ws,
+                           hipStream_t s) {
+  const LinearBackLayout L = linear_back_layout(m, w);
+  char* base = static_cast<char*>(ws);
+  uint16_t* wt = reinterpret_cast<uint16_t*>(base);
+  const uint16_t* a = static_cast<const uint16_t*>(dY);
+  if (L.Fp != w->d_out || !aligned16(dY) || lddy % 8 != 0 || lddy * 2 > kMaxRowBytes) {
+    uint16_t* c = reinterpret_cast<uint16_t*>(base + L.off_y);
+    const int st = order_x(dY, lddy, m, w->d_out, nullptr, c, s);
+    if (st != GPTQ_OK) return st;
+    a = c;
+    lddy = L.Fp;
+  }
+  w4_dense_t_kernel<T><<<dim3((unsigned)((w->d_in + 127) / 128), grid_rows((L.Fp + 63) / 64), 1), 256, 0, s>>>(
+      dev_of(w), dev_of(w), w->d_out, w->d_in, w4_group(w), w->n_groups, w->perm, L.Fp, wt);
+  GPTQ_LAUNCH_CHECK();
+  return launch_gemm16<T>(Gemm16Args{a, a, lddy, wt, L.Fp, m, w->d_in, L.Fp / kGk, L.Fp / kGk}, epi, base + L.off_part, s);
+}
+
 }  // namespace gptq
 
 using namespace gptq;
@@ -924,4 +959,29 @@ extern "C" int gptq_w4_gated_backward(const void* dM, const void* G, const void*
   if (!ws || ws_bytes < back_layout(m, gate).total || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return GPTQ_ERR_WORKSPACE;
   if (dtype == GPTQ_BF16) return backward<__bf16>(dM, G, U, m, gate, up, act, dG, dU, dX, ws, s);
   return backward<_Float16>(dM, G, U, m, gate, up, act, dG, dU, dX, ws, s);
+}
+
+extern "C" size_t gptq_w4_linear_backward_workspace_size(int64_t m, const gptq_w4_weight* w) {
+  if (m <= 0 || m > INT_MAX || !w4_ok(w) || w->d_out > kW4MaxCols) return 0;
+  return linear_back_layout(m, w).total;
+}
+
+extern "C" int gptq_w4_linear_backward(const void* dY, gptq_dtype dtype, int64_t m, int64_t lddy, const gptq_w4_weight* w,
+                                       const void* R, int64_t ldr, void* dX, gptq_dtype x_dtype, int64_t lddx, void* ws,
+                                       size_t ws_bytes, hipStream_t s) {
+  if (!w4_ok(w) || w->d_out > kW4MaxCols || m < 0 || m > INT_MAX || !is16(dtype)) return GPTQ_ERR_INVALID_ARG;
+  if (x_dtype != GPTQ_F32 && !is16(x_dtype)) return GPTQ_ERR_INVALID_ARG;
+  if (m == 0) return GPTQ_OK;
+  if (!dY || !dX || lddy < w->d_out || lddx < w->d_in || (R && ldr < w->d_in)) return GPTQ_ERR_INVALID_ARG;
+  if (!elem_ok(dY, dtype) || !elem_ok(R, x_dtype) || !elem_ok(dX, x_dtype)) return GPTQ_ERR_INVALID_ARG;
+  const int64_t xe = x_dtype == GPTQ_F32 ? 4 : 2;
+  const int64_t xb = rows_bytes(m, lddx, w->d_in, xe);
+  if (overlap(dX, xb, dY, rows_bytes(m, lddy, w->d_out, 2))) return GPTQ_ERR_INVALID_ARG;
+  if (R && !(R == dX && ldr == lddx) && overlap(dX, xb, R, rows_bytes(m, ldr, w->d_in, xe))) return GPTQ_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < linear_back_layout(m, w).total || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return GPTQ_ERR_WORKSPACE;
+  const int64_t step = x_dtype == GPTQ_F32 ? 4 : 8;
+  const bool vec = aligned16(dX) && (lddx % step) == 0 && (!R || (aligned16(R) && (ldr % step) == 0));
+  if (dtype == GPTQ_BF16)
+    return linear_backward<__bf16>(dY, lddy, m, w, LinearEpi<__bf16>{nullptr, R, dX, ldr, lddx, w->d_in, GPTQ_ACT_NONE, x_dtype, vec}, ws, s);
+  return linear_backward<_Float16>(dY, lddy, m, w, LinearEpi<_Float16>{nullptr, R, dX, ldr, lddx, w->d_in, GPTQ_ACT_NONE, x_dtype, vec}, ws, s);
 }

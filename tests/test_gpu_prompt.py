@@ -1,0 +1,241 @@
+"""GPU tests of attention over whole prompts against float64, forward and backward."""
+from __future__ import annotations
+
+import pytest
+
+torch = pytest.importorskip("torch")
+import block_ops_ref as R  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def P():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    import post_weight_quantization_29_amd as P
+    P.lib()
+    return P
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def rand(shape, dtype, seed, std=1.0):
+    return (torch.randn(shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda") * std).to(dtype)
+
+
+def inputs(T, H, n_kv, hd, dtype, seed=1, std=1.0):
+    """Queries, keys and values of one fused row."""
+    row = rand((T, H + 2 * n_kv, hd), dtype, seed, std)
+    return row[:, :H], row[:, H:H + n_kv], row[:, H + n_kv:]
+
+
+def forward(P, Q, K, V, start, max_len, scale=None):
+    T, H, hd = Q.shape
+    out, lse = torch.full((T, H, hd), 7.0, dtype=Q.dtype, device="cuda"), torch.full((T, H), 7.0, device="cuda")
+    P.gptq_prompt_attention(Q, K, V, i32(start), max_len, out, lse=lse, scale=scale)
+    return out, lse
+
+
+def backward(P, dO, Q, K, V, out, lse, start, max_len, scale=None):
+    row = torch.full((Q.shape[0], Q.shape[1] + 2 * K.shape[1], Q.shape[2]), 7.0, dtype=Q.dtype, device="cuda")
+    H, n_kv = Q.shape[1], K.shape[1]
+    d = row[:, :H], row[:, H:H + n_kv], row[:, H + n_kv:]
+    P.gptq_prompt_attention_backward(dO, Q, K, V, out, lse, i32(start), max_len, *d, scale=scale)
+    return d
+
+
+def check(P, lens, H, n_kv, hd, dtype, scale=None, lead=0, tail=1, max_len=None, std=1.0, dstd=0.1):
+    start = [lead]
+    for n in lens:
+        start.append(start[-1] + n)
+    T = start[-1] + tail
+    most = max(max(lens), 1) if max_len is None else max_len
+    Q, K, V = inputs(T, H, n_kv, hd, dtype, std=std)
+    sc = hd ** -0.5 if scale is None else scale
+    out, lse = forward(P, Q, K, V, start, most, scale)
+    ro, rl, eo, el, live = R.prompt64(Q, K, V, start, sc, most)
+    R.within(out[live], ro[live], eo[live], "out")
+    R.within(lse[live], rl[live], el[live], "lse")
+    assert bool((out[~live] == 7).all()) and bool((lse[~live] == 7).all())
+    plain = torch.full_like(out, 7.0)
+    P.gptq_prompt_attention(Q, K, V, i32(start), most, plain, scale=scale)
+    assert torch.equal(plain, out)
+    dO = rand((T, H, hd), dtype, 9, dstd)
+    got = backward(P, dO, Q, K, V, out, lse, start, most, scale)
+    ref = R.prompt_backward64(dO, Q, K, V, out, lse, start, sc, most)
+    for x, name in zip(got, ("dq", "dk", "dv")):
+        R.within(x[live], ref[name][0][live], ref[name][1][live], name)
+        assert bool((x[~live] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("n", [1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 191, 193, 300])
+def test_lengths(P, dtype, hd, n):
+    check(P, [n], 2, 1, hd, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("H,n_kv", [(1, 1), (3, 3), (6, 2), (8, 1), (10, 2), (12, 4)])
+def test_heads(P, dtype, hd, H, n_kv):
+    check(P, [70, 140], H, n_kv, hd, dtype)
+
+
+@pytest.mark.parametrize("lens,lead,tail", [([1] * 70, 0, 0), ([0, 5, 0, 0, 130, 1, 0], 3, 4), ([0] * 80 + [40] + [0] * 80, 1, 0),
+                                            ([200, 1, 64, 128, 17], 0, 2), ([0], 2, 3), (list(range(1, 100)), 0, 0)])
+def test_batches(P, lens, lead, tail):
+    check(P, lens, 4, 2, 64, BF, lead=lead, tail=tail)
+    check(P, lens, 2, 2, 128, HF, lead=lead, tail=tail)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.1, 0.7])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_scales(P, dtype, scale):
+    check(P, [100, 37], 2, 1, 128, dtype, scale=scale)
+
+
+def test_long(P):
+    check(P, [2100, 1], 2, 1, 128, BF)
+    check(P, [1500, 600], 4, 1, 64, HF)
+
+
+@pytest.mark.parametrize("max_len", [1, 40, 64, 130])
+def test_tokens_past_the_bound_are_left_alone(P, max_len):
+    check(P, [50, 200, 3], 2, 1, 64, BF, max_len=max_len)
+
+
+def test_a_bound_above_the_lengths(P):
+    check(P, [50, 20], 2, 1, 64, BF, max_len=5000)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("std", [0.05, 6.0])
+def test_flat_and_sharp_probabilities(P, dtype, std):
+    check(P, [150, 90], 2, 1, 128, dtype, std=std)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("dstd", [2e-5, 300.0])
+def test_small_and_large_gradients(P, dtype, dstd):
+    """fp16: ds of a token is far below its normal range, or dout . v above a thousand."""
+    check(P, [150, 90], 2, 1, 64, dtype, dstd=dstd, std=0.5)
+
+
+def test_rows_of_very_different_gradients(P):
+    T, dtype = 200, HF
+    Q, K, V = inputs(T, 2, 1, 64, dtype)
+    out, lse = forward(P, Q, K, V, [0, T], T)
+    dO = rand((T, 2, 64), F32, 5)
+    dO *= 10.0 ** torch.linspace(-3, 3, T, device="cuda")[torch.randperm(T, generator=torch.Generator().manual_seed(1)).cuda()][:, None, None]
+    dO = dO.to(dtype)
+    got = backward(P, dO, Q, K, V, out, lse, [0, T], T)
+    ref = R.prompt_backward64(dO, Q, K, V, out, lse, [0, T], 64 ** -0.5)
+    for x, name in zip(got, ("dq", "dk", "dv")):
+        R.within(x, *ref[name], name)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_what_a_token_does_not_see_does_not_reach_it(P, dtype, hd, value):
+    """A value that is no number at token j of one of two sequences: the other sequence, the tokens before j (forward,
+    dQ) and the keys behind it (dK, dV) stay bit for bit as they are; what sees it is no number."""
+    lens, H, n_kv = [150, 90], 2, 1
+    start, T, j = [0, 150, 240], 240, 97
+    Q, K, V = inputs(T, H, n_kv, hd, dtype)
+    out, lse = forward(P, Q, K, V, start, 150)
+    dO = rand((T, H, hd), dtype, 9)
+    good = backward(P, dO, Q, K, V, out, lse, start, 150)
+    other = torch.arange(150, 240, device="cuda")
+    for which in "qkvo":
+        Q2, K2, V2, dO2 = (t.clone() for t in (Q, K, V, dO))
+        dict(q=Q2, k=K2, v=V2, o=dO2)[which][j, 0, 5] = value
+        out2, lse2 = forward(P, Q2, K2, V2, start, 150)
+        keep = [t for t in range(T) if t < j or t >= 150] if which in "kv" else [t for t in range(T) if t != j]
+        if which != "o":
+            assert torch.equal(out2[keep], out[keep]) and torch.equal(lse2[keep], lse[keep]), which
+        if which == "v":
+            assert not bool(torch.isfinite(out2[j:150, :, 5]).any())
+            assert torch.equal(out2[j:150, :, 6], out[j:150, :, 6])
+        got = backward(P, dO2, Q2, K2, V2, out2, lse2, start, 150)
+        for x, ref in zip(got, good):
+            assert torch.equal(x[other], ref[other]), which
+        if which in "qo":
+            rest = [t for t in range(150) if t != j]
+            assert torch.equal(got[0][rest], good[0][rest]), which
+            for x, ref in zip(got[1:], good[1:]):
+                assert torch.equal(x[j + 1:150], ref[j + 1:150]), which
+            assert not bool(torch.isfinite(got[0][j, 0]).all()), which
+        else:
+            assert torch.equal(got[0][:j], good[0][:j]), which
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_lowest_and_largest_values(P, dtype):
+    """Scores at the end of the type's range: the largest key takes all, up to 1e38 (beyond, its log2 is no fp32 number and
+    the rows that see it are none either); scores below -1e30 count as not seen."""
+    T, hd = 70, 64
+    Q, K, V = (t.clone() for t in inputs(T, 1, 1, hd, dtype))
+    big = torch.finfo(dtype).max
+    Q[:, 0, 0], K[:, 0, 0] = 1.0, 0.0
+    K[3, 0, 0] = big
+    out, lse = forward(P, Q, K, V, [0, T], T, 1.0)
+    assert bool(torch.isfinite(out[:3]).all())
+    if big > 1e38:
+        assert bool(out[3:].isnan().all()) and not bool(torch.isfinite(lse[3:]).any())
+        K[3, 0, 0] = 1e38
+        out, lse = forward(P, Q, K, V, [0, T], T, 1.0)
+    assert torch.equal(out[3:, 0], V[3:4, 0].expand(T - 3, hd)) and bool(torch.isfinite(lse).all())
+    if dtype == BF:
+        K[:, 0, 0] = torch.finfo(dtype).min
+        K[40:, 0, 0] = 0.0
+        out, lse = forward(P, Q, K, V, [0, T], T, 1.0)
+        assert bool((out[:40] == 0).all()) and bool((lse[:40] == float("-inf")).all()) and bool(torch.isfinite(lse[40:]).all())
+        assert torch.equal(out[40], V[40])
+        d = backward(P, torch.ones_like(out), Q, K, V, out, lse, [0, T], T, 1.0)
+        assert all(bool(torch.isfinite(x).all()) for x in d) and bool((d[0][:40] == 0).all()) and bool((d[2][:40] == 0).all())
+
+
+def test_separate_tensors_and_pitches(P):
+    T, H, n_kv, hd = 140, 4, 2, 64
+    Q, K, V = inputs(T, H, n_kv, hd, BF)
+    out, lse = forward(P, Q, K, V, [0, T], T)
+    parts = [t.contiguous() for t in (Q, K, V)]
+    out2, lse2 = forward(P, *parts, [0, T], T)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    dO = rand((T, H, hd), BF, 2)
+    d = backward(P, dO, Q, K, V, out, lse, [0, T], T)
+    d2 = [torch.empty_like(t) for t in parts]
+    P.gptq_prompt_attention_backward(dO, *parts, out, lse, i32([0, T]), T, *d2)
+    assert all(torch.equal(x, y) for x, y in zip(d, d2))
+
+
+def test_no_tokens(P):
+    e, k = torch.empty((0, 4, 64), dtype=BF, device="cuda"), torch.empty((0, 2, 64), dtype=BF, device="cuda")
+    P.gptq_prompt_attention(e, k, k.clone(), i32([0, 0]), 0, e.clone())
+    P.gptq_prompt_attention_backward(e, e, k, k, e, torch.empty((0, 4), device="cuda"), i32([0, 0]), 0, e.clone(), k.clone(), k.clone())
+
+
+def test_gradient_against_differences(P):
+    """The kernel's gradients along a direction, and the difference of float64 values there.  out's rounding to fp16 is in D."""
+    T, H, n_kv, hd, start = 60, 4, 2, 64, [0, 45, 60]
+    Q, K, V = inputs(T, H, n_kv, hd, HF)
+    out, lse = forward(P, Q, K, V, start, 45)
+    dO = rand((T, H, hd), HF, 9)
+    got = backward(P, dO, Q, K, V, out, lse, start, 45)
+    at = [t.double() for t in (Q, K, V)]
+    loss = lambda q, k, v: (R.prompt64(q, k, v, start, hd ** -0.5)[0] * dO.double()).sum()  # noqa: E731
+    R.EPS[torch.float64] = 0.0
+    for k, g in enumerate(got):
+        v = rand(g.shape, F32, 30 + k).double()
+        up, down = [t.clone() for t in at], [t.clone() for t in at]
+        up[k] += 1e-5 * v
+        down[k] -= 1e-5 * v
+        diff = (loss(*up) - loss(*down)) / 2e-5
+        # four roundings to fp16 (p, ds, out in D, the result) of terms that are not far larger than what they add up to
+        assert abs(float((g.double() * v).sum() - diff)) <= 4 * 4 * 2.0 ** -11 * float((g.double() * v).abs().sum()) + 1e-5
