@@ -23,7 +23,7 @@
 namespace gptq {
 
 constexpr int kLoraMaxRank = 128, kLoraMaxDim = 1 << 20, kLoraMaxSets = 65535;
-constexpr int kLowWaves = 4, kUpWaves = 4;
+constexpr int kUpWaves = 4;
 
 struct LoraBatch {
   const int32_t* q_start;
@@ -34,25 +34,35 @@ struct LoraBatch {
 
 constexpr int kNoAdapter = -1, kNoToken = -2;
 
-// The adapters of tokens t0 .. t0 + 15 (lane i: token i % 16's): a token's
-// sequence is the number of starts up to it, less one, so sequences without
-// tokens are passed over.
-GPTQ_DEV int adapter_of(const LoraBatch& b, int64_t t0) {
+// The adapters of tokens t0 + 16 j .. t0 + 16 j + 15 (lane i: token i % 16's): a
+// token's sequence is the number of starts up to it, less one, so sequences
+// without tokens are passed over.  The starts are loaded once for all blocks.
+template <int N> GPTQ_DEV void adapters_of(const LoraBatch& b, int64_t t0, int (&id)[N]) {
   const int lane = threadIdx.x & 63;
-  int count = 0;
+  int count[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) count[j] = 0;
   for (int i0 = 0; i0 <= b.n_seqs; i0 += 64) {
     const int64_t v = i0 + lane <= b.n_seqs ? (int64_t)b.q_start[i0 + lane] : INT64_MAX;
     int c = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      c = __popcll(__ballot(v <= t0 + i));
-      if ((lane & 15) == i) count += c;
-    }
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        c = __popcll(__ballot(v <= t0 + 16 * j + i));
+        if ((lane & 15) == i) count[j] += c;
+      }
     if (c < 64) break;
   }
-  if (count < 1 || count > b.n_seqs || t0 + (lane & 15) >= b.m) return kNoToken;
-  const int a = b.adapter[count - 1];
-  return a >= 0 && a < b.n_adapters ? a : kNoAdapter;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const bool in = count[j] >= 1 && count[j] <= b.n_seqs && t0 + 16 * j + (lane & 15) < b.m;
+    id[j] = kNoToken;
+    if (in) {
+      const int a = b.adapter[count[j] - 1];
+      id[j] = a >= 0 && a < b.n_adapters ? a : kNoAdapter;
+    }
+  }
 }
 
 // the first of the adapters (or kNoAdapter) among the lanes of `left`, which loses its lanes
@@ -76,7 +86,7 @@ struct LowArgs {
   const uint16_t* X;      // [m x K], pitch ldx
   const uint16_t* A;      // [adapters][rank x K], row pitch lda
   int64_t ldx, lda, set;  // set: from one adapter's matrix to the next's
-  int K, rank, slice_k;   // a workgroup's share of k, a multiple of 64 kLowWaves
+  int K, rank, slice_k;   // a workgroup's share of k, a multiple of 64 times its waves
   float* part;            // [slice][m][16 NB]
   int32_t* ids;           // [m], written by the first slice
 };
@@ -86,44 +96,34 @@ struct LowArgs {
 // a lane has four neighbouring ranks of one token.  blockIdx.z takes every
 // gridDim.z-th adapter of the tile: in a decode step each token may have its own,
 // and one after the other they would be a chain of memory latencies.
-template <typename T, int NB, int MT, bool VEC>
-__global__ __launch_bounds__(64 * kLowWaves) void lora_low_kernel(LowArgs p, LoraBatch batch) {
+template <typename T, int NB, int MT, int W, bool VEC>
+__global__ __launch_bounds__(64 * W) void lora_low_kernel(LowArgs p, LoraBatch batch) {
   typedef typename T16<T>::v8 v8;
-  __shared__ f32x4_t red[kLowWaves][MT][NB][64];
+  __shared__ f32x4_t red[W][MT][NB][64];
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t0 = (int64_t)blockIdx.x * (16 * MT);
   int id[MT];
+  adapters_of<MT>(batch, t0, id);
   const uint16_t* x[MT];
+  uint64_t left[MT];
+  bool mine[MT];           // this workgroup sums the lane's token
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
-    id[j] = adapter_of(batch, t0 + 16 * j);
     x[j] = p.X + min(t0 + 16 * j + i, batch.m - 1) * p.ldx;
     if (blockIdx.y == 0 && blockIdx.z == 0 && wave == 0 && lane < 16 && t0 + 16 * j + i < batch.m) p.ids[t0 + 16 * j + i] = id[j];
-#pragma unroll
-    for (int n = 0; n < NB; ++n) red[wave][j][n][lane] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    left[j] = __ballot(lane < 16 && id[j] >= 0);
+    mine[j] = false;
   }
   const int k_lo = blockIdx.y * p.slice_k, k_hi = min(k_lo + p.slice_k, p.K);
-  uint64_t left[MT];
-  bool mine[MT];           // this workgroup writes the lane's token
-#pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    left[j] = __ballot(lane < 16 && id[j] >= 0);
-    mine[j] = id[j] < 0 && blockIdx.z == 0;
-  }
-  for (int n_set = 0;; ++n_set) {
+  for (uint32_t n_set = 0;; ++n_set) {
     int a = -1;
 #pragma unroll
     for (int j = 0; j < MT; ++j)
       if (a < 0 && left[j]) a = __builtin_amdgcn_readlane(id[j], __builtin_ctzll(left[j]));
     if (a < 0) break;
-    bool some[MT];
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      const uint64_t same = __ballot(lane < 16 && id[j] == a);
-      some[j] = same != 0;
-      left[j] &= ~same;
-    }
+    for (int j = 0; j < MT; ++j) left[j] &= ~__ballot(id[j] == a);
     if (n_set % gridDim.z != blockIdx.z) continue;
     const uint16_t* A = p.A + a * p.set;
     f32x4_t acc[MT][NB];
@@ -147,7 +147,7 @@ __global__ __launch_bounds__(64 * kLowWaves) void lora_low_kernel(LowArgs p, Lor
     };
     int k0 = k_lo + 64 * wave;
     if (k0 < k_hi) load(k0);
-    for (; k0 < k_hi; k0 += 64 * kLowWaves) {
+    for (; k0 < k_hi; k0 += 64 * W) {
       v8 xo[MT][2], ao[NB][2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -156,7 +156,7 @@ __global__ __launch_bounds__(64 * kLowWaves) void lora_low_kernel(LowArgs p, Lor
 #pragma unroll
         for (int n = 0; n < NB; ++n) ao[n][h] = __builtin_bit_cast(v8, av[n][h]);
       }
-      if (k0 + 64 * kLowWaves < k_hi) load(k0 + 64 * kLowWaves);
+      if (k0 + 64 * W < k_hi) load(k0 + 64 * W);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -166,7 +166,7 @@ __global__ __launch_bounds__(64 * kLowWaves) void lora_low_kernel(LowArgs p, Lor
     }
 #pragma unroll
     for (int j = 0; j < MT; ++j)
-      if (some[j] && id[j] == a) {
+      if (id[j] == a) {
         mine[j] = true;
 #pragma unroll
         for (int n = 0; n < NB; ++n) red[wave][j][n][lane] = acc[j][n];
@@ -176,17 +176,85 @@ __global__ __launch_bounds__(64 * kLowWaves) void lora_low_kernel(LowArgs p, Lor
 #pragma unroll
   for (int u = 0; u < MT * NB; ++u) {
     const int j = u / NB, n = u % NB;
-    if (u % kLowWaves != wave || !mine[j]) continue;
-    f32x4_t s = red[0][j][n][lane];
-#pragma unroll
-    for (int w = 1; w < kLowWaves; ++w) s += red[w][j][n][lane];
     const int64_t t = t0 + 16 * j + i;
-    if (t < batch.m) *reinterpret_cast<f32x4_t*>(p.part + ((int64_t)blockIdx.y * batch.m + t) * (16 * NB) + 16 * n + 4 * g) = s;
+    if (u % W != wave || t >= batch.m || !(mine[j] || (id[j] < 0 && blockIdx.z == 0))) continue;
+    f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (mine[j]) {
+#pragma unroll
+      for (int w = 0; w < W; ++w) s += red[w][j][n][lane];
+    }
+    *reinterpret_cast<f32x4_t*>(p.part + ((int64_t)blockIdx.y * batch.m + t) * (16 * NB) + 16 * n + 4 * g) = s;
+  }
+}
+
+// Rows of s as an operand: in two pieces of T, [hi ranks | lo ranks], below the
+// row's power of two (fp16 has not the range of fp32), which `row` takes.
+template <typename T> GPTQ_DEV float piece_scale(float top, float& row) {
+  int ex = (int)(__builtin_bit_cast(uint32_t, top) >> 23);
+  ex = ex == 255 || ex == 0 ? 127 : min(ex, 252);
+  row = __builtin_bit_cast(float, (uint32_t)ex << 23);
+  return __builtin_bit_cast(float, (uint32_t)(254 - ex) << 23);
+}
+template <typename T> GPTQ_DEV uint4 piece_of(const float (&s)[8], float inv, bool low) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float a0 = s[2 * e] * inv, a1 = s[2 * e + 1] * inv;
+    w[e] = pack2<T>(a0, a1);
+    if (low) {
+      const float h0 = lo16f<T>(w[e]), h1 = hi16f<T>(w[e]);
+      w[e] = pack2<T>(fabsf(h0) < INFINITY ? a0 - h0 : 0.0f, fabsf(h1) < INFINITY ? a1 - h1 : 0.0f);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The slices' sums in order: s (fp32, where it is wanted), its pieces and their
+// rows' scales.  2 NB threads to a token, eight ranks each.  (In long runs every one
+// of a token's channel groups would add the slices again.)
+template <typename T>
+__global__ __launch_bounds__(256) void lora_pieces_kernel(const float* __restrict__ part, int slices, const int32_t* __restrict__ ids, int64_t m,
+                                                          int nb, int rank, float* __restrict__ S, uint16_t* __restrict__ pieces,
+                                                          float* __restrict__ rows) {
+  const int per = 2 * nb, c = threadIdx.x % per;
+  const int64_t t = (int64_t)blockIdx.x * (256 / per) + threadIdx.x / per;
+  float s[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s[e] = 0.0f;
+  if (t < m) {
+#pragma unroll 4
+    for (int z = 0; z < slices; ++z) {
+      const f32x4_t* from = reinterpret_cast<const f32x4_t*>(part + ((int64_t)z * m + t) * (16 * nb) + 8 * c);
+      const f32x4_t lo = from[0], hi = from[1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[e] += lo[e];
+        s[4 + e] += hi[e];
+      }
+    }
+  }
+  float top = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(s[e]));
+  for (int o = 1; o < per; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+  if (t >= m) return;
+  float row;
+  const float inv = piece_scale<T>(top, row);
+  uint4* to = reinterpret_cast<uint4*>(pieces + t * (32 * nb));
+  to[c] = piece_of<T>(s, inv, false);
+  to[per + c] = piece_of<T>(s, inv, true);
+  if (c == 0) rows[t] = row;
+  if (S && ids[t] != kNoToken) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (8 * c + e < rank) S[t * rank + 8 * c + e] = s[e];
   }
 }
 
 struct UpArgs {
   const float* part;      // [slices][m][16 NB]
+  const uint16_t* pieces; // [m][32 NB], where lora_pieces_kernel has made them
+  const float* rows;      // [m]
   const int32_t* ids;
   const uint16_t* B;      // [adapters][d x rank], row pitch ldb
   const float* scale;
@@ -203,13 +271,12 @@ struct UpArgs {
 };
 
 // Y = R + scale S B^T: a wave has 64 channels; a unit is a block of 16 tokens and
-// one of the adapters in it.  In a run of one adapter B's operands stay in
-// registers; in a decode step, where every unit has its own, the waves share one
-// channel group's units.  Row 4 g + r of matrix block b stands for channel 16 g + 4 b
-// + r, so a lane ends with 16 neighbouring channels of one token.
-// s comes in two pieces of T below its row's power of two (fp16 has not the
-// range): k of the products is [hi ranks | lo ranks].
-template <typename T, int NB, bool VEC>
+// one of the adapters in it.  In a run of one adapter (MADE: its pieces of s are
+// there) B's operands stay in registers; in a decode step, where every unit has its
+// own, the waves share one channel group's units and make the pieces themselves.
+// Row 4 g + r of matrix block b stands for channel 16 g + 4 b + r, so a lane ends with
+// 16 neighbouring channels of one token.
+template <typename T, int NB, bool VEC, bool MADE>
 __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(UpArgs p) {
   typedef typename T16<T>::v8 v8;
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
@@ -219,7 +286,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(UpArgs p) {
   const int64_t tile = blockIdx.x / groups;
   const int c0 = 64 * (int)((blockIdx.x - tile * groups) * per + wave / p.unit_waves);
   if (c0 >= p.d) return;
-  const bool writes_s = p.S && c0 == 0 && share == 0;
+  const bool writes_s = !MADE && p.S && c0 == 0 && share == 0;
   v8 bo[4][NB];
   float scale = 0.0f;
   int have_set = kNoToken, unit = 0;
@@ -231,9 +298,16 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(UpArgs p) {
     bool have_s = false;
     v8 so[NB];
     float row = 1.0f;
-    // s of this lane's token, ranks 8 q .. 8 q + 7 of the chunks it needs, in its piece
+    // this lane's chunks of its token's pieces
     auto make_s = [&]() {
       have_s = true;
+      if constexpr (MADE) {
+        const int64_t at = min(t, p.m - 1);
+        row = p.rows[at];
+#pragma unroll
+        for (int kb = 0; kb < NB; ++kb) so[kb] = *reinterpret_cast<const v8*>(p.pieces + at * (32 * NB) + 8 * (4 * kb + g));
+        return;
+      }
       float s[NB][8], top = 0.0f;
 #pragma unroll
       for (int kb = 0; kb < NB; ++kb) {
@@ -241,6 +315,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(UpArgs p) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[kb][e] = 0.0f;
         if (id != kNoToken) {
+#pragma unroll 4
           for (int z = 0; z < p.slices; ++z) {
             const f32x4_t* from = reinterpret_cast<const f32x4_t*>(p.part + ((int64_t)z * p.m + t) * (16 * NB) + 8 * rc);
             const f32x4_t lo = from[0], hi = from[1];
@@ -256,24 +331,11 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(UpArgs p) {
       }
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
-      int ex = (int)(__builtin_bit_cast(uint32_t, top) >> 23);
-      ex = ex == 255 || ex == 0 ? 127 : min(ex, 252);
-      row = __builtin_bit_cast(float, (uint32_t)ex << 23);
-      const float inv = __builtin_bit_cast(float, (uint32_t)(254 - ex) << 23);
+      const float inv = piece_scale<T>(top, row);
 #pragma unroll
       for (int kb = 0; kb < NB; ++kb) {
         const bool low = (4 * kb + g) / (2 * NB) != 0;
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float a0 = s[kb][2 * e] * inv, a1 = s[kb][2 * e + 1] * inv;
-          w[e] = pack2<T>(a0, a1);
-          if (low) {
-            const float h0 = lo16f<T>(w[e]), h1 = hi16f<T>(w[e]);
-            w[e] = pack2<T>(fabsf(h0) < INFINITY ? a0 - h0 : 0.0f, fabsf(h1) < INFINITY ? a1 - h1 : 0.0f);
-          }
-        }
-        so[kb] = __builtin_bit_cast(v8, make_uint4(w[0], w[1], w[2], w[3]));
+        so[kb] = __builtin_bit_cast(v8, piece_of<T>(s[kb], inv, low));
         if (writes_s && !low && id != kNoToken) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -338,22 +400,33 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(UpArgs p) {
 
 // ---------------------------------------------------------------- backward
 
-// [n][rows x cols] -> [n][cols x rows], row pitch `pitch` (a multiple of 8, zeros from rows on): 64 x 64 tiles through LDS
-__global__ __launch_bounds__(256) void lora_transpose_kernel(const uint16_t* __restrict__ in, int rows, int cols, int pitch,
-                                                             uint16_t* __restrict__ out) {
+// [n][rows x cols] -> [n][cols x rows], row pitch `pitch` (a multiple of 8, zeros from
+// rows on), of one or two matrices a set: 64 x 64 tiles through LDS
+struct TransposeSide {
+  const uint16_t* in;
+  uint16_t* out;
+  int rows, cols, pitch;
+  int tiles_c, tiles;      // tiles of 64 columns, all tiles (0: nothing to do)
+};
+__global__ __launch_bounds__(256) void lora_transpose_kernel(TransposeSide s0, TransposeSide s1) {
   __shared__ uint16_t tile[64][66];
-  const int64_t set = blockIdx.z;
-  const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
-  const uint16_t* from = in + set * rows * cols;
-  uint16_t* to = out + set * cols * pitch;
-  for (int u = threadIdx.x; u < 64 * 64; u += 256) {
-    const int r = r0 + (u >> 6), c = c0 + (u & 63);
-    tile[u >> 6][u & 63] = r < rows && c < cols ? from[(int64_t)r * cols + c] : (uint16_t)0;
+  const bool second = (int)blockIdx.x >= s0.tiles;
+  const TransposeSide& s = second ? s1 : s0;
+  const int u = blockIdx.x - (second ? s0.tiles : 0);
+  const int64_t set = blockIdx.y;
+  const int r0 = u / s.tiles_c * 64, c0 = u % s.tiles_c * 64, x = threadIdx.x & 63, y = threadIdx.x >> 6;
+  const uint16_t* from = s.in + set * s.rows * s.cols;
+  uint16_t* to = s.out + set * s.cols * s.pitch;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const int r = r0 + y + 4 * k, c = c0 + x;
+    tile[y + 4 * k][x] = r < s.rows && c < s.cols ? from[(int64_t)r * s.cols + c] : (uint16_t)0;
   }
   __syncthreads();
-  for (int u = threadIdx.x; u < 64 * 64; u += 256) {
-    const int c = c0 + (u >> 6), r = r0 + (u & 63);
-    if (c < cols && r < pitch) to[(int64_t)c * pitch + r] = tile[u & 63][u >> 6];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const int c = c0 + y + 4 * k, r = r0 + x;
+    if (c < s.cols && r < s.pitch) to[(int64_t)c * s.pitch + r] = tile[x][y + 4 * k];
   }
 }
 
@@ -392,8 +465,8 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(OuterArgs p) {
   typedef typename T16<__bf16>::v8 b8;
   constexpr bool kSplitX = T16<T>::kType == GPTQ_F16;
   constexpr int kPitch = 40;                         // tokens of a rank's row in LDS: 80 bytes
-  __shared__ __attribute__((aligned(1024))) uint16_t xs[32 * 128];
-  __shared__ __attribute__((aligned(16))) uint16_t ss[2][16 * NB * kPitch];
+  __shared__ __attribute__((aligned(1024))) uint16_t xs[2 * 32 * 128];
+  __shared__ __attribute__((aligned(16))) uint16_t ss[2 * 2 * 16 * NB * kPitch];
   const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const bool is_b = (int)blockIdx.x >= p.side[0].tiles;
@@ -401,7 +474,7 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(OuterArgs p) {
   const int c0 = 128 * ((int)blockIdx.x - (is_b ? p.side[0].tiles : 0)), a = blockIdx.z;
   const int64_t t_lo = blockIdx.y * p.slice, t_hi = min(t_lo + p.slice, p.m);
   const float scale = p.scale[a];
-  const uint32_t xl = (uint32_t)(uintptr_t)(LDS_AS const char*)(const char*)xs;
+  const uint32_t xl0 = (uint32_t)(uintptr_t)(LDS_AS const char*)(const char*)xs;
   // 32-byte pairs of chunks of row t sit at pair ^ (t % 4 + 4 (t / 8 % 2)): the rows that a read takes differ in it
   auto swz = [](int t) { return (t & 3) | ((t >> 1) & 4); };
   f32x4_t acc[2][NB];
@@ -409,28 +482,60 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(OuterArgs p) {
   for (int b = 0; b < 2; ++b)
 #pragma unroll
     for (int n = 0; n < NB; ++n) acc[b][n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t t0 = t_lo; t0 < t_hi; t0 += 32) {
-    const int64_t mine_t = t0 + (lane & 31);
-    const bool mine = mine_t < t_hi && p.ids[mine_t] == a;
-    const uint64_t some = __ballot(mine);
-    if (!some) continue;
-    // another adapter's tokens count as zeros, whatever they hold
+  // One step ahead: a step's values are on their way while the one before it is
+  // multiplied, its tokens' adapters one step longer.
+  uint4 xv[2];
+  float sv[2 * NB];
+  auto load_ids = [&](int64_t t0) {
+    const int64_t t = t0 + (lane & 31);
+    return t < t_hi ? p.ids[t] : kNoToken;
+  };
+  // another adapter's tokens count as zeros, whatever they hold
+  auto load = [&](int64_t t0, uint32_t some) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int t = (tid >> 4) + 16 * h, ch = tid & 15, c = c0 + 8 * ch;
+      const int t = (tid >> 4) + 16 * h, c = c0 + 8 * (tid & 15);
       const int have = (some >> t) & 1 ? o.d - c : 0;
       const uint16_t* x = o.X + (t0 + t) * o.ldx + c;
-      const uint4 v = o.vec && have >= 8 ? load_chunk<true>(x, have) : load_chunk<false>(x, have);
-      *reinterpret_cast<uint4*>(xs + t * 128 + (((ch >> 1) ^ swz(t)) << 4) + 8 * (ch & 1)) = v;
+      xv[h] = o.vec && have >= 8 ? load_chunk<true>(x, have) : load_chunk<false>(x, have);
     }
-    for (int u = tid; u < 32 * 16 * NB; u += 256) {
-      const int t = u / (16 * NB), r = u % (16 * NB);
-      const float v = ((some >> t) & 1) && r < p.rank ? scale * o.S[(t0 + t) * p.rank + r] : 0.0f;
-      const uint16_t hi = bits16<__bf16>(v);
-      const float rest = v - (float)__builtin_bit_cast(__bf16, hi);
-      ss[0][r * kPitch + t] = hi;
-      ss[1][r * kPitch + t] = bits16<__bf16>(fabsf((float)__builtin_bit_cast(__bf16, hi)) < INFINITY ? rest : 0.0f);
+#pragma unroll
+    for (int k = 0; k < 2 * NB; ++k) {
+      const int u = tid + 256 * k, t = u / (16 * NB), r = u % (16 * NB);
+      sv[k] = ((some >> t) & 1) && r < p.rank ? o.S[(t0 + t) * p.rank + r] : 0.0f;
     }
+  };
+  uint32_t now = (uint32_t)__ballot(load_ids(t_lo) == a);
+  if (now) load(t_lo, now);
+  int next_ids = load_ids(t_lo + 32);
+  uint32_t turn = 0;
+  for (int64_t t0 = t_lo; t0 < t_hi; t0 += 32) {
+    const uint32_t next = (uint32_t)__ballot(next_ids == a), some = now;
+    uint16_t* xb = xs + (turn & 1) * (32 * 128);
+    uint16_t* sb = ss + (turn & 1) * (2 * 16 * NB * kPitch);
+    if (some) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int t = (tid >> 4) + 16 * h, ch = tid & 15;
+        *reinterpret_cast<uint4*>(xb + t * 128 + (((ch >> 1) ^ swz(t)) << 4) + 8 * (ch & 1)) = xv[h];
+      }
+#pragma unroll
+      for (int k = 0; k < 2 * NB; ++k) {
+        const int u = tid + 256 * k, t = u / (16 * NB), r = u % (16 * NB);
+        const float v = scale * sv[k];
+        const uint16_t hi = bits16<__bf16>((some >> t) & 1 ? v : 0.0f);
+        const float hf = (float)__builtin_bit_cast(__bf16, hi);
+        sb[r * kPitch + t] = hi;
+        sb[16 * NB * kPitch + r * kPitch + t] = bits16<__bf16>(((some >> t) & 1) && fabsf(hf) < INFINITY ? v - hf : 0.0f);
+      }
+    }
+    if (next) load(t0 + 32, next);
+    next_ids = load_ids(t0 + 64);
+    now = next;
+    if (!some) continue;
+    const uint32_t xl = xl0 + (turn & 1) * (32 * 128 * 2);
+    ++turn;
+    // (two buffers: a wave that is behind still reads the other one)
     __syncthreads();
     b8 xo[2][kSplitX ? 2 : 1];
 #pragma unroll
@@ -462,7 +567,7 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(OuterArgs p) {
     for (int n = 0; n < NB; ++n) {
       b8 so[2];
 #pragma unroll
-      for (int z = 0; z < 2; ++z) so[z] = *reinterpret_cast<const b8*>(ss[z] + (16 * n + i) * kPitch + 8 * g);
+      for (int z = 0; z < 2; ++z) so[z] = *reinterpret_cast<const b8*>(sb + (16 * NB * z + 16 * n + i) * kPitch + 8 * g);
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         auto product = [&](const b8& x, const b8& s) {
@@ -477,7 +582,6 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(OuterArgs p) {
         }
       }
     }
-    __syncthreads();
   }
   float* out = o.out + blockIdx.y * o.split + (int64_t)a * p.rank * o.d;
 #pragma unroll
@@ -515,61 +619,93 @@ static bool lora_ok(const gptq_lora_set* a) {
 }
 constexpr int64_t kLoraMaxTokens = 1 << 24;
 
-// How X A^T is dealt out: 16 MT tokens a workgroup, k in slices, until there are
-// four workgroups a CU; the adapters of a tile over `shares`.
+// How X A^T is dealt out.  Runs: 32 tokens a workgroup of eight waves (at rank 128
+// 16), k in slices until there are two workgroups a CU.  Steps of mixed adapters: 16
+// tokens a workgroup of four waves, one of the adapters each, up to 8 slices (which the
+// second product adds itself).
 struct LowPlan {
+  bool mix;
   int mt, tiles, slices, slice_k, shares;
 };
 static bool mixed(int64_t m, int n_seqs) { return m < 16 * (int64_t)n_seqs; }     // a block of tokens has several adapters
 static LowPlan low_plan(int64_t m, int n_seqs, int K, int nb) {
   LowPlan p;
-  const bool mix = mixed(m, n_seqs);
-  p.mt = mix || m <= 32 ? 1 : nb == 8 ? 2 : 4;
+  p.mix = mixed(m, n_seqs);
+  p.mt = p.mix || nb == 8 ? 1 : 2;
   p.tiles = (int)((m + 16 * p.mt - 1) / (16 * p.mt));
-  p.shares = mix ? 4 : 1;
-  const int step = 64 * kLowWaves, most = (K + step - 1) / step;
-  const int64_t want = 1024 / ((int64_t)p.tiles * p.shares);
-  int n = (int)std::max<int64_t>(1, std::min<int64_t>(want, std::min(most, 32)));
+  p.shares = p.mix ? 16 : 1;
+  const int step = 64 * (p.mix ? 4 : 8), most = (K + step - 1) / step;
+  const int n = (int)std::max<int64_t>(1, std::min<int64_t>(512 / (p.mix ? (p.tiles + 7) / 8 * 8 : p.tiles), std::min(most, p.mix ? 8 : 16)));
   p.slice_k = (most + n - 1) / n * step;
   p.slices = (K + p.slice_k - 1) / p.slice_k;
   return p;
 }
-// room for every plan of m tokens, whatever the sequences
-static size_t part_bytes(int64_t m, int K, int nb) {
-  int slices = 1;
-  for (int n_seqs : {1, (int)std::min<int64_t>(m, INT_MAX - 1) / 16 + 1}) slices = std::max(slices, low_plan(m, n_seqs, K, nb).slices);
-  return align_up((size_t)slices * m * 16 * nb * sizeof(float));
+// The partial sums' part of the workspace: token ids, sums, and s's pieces with their rows' scales; room for every
+// batch of m tokens, whatever its sequences.
+struct LowLayout {
+  size_t off_part, off_pieces, off_rows, total;
+};
+static LowLayout low_layout(int64_t m, int K, int nb) {
+  LowLayout L;
+  const int slices = std::max(low_plan(m, 1, K, nb).slices, low_plan(m, (int)(m / 16 + 1), K, nb).slices);
+  L.off_part = align_up((size_t)m * sizeof(int32_t));
+  L.off_pieces = L.off_part + align_up((size_t)slices * m * 16 * nb * sizeof(float));
+  L.off_rows = L.off_pieces + align_up((size_t)m * 32 * nb * 2);
+  L.total = L.off_rows + align_up((size_t)m * sizeof(float));
+  return L;
 }
 
+// s of every token into the workspace at base; where they are runs, as pieces
 template <typename T>
-static int launch_low(const LowPlan& p, int nb, bool vec, const LowArgs& a, const LoraBatch& b, hipStream_t s) {
+static int launch_low(const LowPlan& p, const LowLayout& L, int nb, bool vec, LowArgs a, const LoraBatch& b, char* base, float* S, hipStream_t s) {
   const dim3 grid((unsigned)p.tiles, (unsigned)p.slices, (unsigned)p.shares);
-  auto go = [&]<int NB, int MT>() {
-    if (vec) lora_low_kernel<T, NB, MT, true><<<grid, 64 * kLowWaves, 0, s>>>(a, b);
-    else lora_low_kernel<T, NB, MT, false><<<grid, 64 * kLowWaves, 0, s>>>(a, b);
+  a.slice_k = p.slice_k;
+  a.ids = reinterpret_cast<int32_t*>(base);
+  a.part = reinterpret_cast<float*>(base + L.off_part);
+  auto go = [&]<int NB>() {
+    auto on = [&]<int MT, int W>() {
+      if (vec) lora_low_kernel<T, NB, MT, W, true><<<grid, 64 * W, 0, s>>>(a, b);
+      else lora_low_kernel<T, NB, MT, W, false><<<grid, 64 * W, 0, s>>>(a, b);
+    };
+    p.mix ? on.template operator()<1, 4>() : on.template operator()<NB == 8 ? 1 : 2, 8>();
   };
-  if (nb == 1) p.mt == 1 ? go.template operator()<1, 1>() : go.template operator()<1, 4>();
-  else if (nb == 2) p.mt == 1 ? go.template operator()<2, 1>() : go.template operator()<2, 4>();
-  else if (nb == 4) p.mt == 1 ? go.template operator()<4, 1>() : go.template operator()<4, 4>();
-  else p.mt == 1 ? go.template operator()<8, 1>() : go.template operator()<8, 2>();
+  if (nb == 1) go.template operator()<1>();
+  else if (nb == 2) go.template operator()<2>();
+  else if (nb == 4) go.template operator()<4>();
+  else go.template operator()<8>();
   GPTQ_LAUNCH_CHECK();
+  if (!p.mix) {
+    lora_pieces_kernel<T><<<(unsigned)((b.m * 2 * nb + 255) / 256), 256, 0, s>>>(a.part, p.slices, a.ids, b.m, nb, a.rank, S,
+                                                                              reinterpret_cast<uint16_t*>(base + L.off_pieces),
+                                                                              reinterpret_cast<float*>(base + L.off_rows));
+    GPTQ_LAUNCH_CHECK();
+  }
   return GPTQ_OK;
 }
 
+// The second product (a.Y; a.S where the pieces are made here), from what launch_low left at base.
 template <typename T>
-static int launch_up(UpArgs a, int nb, bool mix, hipStream_t s) {
-  a.unit_waves = mix ? kUpWaves : 1;
+static int launch_up(UpArgs a, const LowPlan& lp, const LowLayout& L, int nb, char* base, hipStream_t s) {
+  a.part = reinterpret_cast<float*>(base + L.off_part);
+  a.pieces = reinterpret_cast<uint16_t*>(base + L.off_pieces);
+  a.rows = reinterpret_cast<float*>(base + L.off_rows);
+  a.ids = reinterpret_cast<int32_t*>(base);
+  a.slices = lp.slices;
+  a.unit_waves = lp.mix ? kUpWaves : 1;
   const int per = kUpWaves / a.unit_waves;
-  const int64_t groups = a.Y ? ((a.d + 63) / 64 + per - 1) / per : 1;
-  // as many token blocks a workgroup (B's operands serve them all) as leave two workgroups a CU
-  a.blocks = mix ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(8, (a.m + 15) / 16 * groups / 512));
-  const int64_t tiles = (a.m + 16 * a.blocks - 1) / (16 * a.blocks);
   if (!a.Y) a.d = 1;
+  const int64_t groups = ((a.d + 63) / 64 + per - 1) / per;
+  // as many token blocks a workgroup (B's operands serve them all) as leave two workgroups a CU
+  a.blocks = lp.mix ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(8, (a.m + 15) / 16 * groups / 512));
+  const int64_t tiles = (a.m + 16 * a.blocks - 1) / (16 * a.blocks);
   const bool vec = at16(a.B) && a.rank % 8 == 0 && a.ldb % 8 == 0 && a.set % 8 == 0;
   if (tiles * groups > (1 << 24) - 1) return GPTQ_ERR_INVALID_ARG;
   auto go = [&]<int NB>() {
-    if (vec) lora_up_kernel<T, NB, true><<<(unsigned)(tiles * groups), 64 * kUpWaves, 0, s>>>(a);
-    else lora_up_kernel<T, NB, false><<<(unsigned)(tiles * groups), 64 * kUpWaves, 0, s>>>(a);
+    auto on = [&]<bool VEC>() {
+      if (lp.mix) lora_up_kernel<T, NB, VEC, false><<<(unsigned)(tiles * groups), 64 * kUpWaves, 0, s>>>(a);
+      else lora_up_kernel<T, NB, VEC, true><<<(unsigned)(tiles * groups), 64 * kUpWaves, 0, s>>>(a);
+    };
+    vec ? on.template operator()<true>() : on.template operator()<false>();
   };
   if (nb == 1) go.template operator()<1>();
   else if (nb == 2) go.template operator()<2>();
@@ -588,7 +724,8 @@ static bool share_bytes(const void* a, uint64_t na, const void* b, uint64_t nb) 
 static bool rows_vec(const void* p, int64_t ld, gptq_dtype t) { return !p || (at16(p) && ld % (t == GPTQ_F32 ? 4 : 8) == 0); }
 
 struct LoraBackLayout {
-  size_t off_part, off_ds, off_at, off_bt, off_outer, total;
+  LowLayout low;
+  size_t off_ds, off_at, off_bt, off_outer, total;
   int nb, splits;
   int64_t slice, out_pitch;
 };
@@ -596,8 +733,8 @@ static LoraBackLayout lora_back_layout(int64_t m, const gptq_lora_set* a) {
   LoraBackLayout L;
   L.nb = rank_blocks(a->rank);
   const int64_t sets = a->n_adapters, r = a->rank, pitch = (r + 7) & ~7;
-  L.off_part = align_up((size_t)m * 4);
-  L.off_ds = L.off_part + part_bytes(m, a->d_out, L.nb);
+  L.low = low_layout(m, a->d_out, L.nb);
+  L.off_ds = L.low.total;
   L.off_at = L.off_ds + align_up((size_t)m * r * 4);
   L.off_bt = L.off_at + align_up((size_t)sets * a->d_in * pitch * 2);
   L.off_outer = L.off_bt + align_up((size_t)sets * r * ((a->d_out + 7) & ~7) * 2);
@@ -617,25 +754,29 @@ static int lora_backward(const void* dY, int64_t lddy, const void* X, int64_t ld
                          float* dB, char* base, hipStream_t s) {
   const LoraBackLayout L = lora_back_layout(b.m, a);
   const int sets = a->n_adapters, r = a->rank, pitch = (r + 7) & ~7, kp = (a->d_out + 7) & ~7;
-  int32_t* ids = reinterpret_cast<int32_t*>(base);
-  float *part = reinterpret_cast<float*>(base + L.off_part), *ds = reinterpret_cast<float*>(base + L.off_ds);
+  const int32_t* ids = reinterpret_cast<const int32_t*>(base);
+  float* ds = reinterpret_cast<float*>(base + L.off_ds);
   uint16_t *at = reinterpret_cast<uint16_t*>(base + L.off_at), *bt = reinterpret_cast<uint16_t*>(base + L.off_bt);
-  const uint16_t *A = static_cast<const uint16_t*>(a->A), *B = static_cast<const uint16_t*>(a->B);
-  lora_transpose_kernel<<<dim3((unsigned)((r + 63) / 64), (unsigned)((kp + 63) / 64), (unsigned)sets), 256, 0, s>>>(B, a->d_out, r, kp, bt);
+  auto side = [](const void* in, uint16_t* out, int rows, int cols, int out_pitch) {
+    const int tc = (cols + 63) / 64;
+    return TransposeSide{static_cast<const uint16_t*>(in), out, rows, cols, out_pitch, tc, tc * ((out_pitch + 63) / 64)};
+  };
+  const TransposeSide tb = side(a->B, bt, a->d_out, r, kp);
+  TransposeSide ta = side(a->A, at, r, a->d_in, pitch);
+  if (!dX) ta.tiles = 0;
+  lora_transpose_kernel<<<dim3((unsigned)(tb.tiles + ta.tiles), (unsigned)sets), 256, 0, s>>>(tb, ta);
   GPTQ_LAUNCH_CHECK();
-  if (dX) {
-    lora_transpose_kernel<<<dim3((unsigned)((a->d_in + 63) / 64), (unsigned)((pitch + 63) / 64), (unsigned)sets), 256, 0, s>>>(A, r, a->d_in,
-                                                                                                                         pitch, at);
-    GPTQ_LAUNCH_CHECK();
-  }
   const LowPlan lp = low_plan(b.m, b.n_seqs, a->d_out, L.nb);
   const bool vec = rows_vec(dY, lddy, GPTQ_BF16) && a->d_out % 8 == 0;
-  int st = launch_low<T>(lp, L.nb, vec, LowArgs{static_cast<const uint16_t*>(dY), bt, lddy, kp, (int64_t)r * kp, a->d_out, r, lp.slice_k, part, ids}, b, s);
+  LowArgs low{static_cast<const uint16_t*>(dY), bt, lddy, kp, (int64_t)r * kp, a->d_out, r};
+  int st = launch_low<T>(lp, L.low, L.nb, vec, low, b, base, dA ? ds : nullptr, s);
   if (st != GPTQ_OK) return st;
-  UpArgs u{part, ids, at, a->scale, R, dX, dA ? ds : nullptr, pitch, (int64_t)a->d_in * pitch, ldr, lddx, b.m, lp.slices, r, a->d_in, x_dtype,
-           rows_vec(R, ldr, x_dtype) && rows_vec(dX, lddx, x_dtype), 1, 1};
-  if (dX || dA) {
-    st = launch_up<T>(u, L.nb, mixed(b.m, b.n_seqs), s);
+  if (dX || (dA && lp.mix)) {
+    UpArgs u{};
+    u.B = at; u.scale = a->scale; u.R = R; u.Y = dX; u.S = dA ? ds : nullptr;
+    u.ldb = pitch; u.set = (int64_t)a->d_in * pitch; u.ldr = ldr; u.ldy = lddx; u.m = b.m; u.rank = r; u.d = a->d_in; u.y_type = x_dtype;
+    u.vec = rows_vec(R, ldr, x_dtype) && rows_vec(dX, lddx, x_dtype);
+    st = launch_up<T>(u, lp, L.low, L.nb, base, s);
     if (st != GPTQ_OK) return st;
   }
   if (!dA && !dB) return GPTQ_OK;
@@ -675,7 +816,7 @@ using namespace gptq;
 
 extern "C" size_t gptq_lora_workspace_size(int64_t m, const gptq_lora_set* a) {
   if (m <= 0 || m > kLoraMaxTokens || !lora_ok(a)) return 0;
-  return align_up((size_t)m * 4) + part_bytes(m, a->d_in, rank_blocks(a->rank));
+  return low_layout(m, a->d_in, rank_blocks(a->rank)).total;
 }
 
 extern "C" int gptq_lora(const void* X, gptq_dtype x_dtype, int64_t m, int64_t ldx, const gptq_lora_set* a, const int32_t* q_start,
@@ -694,22 +835,20 @@ extern "C" int gptq_lora(const void* X, gptq_dtype x_dtype, int64_t m, int64_t l
   if (!ws || ws_bytes < gptq_lora_workspace_size(m, a) || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return GPTQ_ERR_WORKSPACE;
   const int nb = rank_blocks(a->rank);
   const LowPlan lp = low_plan(m, n_seqs, a->d_in, nb);
+  const LowLayout L = low_layout(m, a->d_in, nb);
   const LoraBatch b{q_start, adapter, n_seqs, a->n_adapters, m};
   char* base = static_cast<char*>(ws);
-  int32_t* ids = reinterpret_cast<int32_t*>(base);
-  float* part = reinterpret_cast<float*>(base + align_up((size_t)m * 4));
   const bool vec = rows_vec(X, ldx, x_dtype) && at16(a->A) && a->d_in % 8 == 0;
-  const LowArgs low{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(a->A), ldx, a->d_in, (int64_t)a->rank * a->d_in, a->d_in,
-                    a->rank, lp.slice_k, part, ids};
-  const UpArgs up{part, ids, static_cast<const uint16_t*>(a->B), a->scale, R, Y, S, a->rank, (int64_t)a->d_out * a->rank, ldr, ldy, m,
-                  lp.slices, a->rank, a->d_out, y_dtype, rows_vec(R, ldr, y_dtype) && rows_vec(Y, ldy, y_dtype), 1, 1};
-  const bool mix = mixed(m, n_seqs);
-  if (x_dtype == GPTQ_BF16) {
-    const int st = launch_low<__bf16>(lp, nb, vec, low, b, s);
-    return st != GPTQ_OK ? st : launch_up<__bf16>(up, nb, mix, s);
-  }
-  const int st = launch_low<_Float16>(lp, nb, vec, low, b, s);
-  return st != GPTQ_OK ? st : launch_up<_Float16>(up, nb, mix, s);
+  const LowArgs low{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(a->A), ldx, a->d_in, (int64_t)a->rank * a->d_in, a->d_in, a->rank};
+  UpArgs up{};
+  up.B = static_cast<const uint16_t*>(a->B); up.scale = a->scale; up.R = R; up.Y = Y; up.S = S;
+  up.ldb = a->rank; up.set = (int64_t)a->d_out * a->rank; up.ldr = ldr; up.ldy = ldy; up.m = m; up.rank = a->rank; up.d = a->d_out; up.y_type = y_dtype;
+  up.vec = rows_vec(R, ldr, y_dtype) && rows_vec(Y, ldy, y_dtype);
+  auto go = [&]<typename T>() {
+    const int st = launch_low<T>(lp, L, nb, vec, low, b, base, S, s);
+    return st != GPTQ_OK ? st : launch_up<T>(up, lp, L, nb, base, s);
+  };
+  return x_dtype == GPTQ_BF16 ? go.template operator()<__bf16>() : go.template operator()<_Float16>();
 }
 
 extern "C" size_t gptq_lora_backward_workspace_size(int64_t m, const gptq_lora_set* a) {
