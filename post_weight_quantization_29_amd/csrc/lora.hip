@@ -18,7 +18,6 @@
 #include "w4_epilogue.h"
 
 #include <climits>
-#include <utility>
 
 namespace gptq {
 
@@ -34,35 +33,62 @@ struct LoraBatch {
 
 constexpr int kNoAdapter = -1, kNoToken = -2;
 
-// The adapters of tokens t0 + 16 j .. t0 + 16 j + 15 (lane i: token i % 16's): a
-// token's sequence is the number of starts up to it, less one, so sequences
-// without tokens are passed over.  The starts are loaded once for all blocks.
-template <int N> GPTQ_DEV void adapters_of(const LoraBatch& b, int64_t t0, int (&id)[N]) {
+// The adapters of tokens t0 .. t0 + 15 (lane i: token i % 16's): a token's
+// sequence is the number of starts up to it, less one, so sequences without
+// tokens are passed over.
+GPTQ_DEV int adapter_of(const LoraBatch& b, int64_t t0) {
   const int lane = threadIdx.x & 63;
-  int count[N];
-#pragma unroll
-  for (int j = 0; j < N; ++j) count[j] = 0;
+  int count = 0;
   for (int i0 = 0; i0 <= b.n_seqs; i0 += 64) {
-    const int64_t v = i0 + lane <= b.n_seqs ? (int64_t)b.q_start[i0 + lane] : INT64_MAX;
+    const int v = i0 + lane <= b.n_seqs ? b.q_start[i0 + lane] : INT_MAX;      // tokens are below 2^24
     int c = 0;
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        c = __popcll(__ballot(v <= t0 + 16 * j + i));
-        if ((lane & 15) == i) count[j] += c;
-      }
+    for (int i = 0; i < 16; ++i) {
+      c = __popcll(__ballot(v <= (int)t0 + i));
+      if ((lane & 15) == i) count += c;
+    }
     if (c < 64) break;
   }
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const bool in = count[j] >= 1 && count[j] <= b.n_seqs && t0 + 16 * j + (lane & 15) < b.m;
-    id[j] = kNoToken;
-    if (in) {
-      const int a = b.adapter[count[j] - 1];
-      id[j] = a >= 0 && a < b.n_adapters ? a : kNoAdapter;
+  if (count < 1 || count > b.n_seqs || t0 + (lane & 15) >= b.m) return kNoToken;
+  const int a = b.adapter[count - 1];
+  return a >= 0 && a < b.n_adapters ? a : kNoAdapter;
+}
+
+// Tile u of `tok` tokens of the batch, where tiles end with their sequences: its
+// first row, tokens and adapter (or kNoAdapter); false if there are fewer.  By a
+// running sum of the sequences' tiles; the same in all of a wave's lanes.
+GPTQ_DEV bool run_tile(const LoraBatch& batch, uint32_t u, int tok, int64_t& t0, int& n, int& a) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int s0 = 0; s0 < batch.n_seqs; s0 += 64) {
+    const int b = s0 + lane;
+    int lo = 0, hi = 0;                                // rows are below 2^24
+    if (b < batch.n_seqs) {
+      lo = max(batch.q_start[b], 0);
+      hi = (int)min((int64_t)batch.q_start[b + 1], batch.m);
     }
+    const int tiles = hi > lo ? (hi - lo + tok - 1) / tok : 0;
+    int upto = tiles;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(upto, o);
+      if (lane >= o) upto += v;
+    }
+    upto += before;
+    const uint64_t past = __ballot((int)u < upto);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      const int tile = (int)u - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(tiles, l));
+      const int first = __builtin_amdgcn_readlane(lo, l) + tile * tok;
+      t0 = first;
+      n = min(__builtin_amdgcn_readlane(hi, l) - first, tok);
+      a = batch.adapter[s0 + l];
+      a = a >= 0 && a < batch.n_adapters ? a : kNoAdapter;
+      return true;
+    }
+    before = __builtin_amdgcn_readlane(upto, 63);
   }
+  return false;
 }
 
 // the first of the adapters (or kNoAdapter) among the lanes of `left`, which loses its lanes
@@ -91,99 +117,128 @@ struct LowArgs {
   int32_t* ids;           // [m], written by the first slice
 };
 
-// Partial sums of X A^T: 16 MT tokens by all ranks (16 NB) a workgroup, k dealt to
-// its waves by 64 and joined through LDS in order.  A is the first operand, so that
-// a lane has four neighbouring ranks of one token.  blockIdx.z takes every
-// gridDim.z-th adapter of the tile: in a decode step each token may have its own,
-// and one after the other they would be a chain of memory latencies.
+// one adapter's product: X rows of 16 MT tokens by all ranks over this wave's share of [k_lo, k_hi)
 template <typename T, int NB, int MT, int W, bool VEC>
-__global__ __launch_bounds__(64 * W) void lora_low_kernel(LowArgs p, LoraBatch batch) {
+GPTQ_DEV void low_product(const LowArgs& p, const uint16_t* const (&x)[MT], int a, int k_lo, int k_hi, f32x4_t (&acc)[MT][NB]) {
   typedef typename T16<T>::v8 v8;
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint16_t* A = p.A + a * p.set;
+#pragma unroll
+  for (int j = 0; j < MT; ++j)
+#pragma unroll
+    for (int n = 0; n < NB; ++n) acc[j][n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int k0 = k_lo + 64 * wave; k0 < k_hi; k0 += 64 * W) {
+    uint4 xv[MT][2], av[NB][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = k0 + 32 * h + 8 * g, have = k_hi - k;
+#pragma unroll
+      for (int j = 0; j < MT; ++j) xv[j][h] = load_chunk<VEC>(x[j] + k, have);
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const int r = 16 * n + i;
+        av[n][h] = load_chunk<VEC>(A + r * p.lda + k, r < p.rank ? have : 0);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+          acc[j][n] = T16<T>::mfma16(__builtin_bit_cast(v8, av[n][h]), __builtin_bit_cast(v8, xv[j][h]), acc[j][n]);
+  }
+}
+
+// Partial sums of X A^T: k dealt to a workgroup's waves by 64 and joined through LDS
+// in order.  A is the first operand, so that a lane has four neighbouring ranks of
+// one token.
+//
+// Runs: a workgroup takes 16 MT tokens of one sequence, so of one adapter (tiles that
+// end with their sequences: taken from the rows as they lie, a tile of two adapters
+// went through k twice, and the launch waited for it: 50 us instead of 27 for the
+// prompts below).  Sixteen waves a CU, and the loads of one step a wave in flight.
+template <typename T, int NB, int MT, int W, bool VEC>
+__global__ __launch_bounds__(64 * W, 4) void lora_low_runs_kernel(LowArgs p, LoraBatch batch) {
+  constexpr int TOK = 16 * MT;
   __shared__ f32x4_t red[W][MT][NB][64];
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t0 = (int64_t)blockIdx.x * (16 * MT);
-  int id[MT];
-  adapters_of<MT>(batch, t0, id);
-  const uint16_t* x[MT];
-  uint64_t left[MT];
-  bool mine[MT];           // this workgroup sums the lane's token
-#pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    x[j] = p.X + min(t0 + 16 * j + i, batch.m - 1) * p.ldx;
-    if (blockIdx.y == 0 && blockIdx.z == 0 && wave == 0 && lane < 16 && t0 + 16 * j + i < batch.m) p.ids[t0 + 16 * j + i] = id[j];
-    left[j] = __ballot(lane < 16 && id[j] >= 0);
-    mine[j] = false;
-  }
-  const int k_lo = blockIdx.y * p.slice_k, k_hi = min(k_lo + p.slice_k, p.K);
-  for (uint32_t n_set = 0;; ++n_set) {
-    int a = -1;
-#pragma unroll
-    for (int j = 0; j < MT; ++j)
-      if (a < 0 && left[j]) a = __builtin_amdgcn_readlane(id[j], __builtin_ctzll(left[j]));
-    if (a < 0) break;
-#pragma unroll
-    for (int j = 0; j < MT; ++j) left[j] &= ~__ballot(id[j] == a);
-    if (n_set % gridDim.z != blockIdx.z) continue;
-    const uint16_t* A = p.A + a * p.set;
-    f32x4_t acc[MT][NB];
-#pragma unroll
-    for (int j = 0; j < MT; ++j)
-#pragma unroll
-      for (int n = 0; n < NB; ++n) acc[j][n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    uint4 xv[MT][2], av[NB][2];
-    auto load = [&](int k0) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = k0 + 32 * h + 8 * g, have = k_hi - k;
-#pragma unroll
-        for (int j = 0; j < MT; ++j) xv[j][h] = load_chunk<VEC>(x[j] + k, have);
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          const int r = 16 * n + i;
-          av[n][h] = load_chunk<VEC>(A + r * p.lda + k, r < p.rank ? have : 0);
-        }
-      }
-    };
-    int k0 = k_lo + 64 * wave;
-    if (k0 < k_hi) load(k0);
-    for (; k0 < k_hi; k0 += 64 * W) {
-      v8 xo[MT][2], ao[NB][2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int j = 0; j < MT; ++j) xo[j][h] = __builtin_bit_cast(v8, xv[j][h]);
-#pragma unroll
-        for (int n = 0; n < NB; ++n) ao[n][h] = __builtin_bit_cast(v8, av[n][h]);
-      }
-      if (k0 + 64 * W < k_hi) load(k0 + 64 * W);
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < MT; ++j)
-#pragma unroll
-          for (int n = 0; n < NB; ++n) acc[j][n] = T16<T>::mfma16(ao[n][h], xo[j][h], acc[j][n]);
+  // rows that no sequence has: the last workgroup says so
+  if (blockIdx.x == gridDim.x - 1) {
+    if (blockIdx.y == 0) {
+      const int64_t lo = min(max((int64_t)batch.q_start[0], (int64_t)0), batch.m), hi = min(max((int64_t)batch.q_start[batch.n_seqs], lo), batch.m);
+      for (int64_t t = threadIdx.x; t < lo; t += 64 * W) p.ids[t] = kNoToken;
+      for (int64_t t = hi + threadIdx.x; t < batch.m; t += 64 * W) p.ids[t] = kNoToken;
     }
+    return;
+  }
+  int64_t t0;
+  int n, a;
+  if (!run_tile(batch, blockIdx.x, TOK, t0, n, a)) return;
+  if (blockIdx.y == 0 && (int)threadIdx.x < n) p.ids[t0 + threadIdx.x] = a;
+  const int k_lo = blockIdx.y * p.slice_k, k_hi = min(k_lo + p.slice_k, p.K);
+  if (a >= 0) {
+    const uint16_t* x[MT];
+#pragma unroll
+    for (int j = 0; j < MT; ++j) x[j] = p.X + (t0 + min(16 * j + i, n - 1)) * p.ldx;
+    f32x4_t acc[MT][NB];
+    low_product<T, NB, MT, W, VEC>(p, x, a, k_lo, k_hi, acc);
 #pragma unroll
     for (int j = 0; j < MT; ++j)
-      if (id[j] == a) {
-        mine[j] = true;
 #pragma unroll
-        for (int n = 0; n < NB; ++n) red[wave][j][n][lane] = acc[j][n];
-      }
+      for (int b = 0; b < NB; ++b) red[wave][j][b][lane] = acc[j][b];
   }
   __syncthreads();
-#pragma unroll
-  for (int u = 0; u < MT * NB; ++u) {
-    const int j = u / NB, n = u % NB;
-    const int64_t t = t0 + 16 * j + i;
-    if (u % W != wave || t >= batch.m || !(mine[j] || (id[j] < 0 && blockIdx.z == 0))) continue;
+  for (int u = wave; u < MT * NB; u += W) {
+    const int j = u / NB, b = u % NB;
+    if (16 * j + i >= n) continue;
     f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (mine[j]) {
+    if (a >= 0) {
 #pragma unroll
-      for (int w = 0; w < W; ++w) s += red[w][j][n][lane];
+      for (int w = 0; w < W; ++w) s += red[w][j][b][lane];
     }
-    *reinterpret_cast<f32x4_t*>(p.part + ((int64_t)blockIdx.y * batch.m + t) * (16 * NB) + 16 * n + 4 * g) = s;
+    *reinterpret_cast<f32x4_t*>(p.part + ((int64_t)blockIdx.y * batch.m + t0 + 16 * j + i) * (16 * NB) + 16 * b + 4 * g) = s;
+  }
+}
+
+// Steps of mixed adapters: 16 tokens, whatever their sequences; blockIdx.z takes every
+// gridDim.z-th of the tile's adapters (one after the other they would be a chain of
+// memory latencies).
+template <typename T, int NB, bool VEC>
+__global__ __launch_bounds__(256) void lora_low_steps_kernel(LowArgs p, LoraBatch batch) {
+  constexpr int W = 4;
+  __shared__ f32x4_t red[W][NB][64];
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t0 = (int64_t)blockIdx.x * 16, t = t0 + i;
+  const int id = adapter_of(batch, t0);
+  const uint16_t* const x[1] = {p.X + min(t, batch.m - 1) * p.ldx};
+  if (blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < 16 && t < batch.m) p.ids[t] = id;
+  uint64_t left = __ballot(lane < 16 && id >= 0);
+  bool mine = false;           // this workgroup sums the lane's token
+  const int k_lo = blockIdx.y * p.slice_k, k_hi = min(k_lo + p.slice_k, p.K);
+  for (uint32_t n_set = 0; left; ++n_set) {
+    const int a = next_adapter(id, left);
+    if (n_set % gridDim.z != blockIdx.z) continue;
+    f32x4_t acc[1][NB];
+    low_product<T, NB, 1, W, VEC>(p, x, a, k_lo, k_hi, acc);
+    if (id == a) {
+      mine = true;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) red[wave][b][lane] = acc[0][b];
+    }
+  }
+  __syncthreads();
+  if (t >= batch.m || !(mine || (id < 0 && blockIdx.z == 0))) return;
+  for (int b = wave; b < NB; b += W) {
+    f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (mine) {
+#pragma unroll
+      for (int w = 0; w < W; ++w) s += red[w][b][lane];
+    }
+    *reinterpret_cast<f32x4_t*>(p.part + ((int64_t)blockIdx.y * batch.m + t) * (16 * NB) + 16 * b + 4 * g) = s;
   }
 }
 
@@ -267,133 +322,261 @@ struct UpArgs {
   int y_type;
   bool vec;               // rows of Y and R allow 16-byte accesses
   int blocks;             // token blocks of a workgroup
-  int unit_waves;         // waves that share a channel group's units; the others take further channel groups
 };
 
-// Y = R + scale S B^T: a wave has 64 channels; a unit is a block of 16 tokens and
-// one of the adapters in it.  In a run of one adapter (MADE: its pieces of s are
-// there) B's operands stay in registers; in a decode step, where every unit has its
-// own, the waves share one channel group's units and make the pieces themselves.
-// Row 4 g + r of matrix block b stands for channel 16 g + 4 b + r, so a lane ends with
-// 16 neighbouring channels of one token.
-template <typename T, int NB, bool VEC, bool MADE>
-__global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(UpArgs p) {
+// Row rho of matrix block b stands for this channel of the wave's 64: a lane then has
+// eight neighbouring channels twice, 8 g .. and 32 + 8 g ..
+GPTQ_DEV int up_channel(int rho, int b) { return 32 * (b >> 1) + 8 * (rho >> 2) + 4 * (b & 1) + (rho & 3); }
+
+// Eight channels of one token: Y = R + add, R's load done by the caller where it is
+// wide.  BITS32: fp32 values, else 16-bit ones (of bf16 or fp16: `bf`).
+template <bool BITS32> struct UpRow {
+  static constexpr int kLoads = BITS32 ? 2 : 1;
+  uint4 raw[kLoads];
+  GPTQ_DEV static bool wide(const UpArgs& p, int c) { return p.vec && c + 8 <= p.d; }
+  GPTQ_DEV void load(const UpArgs& p, int64_t t, int c) {
+    if (!p.R || !wide(p, c)) return;
+    const uint4* r = reinterpret_cast<const uint4*>(static_cast<const char*>(p.R) + (t * p.ldr + c) * (BITS32 ? 4 : 2));
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) raw[q] = r[q];
+  }
+  GPTQ_DEV void finish(const UpArgs& p, int64_t t, int c, bool bf, const float (&add)[8]) const {
+    const int have = p.d - c;
+    const bool full = wide(p, c);
+    if (have <= 0) return;
+    float r[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = 0.0f;
+    if (p.R) {
+      if constexpr (BITS32) {
+        if (full) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const f32x4_t v = __builtin_bit_cast(f32x4_t, raw[BITS32 ? q : 0]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r[4 * q + e] = v[e];
+          }
+        } else {
+          load_f32<8>(static_cast<const float*>(p.R) + t * p.ldr + c, false, have, r);
+        }
+      } else if (full) {
+        const uint32_t v[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
+        auto values = [&]<typename T>() {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            r[2 * e] = lo16f<T>(v[e]);
+            r[2 * e + 1] = hi16f<T>(v[e]);
+          }
+        };
+        if (bf) values.template operator()<__bf16>();
+        else values.template operator()<_Float16>();
+      } else if (bf) {
+        load_n<__bf16, 8>(static_cast<const uint16_t*>(p.R) + t * p.ldr + c, false, have, r);
+      } else {
+        load_n<_Float16, 8>(static_cast<const uint16_t*>(p.R) + t * p.ldr + c, false, have, r);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] += add[e];
+    if constexpr (BITS32) store_f32<8>(static_cast<float*>(p.Y) + t * p.ldy + c, full, have, r);
+    else if (bf) store_n<__bf16, 8>(static_cast<uint16_t*>(p.Y) + t * p.ldy + c, full, have, r);
+    else store_n<_Float16, 8>(static_cast<uint16_t*>(p.Y) + t * p.ldy + c, full, have, r);
+  }
+};
+
+// Y = R + scale S B^T in runs: 256 channels, 64 a wave with B's rows in registers, by a
+// tile of up to 16 p.blocks tokens of one sequence, so of one adapter.  32 tokens at a
+// time the sums go through LDS, so that residual and output pass in pieces of 512
+// bytes (fp32 1 KB) of a row: stored as the matrix instruction leaves them, in pieces
+// of 64 or 128 bytes, the stores alone went at 2 TB/s.  A step's residual and pieces of
+// s are on their way while the one before it is multiplied and stored.
+template <typename T, int NB, bool VEC, bool BITS32>
+__global__ __launch_bounds__(64 * kUpWaves, NB == 8 ? 1 : (NB == 4 ? 3 : 4) - BITS32) void lora_up_runs_kernel(UpArgs p, LoraBatch batch) {
+  typedef typename T16<T>::v8 v8;
+  constexpr int kPitch = 256 + 4;                      // floats of a token's sums in LDS
+  constexpr int kRow = 32 * NB + 8;                    // 16-bit values of its pieces there
+  constexpr int kEach = 32 * 32 / (64 * kUpWaves);     // eight-channel pieces of 32 tokens, a thread
+  constexpr int kLoads = 32 * 4 * NB / (64 * kUpWaves) > 0 ? 32 * 4 * NB / (64 * kUpWaves) : 1;
+  __shared__ __attribute__((aligned(16))) float out[32 * kPitch];
+  __shared__ __attribute__((aligned(16))) uint16_t low[32 * kRow];
+  const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int groups = (p.d + 255) / 256;
+  const int c0 = 256 * (int)(blockIdx.x % groups);
+  int64_t t0;
+  int n, a;
+  if (!run_tile(batch, blockIdx.x / groups, 16 * p.blocks, t0, n, a)) return;
+  const bool bf = p.y_type == GPTQ_BF16, has = a >= 0;
+  float scale = 0.0f;
+  v8 bo[4][NB];
+  if (has) {
+    scale = p.scale[a];
+    const uint16_t* B = p.B + a * p.set;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int ch = c0 + 64 * wave + up_channel(i, b);
+#pragma unroll
+      for (int kb = 0; kb < NB; ++kb) {
+        const int r = 8 * ((4 * kb + g) % (2 * NB));
+        bo[b][kb] = __builtin_bit_cast(v8, load_chunk<VEC>(B + ch * p.ldb + r, ch < p.d ? p.rank - r : 0));
+      }
+    }
+  }
+  const int c = c0 + 8 * (tid & 31);                   // this thread's channels of the rows tid / 32 + 8 k
+  UpRow<BITS32> res[2][kEach];
+  float f[2][kEach];
+  uint4 sv[kLoads];
+  auto fetch = [&]<int TO>(int k0) {
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int64_t t = t0 + min(k0 + (tid >> 5) + 8 * k, n - 1);
+      res[TO][k].load(p, t, c);
+      f[TO][k] = has ? p.rows[t] : 0.0f;
+    }
+    if (has) {
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+        const int u = tid + 64 * kUpWaves * k, row = u / (4 * NB);
+        sv[k] = *reinterpret_cast<const uint4*>(p.pieces + (t0 + min(k0 + row, n - 1)) * (32 * NB) + 8 * (u % (4 * NB)));
+      }
+    }
+  };
+  fetch.template operator()<0>(0);
+  auto step = [&]<int CUR>(int k0) {
+    if (has) {
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+        const int u = tid + 64 * kUpWaves * k, row = u / (4 * NB);
+        if (row < 32) *reinterpret_cast<uint4*>(low + row * kRow + 8 * (u % (4 * NB))) = sv[k];
+      }
+    }
+    __syncthreads();
+    if (k0 + 32 < n) fetch.template operator()<CUR ^ 1>(k0 + 32);
+    if (has) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        f32x4_t acc[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) acc[b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int kb = 0; kb < NB; ++kb) {
+          const v8 so = *reinterpret_cast<const v8*>(low + (16 * x + i) * kRow + 8 * (4 * kb + g));
+#pragma unroll
+          for (int b = 0; b < 4; ++b) acc[b] = T16<T>::mfma16(bo[b][kb], so, acc[b]);
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          *reinterpret_cast<f32x4_t*>(out + (16 * x + i) * kPitch + 64 * wave + up_channel(4 * g, b)) = acc[b];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int row = (tid >> 5) + 8 * k;
+      if (k0 + row >= n) continue;
+      float add[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) add[e] = 0.0f;
+      if (has) {
+        load_f32<8>(out + row * kPitch + 8 * (tid & 31), true, 8, add);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) add[e] *= scale * f[CUR][k];
+      }
+      res[CUR][k].finish(p, t0 + k0 + row, c, bf, add);
+    }
+  };
+  for (int k0 = 0; k0 < n; k0 += 64) {
+    step.template operator()<0>(k0);
+    if (k0 + 32 < n) step.template operator()<1>(k0 + 32);
+  }
+}
+
+// The same where a block of tokens has several adapters: a unit is a block of 16
+// tokens and one of the adapters in it, a workgroup's waves share the units of 64
+// channels, and s's pieces are made here, from up to eight slices.
+template <typename T, int NB, bool VEC, bool BITS32>
+__global__ __launch_bounds__(64 * kUpWaves) void lora_up_steps_kernel(UpArgs p) {
   typedef typename T16<T>::v8 v8;
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int share = wave % p.unit_waves;
-  const int per = kUpWaves / p.unit_waves, groups = ((p.d + 63) / 64 + per - 1) / per;
-  const int64_t tile = blockIdx.x / groups;
-  const int c0 = 64 * (int)((blockIdx.x - tile * groups) * per + wave / p.unit_waves);
-  if (c0 >= p.d) return;
-  const bool writes_s = !MADE && p.S && c0 == 0 && share == 0;
-  v8 bo[4][NB];
-  float scale = 0.0f;
-  int have_set = kNoToken, unit = 0;
-  for (int tb = 0; tb < p.blocks; ++tb) {
-    const int64_t t = (tile * p.blocks + tb) * 16 + i;
-    if (t - i >= p.m) break;
-    const int id = t < p.m ? p.ids[t] : kNoToken;
-    uint64_t left = __ballot(id != kNoToken && lane < 16);
-    bool have_s = false;
-    v8 so[NB];
-    float row = 1.0f;
-    // this lane's chunks of its token's pieces
-    auto make_s = [&]() {
-      have_s = true;
-      if constexpr (MADE) {
-        const int64_t at = min(t, p.m - 1);
-        row = p.rows[at];
+  const int groups = (p.d + 63) / 64;
+  const int64_t t = (int64_t)(blockIdx.x / groups) * 16 + i;
+  const int c0 = 64 * (int)(blockIdx.x % groups), c = c0 + 8 * g;
+  const bool writes_s = p.S && c0 == 0 && wave == 0, bf = p.y_type == GPTQ_BF16;
+  const int64_t at = min(t, p.m - 1);
+  const int id = t < p.m ? p.ids[t] : kNoToken;
+  UpRow<BITS32> res[2];
+  if (p.Y) {
+    res[0].load(p, at, c);
+    res[1].load(p, at, c + 32);
+  }
+  // the lane's chunks of its token's pieces
+  v8 so[NB];
+  float row = 1.0f;
+  {
+    float s[NB][8], top = 0.0f;
 #pragma unroll
-        for (int kb = 0; kb < NB; ++kb) so[kb] = *reinterpret_cast<const v8*>(p.pieces + at * (32 * NB) + 8 * (4 * kb + g));
-        return;
-      }
-      float s[NB][8], top = 0.0f;
+    for (int kb = 0; kb < NB; ++kb) {
+      const int rc = (4 * kb + g) % (2 * NB);
 #pragma unroll
-      for (int kb = 0; kb < NB; ++kb) {
-        const int rc = (4 * kb + g) % (2 * NB);
+      for (int e = 0; e < 8; ++e) s[kb][e] = 0.0f;
+#pragma unroll 8
+      for (int z = 0; z < p.slices; ++z) {
+        const f32x4_t* from = reinterpret_cast<const f32x4_t*>(p.part + ((int64_t)z * p.m + at) * (16 * NB) + 8 * rc);
+        const f32x4_t lo = from[0], hi = from[1];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[kb][e] = 0.0f;
-        if (id != kNoToken) {
-#pragma unroll 4
-          for (int z = 0; z < p.slices; ++z) {
-            const f32x4_t* from = reinterpret_cast<const f32x4_t*>(p.part + ((int64_t)z * p.m + t) * (16 * NB) + 8 * rc);
-            const f32x4_t lo = from[0], hi = from[1];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              s[kb][e] += lo[e];
-              s[kb][4 + e] += hi[e];
-            }
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(s[kb][e]));
-      }
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      const float inv = piece_scale<T>(top, row);
-#pragma unroll
-      for (int kb = 0; kb < NB; ++kb) {
-        const bool low = (4 * kb + g) / (2 * NB) != 0;
-        so[kb] = __builtin_bit_cast(v8, piece_of<T>(s[kb], inv, low));
-        if (writes_s && !low && id != kNoToken) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int r = 8 * ((4 * kb + g) % (2 * NB)) + e;
-            if (r < p.rank) p.S[t * p.rank + r] = s[kb][e];
-          }
+        for (int e = 0; e < 4; ++e) {
+          s[kb][e] += lo[e];
+          s[kb][4 + e] += hi[e];
         }
       }
-    };
-    if (writes_s) make_s();
-    while (p.Y && left) {
-      const int a = next_adapter(id, left);
-      if (unit++ % p.unit_waves != share) continue;
-      if (!have_s) make_s();
-      f32x4_t acc[4];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) acc[b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-      if (a >= 0) {
-        if (a != have_set) {
-          have_set = a;
-          scale = p.scale[a];
-          const uint16_t* B = p.B + a * p.set;
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(s[kb][e]));
+    }
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float inv = piece_scale<T>(top, row);
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const int c = c0 + 16 * (i >> 2) + 4 * b + (i & 3);
+    for (int kb = 0; kb < NB; ++kb) {
+      const bool low = (4 * kb + g) / (2 * NB) != 0;
+      so[kb] = __builtin_bit_cast(v8, piece_of<T>(s[kb], inv, low));
+      if (writes_s && !low && id != kNoToken) {
 #pragma unroll
-            for (int kb = 0; kb < NB; ++kb) {
-              const int r = 8 * ((4 * kb + g) % (2 * NB));
-              bo[b][kb] = __builtin_bit_cast(v8, load_chunk<VEC>(B + c * p.ldb + r, c < p.d ? p.rank - r : 0));
-            }
-          }
+        for (int e = 0; e < 8; ++e) {
+          const int r = 8 * ((4 * kb + g) % (2 * NB)) + e;
+          if (r < p.rank) p.S[t * p.rank + r] = s[kb][e];
         }
-#pragma unroll
-        for (int kb = 0; kb < NB; ++kb)
-#pragma unroll
-          for (int b = 0; b < 4; ++b) acc[b] = T16<T>::mfma16(bo[b][kb], so[kb], acc[b]);
       }
-      if (id != a) continue;
-      const float f = a >= 0 ? scale * row : 0.0f;
+    }
+  }
+  if (!p.Y) return;
+  uint64_t left = __ballot(id != kNoToken && lane < 16);
+  for (int unit = 0; left; ++unit) {
+    const int a = next_adapter(id, left);
+    if (unit % kUpWaves != wave) continue;
+    f32x4_t acc[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int c = c0 + 16 * g + 8 * h, have = p.d - c;
-        if (have <= 0) continue;
-        const bool full = p.vec && have >= 8;
-        float r[8], y[8];
+    for (int b = 0; b < 4; ++b) acc[b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    float f = 0.0f;
+    if (a >= 0) {
+      f = p.scale[a] * row;
+      const uint16_t* B = p.B + a * p.set;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[e] = 0.0f;
-        if (p.R) {
-          if (p.y_type == GPTQ_F32) load_f32<8>(static_cast<const float*>(p.R) + t * p.ldr + c, full, have, r);
-          else if (p.y_type == GPTQ_BF16) load_n<__bf16, 8>(static_cast<const uint16_t*>(p.R) + t * p.ldr + c, full, have, r);
-          else load_n<_Float16, 8>(static_cast<const uint16_t*>(p.R) + t * p.ldr + c, full, have, r);
+      for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int ch = c0 + up_channel(i, b), r = 8 * ((4 * kb + g) % (2 * NB));
+          const v8 bo = __builtin_bit_cast(v8, load_chunk<VEC>(B + ch * p.ldb + r, ch < p.d ? p.rank - r : 0));
+          acc[b] = T16<T>::mfma16(bo, so[kb], acc[b]);
         }
+    }
+    if (id != a) continue;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = a >= 0 ? fmaf(f, acc[2 * h + (e >> 2)][e & 3], r[e]) : r[e];
-        if (p.y_type == GPTQ_F32) store_f32<8>(static_cast<float*>(p.Y) + t * p.ldy + c, full, have, y);
-        else if (p.y_type == GPTQ_BF16) store_n<__bf16, 8>(static_cast<uint16_t*>(p.Y) + t * p.ldy + c, full, have, y);
-        else store_n<_Float16, 8>(static_cast<uint16_t*>(p.Y) + t * p.ldy + c, full, have, y);
-      }
+    for (int h = 0; h < 2; ++h) {
+      float add[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) add[e] = a >= 0 ? f * acc[2 * h + (e >> 2)][e & 3] : 0.0f;
+      res[h].finish(p, t, c + 32 * h, bf, add);
     }
   }
 }
@@ -597,13 +780,16 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(OuterArgs p) {
     }
 }
 
-// out = the splits' parts in order
-__global__ __launch_bounds__(256) void lora_join_kernel(const float* __restrict__ part, int64_t split, int splits, int64_t n,
-                                                        float* __restrict__ out) {
+// the splits' parts in order: the first n0 values of a part are o0's, the others o1's (each may be NULL)
+__global__ __launch_bounds__(256) void lora_join_kernel(const float* __restrict__ part, int64_t split, int splits, int64_t n0, int64_t n,
+                                                        float* __restrict__ o0, float* __restrict__ o1) {
   for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < n; u += (int64_t)gridDim.x * 256) {
+    float* out = u < n0 ? o0 : o1;
+    if (!out) continue;
     float v = 0.0f;
+#pragma unroll 8
     for (int z = 0; z < splits; ++z) v += part[z * split + u];
-    out[u] = v;
+    out[u < n0 ? u : u - n0] = v;
   }
 }
 
@@ -638,6 +824,7 @@ static LowPlan low_plan(int64_t m, int n_seqs, int K, int nb) {
   const int n = (int)std::max<int64_t>(1, std::min<int64_t>(512 / (p.mix ? (p.tiles + 7) / 8 * 8 : p.tiles), std::min(most, p.mix ? 8 : 16)));
   p.slice_k = (most + n - 1) / n * step;
   p.slices = (K + p.slice_k - 1) / p.slice_k;
+  if (!p.mix) p.tiles += n_seqs;       // tiles that end with their sequences, and one workgroup more
   return p;
 }
 // The partial sums' part of the workspace: token ids, sums, and s's pieces with their rows' scales; room for every
@@ -659,15 +846,19 @@ static LowLayout low_layout(int64_t m, int K, int nb) {
 template <typename T>
 static int launch_low(const LowPlan& p, const LowLayout& L, int nb, bool vec, LowArgs a, const LoraBatch& b, char* base, float* S, hipStream_t s) {
   const dim3 grid((unsigned)p.tiles, (unsigned)p.slices, (unsigned)p.shares);
+  if ((int64_t)p.tiles * 512 > UINT32_MAX) return GPTQ_ERR_INVALID_ARG;
   a.slice_k = p.slice_k;
   a.ids = reinterpret_cast<int32_t*>(base);
   a.part = reinterpret_cast<float*>(base + L.off_part);
   auto go = [&]<int NB>() {
-    auto on = [&]<int MT, int W>() {
-      if (vec) lora_low_kernel<T, NB, MT, W, true><<<grid, 64 * W, 0, s>>>(a, b);
-      else lora_low_kernel<T, NB, MT, W, false><<<grid, 64 * W, 0, s>>>(a, b);
-    };
-    p.mix ? on.template operator()<1, 4>() : on.template operator()<NB == 8 ? 1 : 2, 8>();
+    constexpr int MT = NB == 8 ? 1 : 2;
+    if (p.mix) {
+      if (vec) lora_low_steps_kernel<T, NB, true><<<grid, 256, 0, s>>>(a, b);
+      else lora_low_steps_kernel<T, NB, false><<<grid, 256, 0, s>>>(a, b);
+    } else {
+      if (vec) lora_low_runs_kernel<T, NB, MT, 8, true><<<grid, 512, 0, s>>>(a, b);
+      else lora_low_runs_kernel<T, NB, MT, 8, false><<<grid, 512, 0, s>>>(a, b);
+    }
   };
   if (nb == 1) go.template operator()<1>();
   else if (nb == 2) go.template operator()<2>();
@@ -685,27 +876,28 @@ static int launch_low(const LowPlan& p, const LowLayout& L, int nb, bool vec, Lo
 
 // The second product (a.Y; a.S where the pieces are made here), from what launch_low left at base.
 template <typename T>
-static int launch_up(UpArgs a, const LowPlan& lp, const LowLayout& L, int nb, char* base, hipStream_t s) {
+static int launch_up(UpArgs a, const LowPlan& lp, const LowLayout& L, int nb, const LoraBatch& b, char* base, hipStream_t s) {
   a.part = reinterpret_cast<float*>(base + L.off_part);
   a.pieces = reinterpret_cast<uint16_t*>(base + L.off_pieces);
   a.rows = reinterpret_cast<float*>(base + L.off_rows);
   a.ids = reinterpret_cast<int32_t*>(base);
   a.slices = lp.slices;
-  a.unit_waves = lp.mix ? kUpWaves : 1;
-  const int per = kUpWaves / a.unit_waves;
   if (!a.Y) a.d = 1;
-  const int64_t groups = ((a.d + 63) / 64 + per - 1) / per;
-  // as many token blocks a workgroup (B's operands serve them all) as leave two workgroups a CU
-  a.blocks = lp.mix ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(8, (a.m + 15) / 16 * groups / 512));
-  const int64_t tiles = (a.m + 16 * a.blocks - 1) / (16 * a.blocks);
+  const int width = lp.mix ? 64 : 256;
+  const int64_t groups = (a.d + width - 1) / width;
+  // a run's tiles as long as leave four workgroups a CU, up to 128 tokens (B's rows serve them all)
+  a.blocks = lp.mix ? 1 : a.m * groups >= 128 * 1024 ? 8 : a.m * groups >= 64 * 1024 ? 4 : 2;
+  const int64_t tiles = (a.m + 16 * a.blocks - 1) / (16 * a.blocks) + (lp.mix ? 0 : b.n_seqs - 1);
   const bool vec = at16(a.B) && a.rank % 8 == 0 && a.ldb % 8 == 0 && a.set % 8 == 0;
   if (tiles * groups > (1 << 24) - 1) return GPTQ_ERR_INVALID_ARG;
+  const unsigned grid = (unsigned)(tiles * groups);
   auto go = [&]<int NB>() {
-    auto on = [&]<bool VEC>() {
-      if (lp.mix) lora_up_kernel<T, NB, VEC, false><<<(unsigned)(tiles * groups), 64 * kUpWaves, 0, s>>>(a);
-      else lora_up_kernel<T, NB, VEC, true><<<(unsigned)(tiles * groups), 64 * kUpWaves, 0, s>>>(a);
+    auto on = [&]<bool VEC, bool BITS32>() {
+      if (lp.mix) lora_up_steps_kernel<T, NB, VEC, BITS32><<<grid, 64 * kUpWaves, 0, s>>>(a);
+      else lora_up_runs_kernel<T, NB, VEC, BITS32><<<grid, 64 * kUpWaves, 0, s>>>(a, b);
     };
-    vec ? on.template operator()<true>() : on.template operator()<false>();
+    if (a.y_type == GPTQ_F32) vec ? on.template operator()<true, true>() : on.template operator()<false, true>();
+    else vec ? on.template operator()<true, false>() : on.template operator()<false, false>();
   };
   if (nb == 1) go.template operator()<1>();
   else if (nb == 2) go.template operator()<2>();
@@ -776,7 +968,7 @@ static int lora_backward(const void* dY, int64_t lddy, const void* X, int64_t ld
     u.B = at; u.scale = a->scale; u.R = R; u.Y = dX; u.S = dA ? ds : nullptr;
     u.ldb = pitch; u.set = (int64_t)a->d_in * pitch; u.ldr = ldr; u.ldy = lddx; u.m = b.m; u.rank = r; u.d = a->d_in; u.y_type = x_dtype;
     u.vec = rows_vec(R, ldr, x_dtype) && rows_vec(dX, lddx, x_dtype);
-    st = launch_up<T>(u, lp, L.low, L.nb, base, s);
+    st = launch_up<T>(u, lp, L.low, L.nb, b, base, s);
     if (st != GPTQ_OK) return st;
   }
   if (!dA && !dB) return GPTQ_OK;
@@ -800,11 +992,7 @@ static int lora_backward(const void* dY, int64_t lddy, const void* X, int64_t ld
   else lora_outer_kernel<T, 8><<<grid, 256, 0, s>>>(o);
   GPTQ_LAUNCH_CHECK();
   if (split) {
-    auto join = [&](const float* from, int64_t n, float* to) {
-      lora_join_kernel<<<(unsigned)std::min<int64_t>((n + 255) / 256, 4096), 256, 0, s>>>(from, L.out_pitch, L.splits, n, to);
-    };
-    if (dA) join(outer, na, dA);
-    if (dB) join(outer + na, nb, dB);
+    lora_join_kernel<<<(unsigned)std::min<int64_t>((na + nb + 255) / 256, 8192), 256, 0, s>>>(outer, L.out_pitch, L.splits, na, na + nb, dA, dB);
     GPTQ_LAUNCH_CHECK();
   }
   return GPTQ_OK;
@@ -846,7 +1034,7 @@ extern "C" int gptq_lora(const void* X, gptq_dtype x_dtype, int64_t m, int64_t l
   up.vec = rows_vec(R, ldr, y_dtype) && rows_vec(Y, ldy, y_dtype);
   auto go = [&]<typename T>() {
     const int st = launch_low<T>(lp, L, nb, vec, low, b, base, S, s);
-    return st != GPTQ_OK ? st : launch_up<T>(up, lp, L, nb, base, s);
+    return st != GPTQ_OK ? st : launch_up<T>(up, lp, L, nb, b, base, s);
   };
   return x_dtype == GPTQ_BF16 ? go.template operator()<__bf16>() : go.template operator()<_Float16>();
 }
@@ -867,11 +1055,9 @@ extern "C" int gptq_lora_backward(const void* dY, gptq_dtype dtype, int64_t m, i
   if (share_bytes(dA, na, dB, nb)) return GPTQ_ERR_INVALID_ARG;
   if (m == 0) {
     // sums over no tokens
-    for (auto [out, n] : {std::pair{dA, na / 4}, std::pair{dB, nb / 4}}) {
-      if (!out) continue;
-      lora_join_kernel<<<(unsigned)std::min<uint64_t>((n + 255) / 256, 4096), 256, 0, s>>>(nullptr, 0, 0, n, out);
-      GPTQ_LAUNCH_CHECK();
-    }
+    const int64_t n0 = na / 4, n = n0 + nb / 4;
+    lora_join_kernel<<<(unsigned)std::min<int64_t>((n + 255) / 256, 8192), 256, 0, s>>>(nullptr, 0, 0, n0, n, dA, dB);
+    GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
   }
   if (!dY || !q_start || !adapter || (!dX && !dA && !dB) || (R && !dX) || (dA && !X) || (dB && !S)) return GPTQ_ERR_INVALID_ARG;
