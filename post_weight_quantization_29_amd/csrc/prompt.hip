@@ -32,6 +32,7 @@ namespace gptq {
 constexpr int kRows = 128, kKeys = 64, kPromptWaves = 4;
 constexpr float kNoScore = -1e30f;       // a running maximum that has seen nothing
 constexpr float kGrow = 4.0f;            // log2 by which scores may pass the maximum before the sums are rescaled
+constexpr float kFar = 65536.0f;         // a maximum whose half step is no longer nothing beside 1
 constexpr int64_t kMaxPitch = (int64_t)1 << 22;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -187,23 +188,6 @@ template <typename T, int HD> GPTQ_DEV bool tile_has_none(uint32_t tile) {
   }
   return __any(top[0] >= E || top[1] >= E);
 }
-// Adds the tile's values that are no number, rows [lo, hi) of it (the lane's own
-// range: those that its column sees), to the lane's sums of the channels they are in.
-template <typename T, int HD> GPTQ_DEV void add_none(f32x16_t (&acc)[HD / 32], uint32_t tile, int lo, int hi) {
-  constexpr uint32_t E = T16<T>::kType == GPTQ_F16 ? 0x7C00u : 0x7F80u;
-  const int h = (threadIdx.x & 63) >> 5;
-#pragma unroll 1
-  for (int k = 0; k < kKeys; ++k)
-#pragma unroll
-    for (int c = 0; c < HD / 32; ++c)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int ch = channel_of<HD>(c, 8 * (r >> 2) + 4 * h + (r & 3));
-        const uint16_t x = *(LDS_AS const uint16_t*)(uintptr_t)(tile + k * (2 * HD) + (((ch >> 3) ^ chunk_flip<HD>(k)) << 4) + 2 * (ch & 7));
-        if ((x & E) == E && k >= lo && k < hi) acc[c][r] += (float)__builtin_bit_cast(T, x);
-      }
-}
-
 // the larger of the two halves' values of a column
 GPTQ_DEV float over_halves_max(float x) {
   const auto v = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x), false, false);
@@ -234,6 +218,47 @@ GPTQ_DEV void add_columns(f32x16_t (&acc)[HD / 32], const TileRead<HD>& rd, uint
       b.x = finite_pair<T>(b.x); b.y = finite_pair<T>(b.y);
     }
     acc[c] = T16<T>::mfma32(__builtin_bit_cast(v8, make_uint4(a.x, a.y, b.x, b.y)), pk, acc[c]);
+  }
+}
+// A value that is no number as a small one that counts it: +inf 1, -inf 128, NaN 16384.
+template <typename T> GPTQ_DEV uint32_t none_pair(uint32_t x) {
+  constexpr uint32_t E = T16<T>::kType == GPTQ_F16 ? 0x7C00u : 0x7F80u;
+  uint32_t r = 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t v = (x >> (16 * h)) & 0xFFFFu;
+    const float n = (v & E) != E ? 0.0f : (v & 0x7FFFu) != E ? 16384.0f : v >> 15 ? 128.0f : 1.0f;
+    r |= (uint32_t)bits16<T>(n) << (16 * h);
+  }
+  return r;
+}
+// Adds the tile's values that are no number where the lane's column sees them
+// (rows [lo, hi) of the tile): their numbers by channel are a product with ones.
+template <typename T, int HD> GPTQ_DEV void add_none(f32x16_t (&acc)[HD / 32], const TileRead<HD>& rd, uint32_t tile, int lo, int hi) {
+  typedef typename T16<T>::v8 v8;
+  const int h = (threadIdx.x & 63) >> 5;
+#pragma unroll
+  for (int c = 0; c < HD / 32; ++c) {
+    f32x16_t n = zeros16();
+#pragma unroll 1
+    for (int t = 0; t < 4; ++t) {
+      uint32_t see[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int k = 16 * t + 8 * (e >> 1) + 4 * h + 2 * (e & 1);
+        see[e] = pack2<T>(k >= lo && k < hi ? 1.0f : 0.0f, k + 1 >= lo && k + 1 < hi ? 1.0f : 0.0f);
+      }
+      const uint2 a = rd.four(tile, t, 0, c), b = rd.four(tile, t, 1, c);
+      n = T16<T>::mfma32(__builtin_bit_cast(v8, make_uint4(none_pair<T>(a.x), none_pair<T>(a.y), none_pair<T>(b.x), none_pair<T>(b.y))),
+                         __builtin_bit_cast(v8, make_uint4(see[0], see[1], see[2], see[3])), n);
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int x = (int)n[r];
+      if (x & 127) acc[c][r] += INFINITY;
+      if ((x >> 7) & 127) acc[c][r] -= INFINITY;
+      if (x >> 14) acc[c][r] = NAN;
+    }
   }
 }
 // eight registers of a block, 8 u .. 8 u + 7, as the operand of rows 16 (2 b + u) ..
@@ -318,67 +343,9 @@ __global__ __launch_bounds__(64 * kPromptWaves, 2) void prompt_forward_kernel(Pr
   ck.go(0, lds);
   cv.go(0, lds + kTile);
   uint32_t buf = lds, other = lds + kBuf;
-  // one tile: MASK: some of its keys are behind some of the wave's tokens
-  auto tile = [&]<bool MASK, bool FINITE>(int k0) {
-    f32x16_t s[2];
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) s[kb] = zeros16();
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) s[kb] = T16<T>::mfma32(rd.template rows<v8>(buf, kb, ks), qv[ks], s[kb]);
-    float top = -INFINITY;
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        if constexpr (MASK) s[kb][r] = k0 + 32 * kb + 8 * (r >> 2) + 4 * h + (r & 3) <= row ? s[kb][r] : -INFINITY;
-        top = fmaxf(top, s[kb][r]);
-      }
-    top = over_halves_max(top) * a.scale2;
-    if (__any(top > m + kGrow)) {
-      // only where it has grown: a token's rounding does not depend on its neighbours
-      const float m_new = top > m + kGrow ? top : m, al = __builtin_amdgcn_exp2f(m - m_new);
-      m = m_new;
-      l *= al;
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) o[c][r] *= al;
-    }
-    // One fma a score; it sees the score times scale2 unrounded and the maximum rounded, half a
-    // step apart, which is nothing until the maximum is large.
-    const float sub = kUp<T> - m;
-    const bool far = fabsf(m) > 65536.0f;
-    if (__any(far)) {
-#pragma clang fp contract(off)
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const float x = s[kb][r] * a.scale2;
-          s[kb][r] = far ? (x - m) + kUp<T> : __builtin_fmaf(s[kb][r], a.scale2, sub);
-        }
-    } else {
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s[kb][r] = fmaf(s[kb][r], a.scale2, sub);
-    }
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        float p = __builtin_amdgcn_exp2f(s[kb][r]);
-        if constexpr (MASK) p = k0 + 32 * kb + 8 * (r >> 2) + 4 * h + (r & 3) <= row ? p : 0.0f;
-        l += p;
-        s[kb][r] = p;
-      }
-#pragma unroll
-    for (int t = 0; t < 4; ++t) add_columns<T, HD, FINITE>(o, rd, buf + kTile, t, pack8<T>(s[t >> 1], t & 1));
-    if constexpr (FINITE) add_none<T, HD>(o, buf + kTile, 0, row - k0 + 1);
-  };
-  for (int k = 0; k < tiles; ++k) {
+  // the next tile's copies have landed and everybody is done with this one's
+  int k = 0;
+  auto arrive = [&]() {
     wait_copies<0>();
     wait_lds_reads();
     ring_barrier();
@@ -386,11 +353,102 @@ __global__ __launch_bounds__(64 * kPromptWaves, 2) void prompt_forward_kernel(Pr
       ck.go(kKeys * (k + 1), other);
       cv.go(kKeys * (k + 1), other + kTile);
     }
+  };
+  auto leave = [&]() {
+    const uint32_t t = buf;
+    buf = other;
+    other = t;
+    ++k;
+  };
+  auto scores = [&](f32x16_t (&s)[2]) {
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) s[kb] = zeros16();
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) s[kb] = T16<T>::mfma32(rd.template rows<v8>(buf, kb, ks), qv[ks], s[kb]);
+  };
+  // Any tile: the last one, on the diagonal; one whose scores have outgrown the
+  // maximum; one with a maximum so large that half a step of it counts.
+  auto any_tile = [&]<bool FINITE>() {
     const int k0 = kKeys * k;
-    if (k0 + kKeys <= w0 + 1) tile.template operator()<false, false>(k0);
-    else if (k0 <= w0 + 31) {
-      if (tile_has_none<T, HD>(buf + kTile)) tile.template operator()<true, true>(k0);
-      else tile.template operator()<true, false>(k0);
+    f32x16_t s[2];
+    scores(s);
+    float top = -INFINITY;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        s[kb][r] = k0 + 32 * kb + 8 * (r >> 2) + 4 * h + (r & 3) <= row ? s[kb][r] : -INFINITY;
+        top = fmaxf(top, s[kb][r]);
+      }
+    top = over_halves_max(top) * a.scale2;
+    // only where it has grown: a token's rounding does not depend on its neighbours
+    const float m_new = top > m + kGrow ? top : m, al = __builtin_amdgcn_exp2f(m - m_new);
+    m = m_new;
+    l *= al;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[c][r] *= al;
+    // One fma a score sees the score times scale2 unrounded and the maximum rounded, half
+    // a step apart, which is nothing until the maximum is large.
+    const bool far = fabsf(m) > kFar;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+#pragma clang fp contract(off)
+        const float x = s[kb][r] * a.scale2;
+        float p = __builtin_amdgcn_exp2f(far ? (x - m) + kUp<T> : __builtin_fmaf(s[kb][r], a.scale2, kUp<T> - m));
+        p = k0 + 32 * kb + 8 * (r >> 2) + 4 * h + (r & 3) <= row ? p : 0.0f;
+        l += p;
+        s[kb][r] = p;
+      }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) add_columns<T, HD, FINITE>(o, rd, buf + kTile, t, pack8<T>(s[t >> 1], t & 1));
+    if constexpr (FINITE) add_none<T, HD>(o, rd, buf + kTile, 0, row - k0 + 1);
+  };
+  // This wave's tiles: w0 / 64 whole ones, then the one on the diagonal.  The sums are
+  // rescaled outside the inner loop, which stops at a tile that asks for it: as a branch
+  // inside, the compiler kept them in two sets of registers and spilled the rest.
+  const int whole = w0 / kKeys;
+  while (k <= whole && k < tiles) {
+    arrive();
+    while (k < whole) {
+      f32x16_t s[2];
+      scores(s);
+      float top = -INFINITY;
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[kb][r]);
+      top = over_halves_max(top) * a.scale2;
+      if (__any(top > m + kGrow || fabsf(m) > kFar)) break;
+      const float sub = kUp<T> - m;
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          s[kb][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][r], a.scale2, sub));
+          l += s[kb][r];
+        }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) add_columns<T, HD, false>(o, rd, buf + kTile, t, pack8<T>(s[t >> 1], t & 1));
+      leave();
+      arrive();
+    }
+    if (k == whole && tile_has_none<T, HD>(buf + kTile)) any_tile.template operator()<true>();
+    else any_tile.template operator()<false>();
+    leave();
+  }
+  for (; k < tiles; ++k) {          // the other waves' tiles
+    wait_copies<0>();
+    wait_lds_reads();
+    ring_barrier();
+    if (k + 1 < tiles) {
+      ck.go(kKeys * (k + 1), other);
+      cv.go(kKeys * (k + 1), other + kTile);
     }
     const uint32_t t = buf;
     buf = other;
@@ -409,24 +467,28 @@ __global__ __launch_bounds__(64 * kPromptWaves, 2) void prompt_forward_kernel(Pr
 // their bits: `up` brings the lane's column into range and grows smaller when the
 // column's values outgrow it, its sums with it.  (bf16 has fp32's range.)
 template <typename T, int HD> struct Scaled {
-  float up = kScaled<T> ? 0x1p126f : 1.0f;
-  GPTQ_DEV void fit(const f32x16_t& ds, f32x16_t (&acc)[HD / 32]) {
+  float up = kScaled<T> ? 0x1p126f : 1.0f, top = 0.0f;
+  // whether a block's values are in range of `up` in all lanes
+  GPTQ_DEV bool fits(const f32x16_t& ds) {
+    if constexpr (!kScaled<T>) return true;
+    top = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) top = fmaxf(top, fabsf(ds[r]));
+    top = over_halves_max(top);
+    return !__any(top * up > 0x1p15f);
+  }
+  // a smaller `up` where they are not
+  GPTQ_DEV void shrink(f32x16_t (&acc)[HD / 32]) {
     if constexpr (kScaled<T>) {
-      float top = 0.0f;
+      const int e = (int)(__builtin_bit_cast(uint32_t, top) >> 23);
+      // top to 2^8 .. 2^9; within what a float's exponent allows
+      const float now = top * up > 0x1p15f ? __builtin_bit_cast(float, (uint32_t)min(max(262 - e, 1), 253) << 23) : up;
+      const float f = now / up;
+      up = now;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) top = fmaxf(top, fabsf(ds[r]));
-      top = over_halves_max(top);
-      if (__any(top * up > 0x1p15f)) {
-        const int e = (int)(__builtin_bit_cast(uint32_t, top) >> 23);
-        // top to 2^8 .. 2^9; within what a float's exponent allows
-        const float now = top * up > 0x1p15f ? __builtin_bit_cast(float, (uint32_t)min(max(262 - e, 1), 253) << 23) : up;
-        const float f = now / up;
-        up = now;
+      for (int c = 0; c < HD / 32; ++c)
 #pragma unroll
-        for (int c = 0; c < HD / 32; ++c)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) acc[c][r] *= f;
-      }
+        for (int r = 0; r < 16; ++r) acc[c][r] *= f;
     }
   }
   GPTQ_DEV void apply(f32x16_t& ds) const {
@@ -487,29 +549,8 @@ __global__ __launch_bounds__(64 * kPromptWaves, 2) void prompt_dq_kernel(PromptA
   Scaled<T, HD> sc;
   const int tiles = (min(r0 + kRows, n) + kKeys - 1) / kKeys;
   uint32_t buf = lds, other = lds + kBuf;
-  auto tile = [&]<bool MASK, bool FINITE>(int k0) {
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      f32x16_t s = zeros16(), dp = zeros16();
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        s = T16<T>::mfma32(rd.template rows<v8>(buf, kb, ks), qv[ks], s);
-        dp = T16<T>::mfma32(rd.template rows<v8>(buf + kTile, kb, ks), dv[ks], dp);
-      }
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const float p = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale2, -lse));
-        s[r] = p * (dp[r] - D);
-        if constexpr (MASK) s[r] = k0 + 32 * kb + 8 * (r >> 2) + 4 * h + (r & 3) <= row ? s[r] : 0.0f;
-      }
-      sc.fit(s, acc);
-      sc.apply(s);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) add_columns<T, HD, FINITE>(acc, rd, buf, 2 * kb + u, pack8<T>(s, u));
-    }
-    if constexpr (FINITE) add_none<T, HD>(acc, buf, 0, row - k0 + 1);
-  };
-  for (int k = 0; k < tiles; ++k) {
+  int k = 0;
+  auto arrive = [&]() {
     wait_copies<0>();
     wait_lds_reads();
     ring_barrier();
@@ -517,11 +558,75 @@ __global__ __launch_bounds__(64 * kPromptWaves, 2) void prompt_dq_kernel(PromptA
       ck.go(kKeys * (k + 1), other);
       cv.go(kKeys * (k + 1), other + kTile);
     }
+  };
+  auto leave = [&]() {
+    const uint32_t t = buf;
+    buf = other;
+    other = t;
+    ++k;
+  };
+  // ds of 32 keys
+  auto slopes = [&](int kb, f32x16_t& s) {
+    f32x16_t dp = zeros16();
+    s = zeros16();
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      s = T16<T>::mfma32(rd.template rows<v8>(buf, kb, ks), qv[ks], s);
+      dp = T16<T>::mfma32(rd.template rows<v8>(buf + kTile, kb, ks), dv[ks], dp);
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], a.scale2, -lse)) * (dp[r] - D);
+  };
+  // blocks kb0 .. 1 of any tile
+  auto any_tile = [&]<bool FINITE>(int kb0) {
     const int k0 = kKeys * k;
-    if (k0 + kKeys <= w0 + 1) tile.template operator()<false, false>(k0);
-    else if (k0 <= w0 + 31) {
-      if (tile_has_none<T, HD>(buf)) tile.template operator()<true, true>(k0);
-      else tile.template operator()<true, false>(k0);
+#pragma unroll 1
+    for (int kb = kb0; kb < 2; ++kb) {
+      f32x16_t s;
+      slopes(kb, s);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s[r] = k0 + 32 * kb + 8 * (r >> 2) + 4 * h + (r & 3) <= row ? s[r] : 0.0f;
+      if (!sc.fits(s)) sc.shrink(acc);
+      sc.apply(s);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) add_columns<T, HD, FINITE>(acc, rd, buf, 2 * kb + u, pack8<T>(s, u));
+    }
+    if constexpr (FINITE) add_none<T, HD>(acc, rd, buf, 0, row - k0 + 1);
+  };
+  const int whole = w0 / kKeys;
+  while (k <= whole && k < tiles) {
+    arrive();
+    int kb0 = 0;
+    while (k < whole) {
+      bool stop = false;
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        f32x16_t s;
+        slopes(kb, s);
+        if (!sc.fits(s)) {
+          kb0 = kb;
+          stop = true;
+          break;
+        }
+        sc.apply(s);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) add_columns<T, HD, false>(acc, rd, buf, 2 * kb + u, pack8<T>(s, u));
+      }
+      if (stop) break;
+      leave();
+      arrive();
+    }
+    if (k == whole && tile_has_none<T, HD>(buf)) any_tile.template operator()<true>(kb0);
+    else any_tile.template operator()<false>(kb0);
+    leave();
+  }
+  for (; k < tiles; ++k) {          // the other waves' tiles
+    wait_copies<0>();
+    wait_lds_reads();
+    ring_barrier();
+    if (k + 1 < tiles) {
+      ck.go(kKeys * (k + 1), other);
+      cv.go(kKeys * (k + 1), other + kTile);
     }
     const uint32_t t = buf;
     buf = other;
@@ -535,7 +640,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, 2) void prompt_dq_kernel(PromptA
 // a lane's registers are tokens of one key (its column), then dV^T += dO^T P and dK^T
 // += Q^T dS.
 template <typename T, int HD>
-__global__ __launch_bounds__(64 * kPromptWaves, 1) void prompt_dkv_kernel(PromptArgs a, PromptBatch q) {
+__global__ __launch_bounds__(64 * kPromptWaves, HD == 64 ? 2 : 1) void prompt_dkv_kernel(PromptArgs a, PromptBatch q) {
   typedef typename T16<T>::v8 v8;
   constexpr int KS = HD / 16, NC = HD / 32;
   constexpr uint32_t kTile = kTileBytes<HD>, kBuf = 2 * kTile + 512;
@@ -590,36 +695,55 @@ __global__ __launch_bounds__(64 * kPromptWaves, 1) void prompt_dkv_kernel(Prompt
   };
   uint32_t buf = lds, other = lds + kBuf;
   copy(0, buf);
-  // q0: the tile's first token
-  auto tile = [&]<bool MASK, bool FINITE>(int q0) {
+  int i = 0, q0 = first * kKeys;
+  auto arrive = [&]() {
+    wait_copies<0>();
+    wait_lds_reads();
+    ring_barrier();
+    if (i + 1 < total) copy(i + 1, other);
+  };
+  auto leave = [&]() {
+    const uint32_t t = buf;
+    buf = other;
+    other = t;
+    ++i;
+    q0 += kKeys;
+    if (q0 >= n) q0 = first * kKeys;
+  };
+  // p and ds of 32 tokens
+  auto slopes = [&](int qb, f32x16_t& s, f32x16_t& ds) {
+    s = zeros16();
+    ds = zeros16();
 #pragma unroll
-    for (int qb = 0; qb < 2; ++qb) {
-      f32x16_t s = zeros16(), dp = zeros16();
+    for (int ks = 0; ks < KS; ++ks) {
+      s = T16<T>::mfma32(rd.template rows<v8>(buf, qb, ks), kr[ks], s);
+      ds = T16<T>::mfma32(rd.template rows<v8>(buf + kTile, qb, ks), vr[ks], ds);
+    }
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        s = T16<T>::mfma32(rd.template rows<v8>(buf, qb, ks), kr[ks], s);
-        dp = T16<T>::mfma32(rd.template rows<v8>(buf + kTile, qb, ks), vr[ks], dp);
+    for (int g = 0; g < 4; ++g) {
+      const uint32_t at = buf + 2 * kTile + 4 * (32 * qb + 8 * g + 4 * h);
+      const f32x4_t lse = *(LDS_AS const f32x4_t*)(uintptr_t)at, D = *(LDS_AS const f32x4_t*)(uintptr_t)(at + 256);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = 4 * g + e;
+        s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], a.scale2, kShift - lse[e]));
+        ds[r] = s[r] * (ds[r] - D[e]);
       }
-      f32x16_t ds;
+    }
+  };
+  // blocks qb0 .. 1 of any tile
+  auto any_tile = [&]<bool FINITE>(int qb0) {
+#pragma unroll 1
+    for (int qb = qb0; qb < 2; ++qb) {
+      f32x16_t s, ds;
+      slopes(qb, s, ds);
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const uint32_t at = buf + 2 * kTile + 4 * (32 * qb + 8 * g + 4 * h);
-        const f32x4_t lse = *(LDS_AS const f32x4_t*)(uintptr_t)at, D = *(LDS_AS const f32x4_t*)(uintptr_t)(at + 256);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = 4 * g + e;
-          float p = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale2, kShift - lse[e]));
-          float d = p * (dp[r] - D[e]);
-          if constexpr (MASK) {
-            const bool seen = q0 + 32 * qb + 8 * g + 4 * h + e >= key;
-            p = seen ? p : 0.0f;
-            d = seen ? d : 0.0f;
-          }
-          s[r] = p;
-          ds[r] = d;
-        }
+      for (int r = 0; r < 16; ++r) {
+        const bool seen = q0 + 32 * qb + 8 * (r >> 2) + 4 * h + (r & 3) >= key;
+        s[r] = seen ? s[r] : 0.0f;
+        ds[r] = seen ? ds[r] : 0.0f;
       }
-      sc.fit(ds, dk);
+      if (!sc.fits(ds)) sc.shrink(dk);
       sc.apply(ds);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -628,25 +752,43 @@ __global__ __launch_bounds__(64 * kPromptWaves, 1) void prompt_dkv_kernel(Prompt
       }
     }
     if constexpr (FINITE) {
-      add_none<T, HD>(dv, buf + kTile, max(key - q0, 0), n - q0);
-      add_none<T, HD>(dk, buf, max(key - q0, 0), n - q0);
+      add_none<T, HD>(dv, rd, buf + kTile, max(key - q0, 0), n - q0);
+      add_none<T, HD>(dk, rd, buf, max(key - q0, 0), n - q0);
     }
   };
-  for (int i = 0; i < total; ++i) {
-    wait_copies<0>();
-    wait_lds_reads();
-    ring_barrier();
-    if (i + 1 < total) copy(i + 1, other);
-    const int q0 = (first + i % per_head) * kKeys;
-    if (q0 >= w0 + 31) tile.template operator()<false, false>(q0);
-    else if (q0 + kKeys > w0) {
-      const bool none = tile_has_none<T, HD>(buf) || tile_has_none<T, HD>(buf + kTile);
-      if (none) tile.template operator()<true, true>(q0);
-      else tile.template operator()<true, false>(q0);
+  while (i < total) {
+    arrive();
+    int qb0 = 0;
+    while (i < total && q0 >= w0 + 31) {       // tiles that see all of the wave's keys
+      bool stop = false;
+#pragma unroll
+      for (int qb = 0; qb < 2; ++qb) {
+        f32x16_t s, ds;
+        slopes(qb, s, ds);
+        if (!sc.fits(ds)) {
+          qb0 = qb;
+          stop = true;
+          break;
+        }
+        sc.apply(ds);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          add_columns<T, HD, false>(dv, rd, buf + kTile, 2 * qb + x, pack8<T>(s, x));
+          add_columns<T, HD, false>(dk, rd, buf, 2 * qb + x, pack8<T>(ds, x));
+        }
+      }
+      if (stop) break;
+      leave();
+      if (i < total) arrive();
     }
-    const uint32_t t = buf;
-    buf = other;
-    other = t;
+    if (i >= total) break;
+    if (q0 + kKeys > w0) {
+      // on the diagonal, or out of range
+      const bool none = q0 < w0 + 31 && (tile_has_none<T, HD>(buf) || tile_has_none<T, HD>(buf + kTile));
+      if (none) any_tile.template operator()<true>(qb0);
+      else any_tile.template operator()<false>(qb0);
+    }
+    leave();
   }
   if (key >= n) return;
   const float back = kScaled<T> ? 0x1p-14f : 1.0f;
