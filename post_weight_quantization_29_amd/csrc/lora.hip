@@ -1056,6 +1056,7 @@ extern "C" int gptq_lora_backward(const void* dY, gptq_dtype dtype, int64_t m, i
   if (m == 0) {
     // sums over no tokens
     const int64_t n0 = na / 4, n = n0 + nb / 4;
+    if (!dA && !dB) return GPTQ_OK;
     lora_join_kernel<<<(unsigned)std::min<int64_t>((n + 255) / 256, 8192), 256, 0, s>>>(nullptr, 0, 0, n0, n, dA, dB);
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;

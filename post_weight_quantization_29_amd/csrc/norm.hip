@@ -51,15 +51,55 @@ template <typename T> GPTQ_DEV void store8(void* p, int64_t at, bool vec, int ha
   else store_n<T, 8>(static_cast<uint16_t*>(p) + at, vec, have, v);
 }
 
+// The same as they lie, for loads that are to be under way for a while
+template <typename T> struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+  GPTQ_DEV void load(const void* p, int64_t at) {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at * (int64_t)sizeof(T));
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(T) / 2; ++k) v[k] = q[k];
+  }
+  GPTQ_DEV void get(float (&x)[8]) const {
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(T) / 2; ++k) {
+      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(T) == 4) {
+          x[4 * k + e] = __builtin_bit_cast(float, w[e]);
+        } else {
+          x[2 * e] = lo16f<T>(w[e]);
+          x[2 * e + 1] = hi16f<T>(w[e]);
+        }
+      }
+    }
+  }
+};
+
+// the sum of a wave's lanes, in all of them: inside rows of 16 by DPP, then across
+GPTQ_DEV float wave_sum(float x) {
+  auto add = [&]<int CTRL>() {
+    x += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, true));
+  };
+  add.template operator()<0xB1>();       // quad_perm 1, 0, 3, 2
+  add.template operator()<0x4E>();       // quad_perm 2, 3, 0, 1
+  add.template operator()<0x141>();      // row_half_mirror
+  add.template operator()<0x140>();      // row_mirror
+  const uint32_t b = __builtin_bit_cast(uint32_t, x);
+  const auto v = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  x = __builtin_bit_cast(float, (uint32_t)v[0]) + __builtin_bit_cast(float, (uint32_t)v[1]);
+  const uint32_t c = __builtin_bit_cast(uint32_t, x);
+  const auto w = __builtin_amdgcn_permlane32_swap(c, c, false, false);
+  return __builtin_bit_cast(float, (uint32_t)w[0]) + __builtin_bit_cast(float, (uint32_t)w[1]);
+}
+
 // Sums of N values over a row's threads, the same in all of them: over a wave's
 // lanes, then over its waves in order.  `red` is [2][16 waves][N]; a call takes
 // the half that the one before it did not, so one barrier a call is enough.
 template <int N>
 GPTQ_DEV void row_sums(float (&v)[N], float* red, int& turn, int waves) {
 #pragma unroll
-  for (int k = 0; k < N; ++k)
-#pragma unroll
-    for (int o = 32; o; o >>= 1) v[k] += __shfl_xor(v[k], o);
+  for (int k = 0; k < N; ++k) v[k] = wave_sum(v[k]);
   const int w = threadIdx.x >> 6, first = w / waves * waves;
   float* r = red + turn * 16 * N;
   turn ^= 1;
@@ -80,6 +120,35 @@ __global__ __launch_bounds__(1024) void residual_norm_kernel(NormArgs a) {
   __shared__ float red[2 * 16];
   const int group = threadIdx.x / a.T, t = threadIdx.x - group * a.T, waves = a.T >> 6;
   int turn = 0;
+  // the vectors stay in registers for all the rows that the workgroup walks (1 past the row's end)
+  float wp[NC][8], wg[NC][8], wy[NC][8];
+#pragma unroll
+  for (int k = 0; k < NC; ++k) {
+    const int c = 8 * (t + k * a.T), have = a.d - c;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) wp[k][e] = wg[k][e] = wy[k][e] = 1.0f;
+    if (have > 0) {
+      if (a.post) load_f32<8>(a.post + c, a.wvec && have >= 8, have, wp[k]);
+      if (a.gate) load_f32<8>(a.gate + c, a.wvec && have >= 8, have, wg[k]);
+      if (a.gamma && a.Y) load_f32<8>(a.gamma + c, a.wvec && have >= 8, have, wy[k]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) wg[k][e] *= a.alpha;
+  }
+  // the next row's values are on their way while a row is worked on
+  Raw8<TH> rh[NC];
+  Raw8<TB> rb[NC];
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      const int c = 8 * (t + k * a.T);
+      if (row < a.m && a.vec && a.d - c >= 8) {
+        rh[k].load(a.R, row * a.ldr + c);
+        if (a.B) rb[k].load(a.B, row * a.ldb + c);
+      }
+    }
+  };
+  fetch((int64_t)blockIdx.x * a.groups + group);
   for (int64_t row0 = (int64_t)blockIdx.x * a.groups; row0 < a.m; row0 += (int64_t)gridDim.x * a.groups) {
     const int64_t row = row0 + group;
     const bool in = row < a.m;
@@ -88,14 +157,17 @@ __global__ __launch_bounds__(1024) void residual_norm_kernel(NormArgs a) {
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
       const int c = 8 * (t + k * a.T), have = in ? a.d - c : 0;
-      const bool full = a.vec && have >= 8;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[k][e] = b[k][e] = 0.0f;
-      if (have > 0) {
-        load8<TH>(a.R, row * a.ldr + c, full, have, h[k]);
-        if (a.B) load8<TB>(a.B, row * a.ldb + c, full, have, b[k]);
+      for (int e = 0; e < 8; ++e) h[k][e] = b[k][e] = 0.0f;          // and 0 past the row's end
+      if (a.vec && have >= 8) {
+        rh[k].get(h[k]);
+        if (a.B) rb[k].get(b[k]);
+      } else if (have > 0) {
+        load8<TH>(a.R, row * a.ldr + c, false, have, h[k]);
+        if (a.B) load8<TB>(a.B, row * a.ldb + c, false, have, b[k]);
       }
     }
+    fetch(row + (int64_t)gridDim.x * a.groups);
     if (a.B) {
       float q = 1.0f;
       if (a.post) {
@@ -109,23 +181,9 @@ __global__ __launch_bounds__(1024) void residual_norm_kernel(NormArgs a) {
 #pragma unroll
       for (int k = 0; k < NC; ++k) {
         const int c = 8 * (t + k * a.T), have = in ? a.d - c : 0;
-        const bool full = a.wvec && have >= 8;
-        if (have > 0) {
-          float w[8];
-          if (a.post) {
-            load_f32<8>(a.post + c, full, have, w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) b[k][e] *= q * w[e];
-          }
-          if (a.gate) {
-            load_f32<8>(a.gate + c, full, have, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) b[k][e] *= w[e];
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) h[k][e] = fmaf(a.alpha, b[k][e], h[k][e]);
-          if (a.Hout) store8<TH>(a.Hout, row * a.ldho + c, a.vec && have >= 8, have, h[k]);
-        }
+        for (int e = 0; e < 8; ++e) h[k][e] = fmaf(b[k][e] * (q * wp[k][e]), wg[k][e], h[k][e]);
+        if (a.Hout && have > 0) store8<TH>(a.Hout, row * a.ldho + c, a.vec && have >= 8, have, h[k]);
       }
     }
     if (!a.Y) continue;
@@ -133,25 +191,15 @@ __global__ __launch_bounds__(1024) void residual_norm_kernel(NormArgs a) {
 #pragma unroll
     for (int k = 0; k < NC; ++k)
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (8 * (t + k * a.T) + e < a.d) sum[0] += h[k][e] * h[k][e];
+      for (int e = 0; e < 8; ++e) sum[0] += h[k][e] * h[k][e];
     row_sums<1>(sum, red, turn, waves);
     const float r = 1.0f / sqrtf(sum[0] / (float)a.d + a.eps);
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
       const int c = 8 * (t + k * a.T), have = in ? a.d - c : 0;
-      if (have > 0) {
-        if (a.gamma) {
-          float w[8];
-          load_f32<8>(a.gamma + c, a.wvec && have >= 8, have, w);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) h[k][e] *= r * w[e];
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) h[k][e] *= r;
-        }
-        store8<TB>(a.Y, row * a.ldyo + c, a.vec && have >= 8, have, h[k]);
-      }
+      for (int e = 0; e < 8; ++e) h[k][e] *= r * wy[k][e];
+      if (have > 0) store8<TB>(a.Y, row * a.ldyo + c, a.vec && have >= 8, have, h[k]);
     }
   }
 }
@@ -172,38 +220,78 @@ __global__ __launch_bounds__(1024) void residual_norm_backward_kernel(NormArgs a
       sg[k][e] = 0.0f;
       if constexpr (MORE) sp[k][e] = sq[k][e] = 0.0f;
     }
+  // the next row's values are on their way while a row is worked on (one chunk a
+  // thread: with two there are no registers for it)
+  constexpr bool kAhead = NC == 1;
+  Raw8<TH> rh[NC], rx[NC];
+  Raw8<TB> rg[NC], rb[NC];
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      const int c = 8 * (t + k * a.T);
+      if (row < a.m && a.vec && a.d - c >= 8) {
+        rh[k].load(a.H, row * a.ldh + c);
+        rg[k].load(a.dY, row * a.ldy + c);
+        if (a.R) rx[k].load(a.R, row * a.ldr + c);
+        if constexpr (MORE) rb[k].load(a.B, row * a.ldb + c);
+      }
+    }
+  };
+  // the vectors (1 where there is none) stay in registers likewise: loaded where they
+  // are used, four times a row, they cost as much as the rows did
+  float vg[kAhead ? NC : 1][8], vp[kAhead && MORE ? NC : 1][8], vw[kAhead && MORE ? NC : 1][8];
+  auto vector = [&](const float* v, int c, float (&w)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+    if (v && c < a.d) load_f32<8>(v + c, a.wvec && a.d - c >= 8, a.d - c, w);
+  };
+  if constexpr (kAhead) {
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      const int c = 8 * (t + k * a.T);
+      vector(a.gamma, c, vg[k]);
+      if constexpr (MORE) {
+        vector(a.post, c, vp[k]);
+        vector(a.gate, c, vw[k]);
+      }
+    }
+    fetch((int64_t)blockIdx.x * a.groups + group);
+  }
   for (int64_t row0 = (int64_t)blockIdx.x * a.groups; row0 < a.m; row0 += (int64_t)gridDim.x * a.groups) {
     const int64_t row = row0 + group;
     const bool in = row < a.m;
     float h[NC][8], g[NC][8], b[NC][8], x[NC][8];
     float sum[3] = {0.0f, 0.0f, 0.0f};
+    if constexpr (!kAhead) fetch(row);
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
       const int c = 8 * (t + k * a.T), have = in ? a.d - c : 0;
-      const bool full = a.vec && have >= 8;
 #pragma unroll
       for (int e = 0; e < 8; ++e) h[k][e] = g[k][e] = b[k][e] = x[k][e] = 0.0f;
-      if (have > 0) {
-        load8<TH>(a.H, row * a.ldh + c, full, have, h[k]);
-        load8<TB>(a.dY, row * a.ldy + c, full, have, g[k]);
-        if (a.R) load8<TH>(a.R, row * a.ldr + c, full, have, x[k]);
-        if constexpr (MORE) load8<TB>(a.B, row * a.ldb + c, full, have, b[k]);
+      if (a.vec && have >= 8) {
+        rh[k].get(h[k]);
+        rg[k].get(g[k]);
+        if (a.R) rx[k].get(x[k]);
+        if constexpr (MORE) rb[k].get(b[k]);
+      } else if (have > 0) {
+        load8<TH>(a.H, row * a.ldh + c, false, have, h[k]);
+        load8<TB>(a.dY, row * a.ldy + c, false, have, g[k]);
+        if (a.R) load8<TH>(a.R, row * a.ldr + c, false, have, x[k]);
+        if constexpr (MORE) load8<TB>(a.B, row * a.ldb + c, false, have, b[k]);
       }
     }
+    if constexpr (kAhead) fetch(row + (int64_t)gridDim.x * a.groups);
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
-      const int c = 8 * (t + k * a.T), have = in ? a.d - c : 0;
-      float w[8];
+      float other[8];
+      if constexpr (!kAhead) vector(a.gamma, 8 * (t + k * a.T), other);
+      const float (&w)[8] = kAhead ? vg[kAhead ? k : 0] : other;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = 1.0f;
-      if (a.gamma && have > 0) load_f32<8>(a.gamma + c, a.wvec && have >= 8, have, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < have) {
-          sum[0] += h[k][e] * h[k][e];
-          sum[1] += g[k][e] * w[e] * h[k][e];
-          if constexpr (MORE) sum[2] += b[k][e] * b[k][e];
-        }
+      for (int e = 0; e < 8; ++e) {          // all 0 past the row's end
+        sum[0] += h[k][e] * h[k][e];
+        sum[1] += g[k][e] * w[e] * h[k][e];
+        if constexpr (MORE) sum[2] += b[k][e] * b[k][e];
+      }
     }
     row_sums<3>(sum, red, turn, waves);
     const float r = 1.0f / sqrtf(sum[0] / (float)a.d + a.eps);
@@ -213,41 +301,35 @@ __global__ __launch_bounds__(1024) void residual_norm_backward_kernel(NormArgs a
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
       const int c = 8 * (t + k * a.T), have = in ? a.d - c : 0;
-      const bool full = a.wvec && have >= 8;
-      float w[8];
+      float other[8];
+      if constexpr (!kAhead) vector(a.gamma, c, other);
+      const float (&w)[8] = kAhead ? vg[kAhead ? k : 0] : other;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = 1.0f;
-      if (a.gamma && have > 0) load_f32<8>(a.gamma + c, full, have, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < have) {
-          const float n = h[k][e] * r;
-          sg[k][e] += g[k][e] * n;
-          x[k][e] += r * (g[k][e] * w[e] - n * mean);      // dh
-        }
+      for (int e = 0; e < 8; ++e) {
+        const float n = h[k][e] * r;
+        sg[k][e] += g[k][e] * n;
+        x[k][e] += r * (g[k][e] * w[e] - n * mean);        // dh
+      }
       if (have > 0 && a.Hout) store8<TH>(a.Hout, row * a.ldho + c, a.vec && have >= 8, have, x[k]);
       if (!a.Y && !a.want_post && !a.want_gate) continue;
       if constexpr (MORE) {
-        float wp[8], wg[8];
+        float other_p[8], other_g[8];
+        if constexpr (!kAhead) {
+          vector(a.post, c, other_p);
+          vector(a.gate, c, other_g);
+        }
+        const float (&wp)[8] = kAhead ? vp[kAhead ? k : 0] : other_p;
+        const float (&wg)[8] = kAhead ? vw[kAhead ? k : 0] : other_g;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) wp[e] = wg[e] = 1.0f;
-        if (a.post && have > 0) load_f32<8>(a.post + c, full, have, wp);
-        if (a.gate && have > 0) load_f32<8>(a.gate + c, full, have, wg);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (e < have) {
-            const float u = b[k][e] * q;
-            sq[k][e] += a.alpha * x[k][e] * (u * wp[e]);
-            const float db = a.alpha * wg[e] * x[k][e];
-            if (a.post) {
-              sp[k][e] += db * u;
-              b[k][e] = u;
-              x[k][e] = db * wp[e];
-              dot[0] += x[k][e] * u;
-            } else {
-              x[k][e] = db;
-            }
-          }
+        for (int e = 0; e < 8; ++e) {
+          b[k][e] *= q;
+          x[k][e] *= a.alpha;
+          sq[k][e] += x[k][e] * (b[k][e] * wp[e]);
+          const float db = wg[e] * x[k][e];
+          sp[k][e] += db * b[k][e];
+          x[k][e] = db * wp[e];
+          dot[0] += x[k][e] * b[k][e];
+        }
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[k][e] *= a.alpha;
@@ -298,21 +380,28 @@ __global__ __launch_bounds__(1024) void residual_norm_backward_kernel(NormArgs a
   }
 }
 
-// The workgroups' column sums in order, 64 columns a workgroup: four threads to
-// a column take every fourth part each.
-__global__ __launch_bounds__(256) void norm_columns_kernel(const float* __restrict__ part, int parts, int d, float* o0, float* o1,
-                                                           float* o2) {
-  __shared__ float s[4][64];
+// The workgroups' column sums, 64 columns a workgroup: sixteen threads to a column
+// take every sixteenth part each, and their sums are added in order.
+__global__ __launch_bounds__(1024) void norm_columns_kernel(const float* __restrict__ part, int parts, int d, float* o0, float* o1,
+                                                            float* o2) {
+  __shared__ float s[16][64];
   float* out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
   if (!out) return;
-  const int c = blockIdx.x * 64 + (threadIdx.x & 63), k = threadIdx.x >> 6;
+  const int x = threadIdx.x & 63, c = blockIdx.x * 64 + x, k = threadIdx.x >> 6;
   const int64_t pitch = (d + 3) & ~3;
   float v = 0.0f;
-  if (c < d)
-    for (int p = k; p < parts; p += 4) v += part[((int64_t)p * 3 + blockIdx.y) * pitch + c];
-  s[k][threadIdx.x & 63] = v;
+  if (c < d) {
+#pragma unroll 8
+    for (int p = k; p < parts; p += 16) v += part[((int64_t)p * 3 + blockIdx.y) * pitch + c];
+  }
+  s[k][x] = v;
   __syncthreads();
-  if (k == 0 && c < d) out[c] = (s[0][threadIdx.x] + s[1][threadIdx.x]) + (s[2][threadIdx.x] + s[3][threadIdx.x]);
+  if (k == 0 && c < d) {
+    v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) v += s[w][x];
+    out[c] = v;
+  }
 }
 
 // Threads of a row: whole waves, one chunk of eight values each up to 8192 values, then two.
@@ -324,6 +413,16 @@ static NormShape norm_shape(int d) {
   s.nc = d > 8192 ? 2 : 1;
   s.T = (d + 512 * s.nc - 1) / (512 * s.nc) * 64;
   s.groups = 1024 / s.T;
+  return s;
+}
+// Forward, where there are rows enough: two chunks a thread and one row a
+// workgroup, so that more rows are under way in a CU and fewer waves meet at a barrier.
+static NormShape forward_shape(int64_t m, int d) {
+  NormShape s = norm_shape(d);
+  if (m < 1024) return s;
+  s.nc = 2;
+  s.T = (d + 512 * s.nc - 1) / (512 * s.nc) * 64;
+  s.groups = 1;
   return s;
 }
 static int norm_parts(int64_t m, int groups) { return (int)std::min<int64_t>(kNormParts, (m + groups - 1) / groups); }
@@ -380,14 +479,14 @@ extern "C" int gptq_residual_rmsnorm(const void* R, gptq_dtype h_dtype, int64_t 
   if (!on(gamma, 4) || !on(post_gamma, 4) || !on(gate, 4)) return GPTQ_ERR_INVALID_ARG;
   if (!apart(h, y, m, d) || !same_or_apart(h, r, m, d) || !same_or_apart(h, b, m, d) || !same_or_apart(y, r, m, d) ||
       !same_or_apart(y, b, m, d)) return GPTQ_ERR_INVALID_ARG;
-  const NormShape n = norm_shape(d);
+  const NormShape n = forward_shape(m, d);
   NormArgs a{};
   a.R = R; a.B = B; a.gamma = gamma; a.post = post_gamma; a.gate = gate; a.Hout = H; a.Y = Y;
   a.ldr = ldr; a.ldb = ldb; a.ldho = ldh; a.ldyo = ldy;
   a.m = m; a.d = d; a.T = n.T; a.groups = n.groups; a.alpha = alpha; a.eps = eps;
   a.vec = wide(R, ldr, h_dtype) && wide(B, ldb, dtype) && wide(H, ldh, h_dtype) && wide(Y, ldy, dtype);
   a.wvec = on(gamma, 16) && on(post_gamma, 16) && on(gate, 16);
-  const unsigned grid = (unsigned)std::min<int64_t>((m + n.groups - 1) / n.groups, 65536);
+  const unsigned grid = (unsigned)std::min<int64_t>((m + n.groups - 1) / n.groups, 256 * std::max(1, 12 / (n.T * n.groups / 64)));
   with_types(h_dtype, dtype, [&]<typename TH, typename TB>() {
     if (n.nc == 1) residual_norm_kernel<TH, TB, 1><<<grid, n.T * n.groups, 0, s>>>(a);
     else residual_norm_kernel<TH, TB, 2><<<grid, n.T * n.groups, 0, s>>>(a);
@@ -414,7 +513,7 @@ extern "C" int gptq_residual_rmsnorm_backward(const void* dY, gptq_dtype dtype, 
   if (!on(dgamma, 4) || !on(dpost_gamma, 4) || !on(dgate, 4)) return GPTQ_ERR_INVALID_ARG;
   if (m == 0) {
     // sums over no rows
-    norm_columns_kernel<<<dim3((unsigned)((d + 63) / 64), 3), 256, 0, s>>>(nullptr, 0, d, dgamma, dpost_gamma, dgate);
+    norm_columns_kernel<<<dim3((unsigned)((d + 63) / 64), 3), 1024, 0, s>>>(nullptr, 0, d, dgamma, dpost_gamma, dgate);
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
   }
@@ -448,7 +547,7 @@ extern "C" int gptq_residual_rmsnorm_backward(const void* dY, gptq_dtype dtype, 
   });
   GPTQ_LAUNCH_CHECK();
   if (sums) {
-    norm_columns_kernel<<<dim3((unsigned)((d + 63) / 64), 3), 256, 0, s>>>(a.part, parts, d, dgamma, dpost_gamma, dgate);
+    norm_columns_kernel<<<dim3((unsigned)((d + 63) / 64), 3), 1024, 0, s>>>(a.part, parts, d, dgamma, dpost_gamma, dgate);
     GPTQ_LAUNCH_CHECK();
   }
   return GPTQ_OK;

@@ -298,6 +298,8 @@ struct PromptArgs {
   uint16_t *out, *dQ, *dK, *dV;
   float* lse;              // forward: out; backward: in
   float* rows;             // backward: [2][n_heads][n_tokens]: lse in log2, D
+  float* part;             // backward, splits > 1: [splits][dK, dV][n_tokens][n_kv][head_dim]
+  int splits;              // workgroups that share the tokens of a tile of keys
   int64_t ldq, ldk, ldv, lddo, ldo, lddq, lddk, lddv;
   int n_heads, n_kv, rep;
   float scale, scale2;     // scale2 = scale * log2 e (forward: of its absolute value)
@@ -648,7 +650,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, HD == 64 ? 2 : 1) void prompt_dk
   const uint32_t lds = (uint32_t)(uintptr_t)(LDS_AS const char*)smem;
   const int lane = threadIdx.x & 63, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int u = blockIdx.x / a.n_kv, kv = blockIdx.x - u * a.n_kv;
+  const int split = blockIdx.x % a.splits, u = blockIdx.x / a.splits / a.n_kv, kv = blockIdx.x / a.splits - u * a.n_kv;
   int b, level;
   if (!tile_at(q, u, b, level)) return;
   int64_t t0;
@@ -670,7 +672,9 @@ __global__ __launch_bounds__(64 * kPromptWaves, HD == 64 ? 2 : 1) void prompt_dk
   }
   Scaled<T, HD> sc;
   constexpr float kShift = kScaled<T> ? 14.0f : 0.0f;
-  const int first = k0 / kKeys, per_head = (n + kKeys - 1) / kKeys - first, total = per_head * a.rep;
+  // tiles of tokens, of one query head after the other; this workgroup's of them
+  const int first = k0 / kKeys, per_head = (n + kKeys - 1) / kKeys - first, all = per_head * a.rep;
+  const int share = (all + a.splits - 1) / a.splits, total = min((split + 1) * share, all);
   TileCopy<HD> cq, co;
   cq.init(a.Q + t0 * a.ldq + (int64_t)kv * a.rep * HD, a.ldq, n, wave);
   co.init(a.dO + t0 * a.lddo + (int64_t)kv * a.rep * HD, a.lddo, n, wave);
@@ -694,8 +698,9 @@ __global__ __launch_bounds__(64 * kPromptWaves, HD == 64 ? 2 : 1) void prompt_dk
     }
   };
   uint32_t buf = lds, other = lds + kBuf;
-  copy(0, buf);
-  int i = 0, q0 = first * kKeys;
+  int i = split * share;
+  if (i < total) copy(i, buf);
+  int q0 = (first + i % per_head) * kKeys;
   auto arrive = [&]() {
     wait_copies<0>();
     wait_lds_reads();
@@ -792,8 +797,60 @@ __global__ __launch_bounds__(64 * kPromptWaves, HD == 64 ? 2 : 1) void prompt_dk
   }
   if (key >= n) return;
   const float back = kScaled<T> ? 0x1p-14f : 1.0f;
+  if (a.splits > 1) {
+    const int64_t plane = q.n_tokens * a.n_kv * HD;
+    float* to = a.part + 2 * split * plane + ((t0 + key) * a.n_kv + kv) * HD;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int ch = channel_of<HD>(c, 8 * g + 4 * h);
+        const float f = a.scale * back / sc.up;
+        f32x4_t x, y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = dk[c][4 * g + e] * f;
+          y[e] = dv[c][4 * g + e] * back;
+        }
+        *reinterpret_cast<f32x4_t*>(to + ch) = x;
+        *reinterpret_cast<f32x4_t*>(to + plane + ch) = y;
+      }
+    return;
+  }
   store_row<T, HD>(a.dK + (t0 + key) * a.lddk + (int64_t)kv * HD, dk, a.scale * back / sc.up);
   store_row<T, HD>(a.dV + (t0 + key) * a.lddv + (int64_t)kv * HD, dv, back);
+}
+
+// dK and dV of a tile of keys: its splits' parts in order
+template <typename T, int HD>
+__global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs a, PromptBatch q) {
+  const int u = blockIdx.x / a.n_kv, kv = blockIdx.x - u * a.n_kv;
+  int b, level;
+  if (!tile_at(q, u, b, level)) return;
+  int64_t t0;
+  int n;
+  q.span(b, t0, n);
+  const int k0 = ((n + kRows - 1) / kRows - 1 - level) * kRows;
+  const int64_t plane = q.n_tokens * a.n_kv * HD;
+  for (int v = threadIdx.x; v < kRows * HD / 8; v += 256) {
+    const int key = k0 + v / (HD / 8), ch = 8 * (v % (HD / 8));
+    if (key >= n) break;
+    const float* from = a.part + ((t0 + key) * a.n_kv + kv) * HD + ch;
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      float s[8], x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[e] = 0.0f;
+#pragma unroll 4
+      for (int z = 0; z < a.splits; ++z) {
+        load_f32<8>(from + (2 * z + y) * plane, true, 8, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] += x[e];
+      }
+      uint16_t* out = y ? a.dV + (t0 + key) * a.lddv : a.dK + (t0 + key) * a.lddk;
+      store_n<T, 8>(out + (int64_t)kv * HD + ch, true, 8, s);
+    }
+  }
 }
 
 // ---------------------------------------------------------------- host side
@@ -829,6 +886,18 @@ static int64_t tile_bound(int64_t n_tokens, int n_seqs, int max_len) {
   return std::min((n_tokens + kRows - 1) / kRows + n_seqs - 1, (int64_t)n_seqs * ((max_len + kRows - 1) / kRows));
 }
 
+// Workgroups that share a tile of keys' tokens: up to four a CU in all, up to
+// eight, with four tiles of tokens each at least.  A few long sequences of few kv heads
+// leave most of the chip idle otherwise (13 ragged sequences up to 2900, 4 kv heads: 343
+// us for the kernel whole, see below for split).  Their parts: at most kPartRows rows of
+// one kv head's dK and dV.
+constexpr int64_t kPartRows = 1024 * kRows;
+static int key_splits(int64_t tiles, int n_kv, int rep, int max_len) {
+  const int64_t s = std::min<int64_t>(1023 / (tiles * n_kv), (int64_t)rep * ((max_len + kKeys - 1) / kKeys) / 4);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(s, 8));
+}
+static size_t rows_part(int64_t n_tokens, int n_heads) { return align_up((size_t)2 * n_heads * n_tokens * sizeof(float)); }
+
 }  // namespace gptq
 
 using namespace gptq;
@@ -863,7 +932,7 @@ extern "C" int gptq_prompt_attention(const void* Q, const void* K, const void* V
 
 extern "C" size_t gptq_prompt_attention_backward_workspace_size(int64_t n_tokens, int32_t n_heads) {
   if (n_tokens <= 0 || n_tokens > INT_MAX || n_heads <= 0 || n_heads >= kMaxPitch) return 0;
-  return align_up((size_t)2 * n_heads * n_tokens * sizeof(float));
+  return rows_part(n_tokens, n_heads) + align_up((size_t)std::min<int64_t>(8 * n_tokens * n_heads, kPartRows) * 2 * 128 * sizeof(float));
 }
 
 extern "C" int gptq_prompt_attention_backward(const void* dOut, int64_t lddo, const void* Q, const void* K, const void* V,
@@ -898,10 +967,13 @@ extern "C" int gptq_prompt_attention_backward(const void* dOut, int64_t lddo, co
   a.ldq = ldq; a.ldk = ldk; a.ldv = ldv; a.lddo = lddo; a.ldo = ldo; a.lddq = lddq; a.lddk = lddk; a.lddv = lddv;
   a.n_heads = n_heads; a.n_kv = n_kv_heads; a.rep = n_heads / n_kv_heads;
   a.scale = scale; a.scale2 = scale * kLog2e;
+  a.splits = key_splits(tiles, n_kv_heads, a.rep, max_len);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + rows_part(n_tokens, n_heads));
   const PromptBatch b{q_start, n_tokens, n_seqs, max_len};
   auto go = [&]<typename T, int HD>() {
     prompt_dq_kernel<T, HD><<<(unsigned)(tiles * n_heads), 64 * kPromptWaves, 0, s>>>(a, b);
-    prompt_dkv_kernel<T, HD><<<(unsigned)(tiles * n_kv_heads), 64 * kPromptWaves, 0, s>>>(a, b);
+    prompt_dkv_kernel<T, HD><<<(unsigned)(tiles * n_kv_heads * a.splits), 64 * kPromptWaves, 0, s>>>(a, b);
+    if (a.splits > 1) prompt_join_kernel<T, HD><<<(unsigned)(tiles * n_kv_heads), 256, 0, s>>>(a, b);
   };
   if (dtype == GPTQ_BF16) head_dim == 128 ? go.template operator()<__bf16, 128>() : go.template operator()<__bf16, 64>();
   else head_dim == 128 ? go.template operator()<_Float16, 128>() : go.template operator()<_Float16, 64>();
