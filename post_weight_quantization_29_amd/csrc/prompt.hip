@@ -318,8 +318,9 @@ template <typename T, int HD>
 __global__ __launch_bounds__(64 * kPromptWaves, 2) void prompt_forward_kernel(PromptArgs a, PromptBatch q) {
   typedef typename T16<T>::v8 v8;
   constexpr int KS = HD / 16, NC = HD / 32;
-  constexpr uint32_t kTile = kTileBytes<HD>, kBuf = 2 * kTile;
-  __shared__ __attribute__((aligned(1024))) char smem[2 * kBuf];
+  // LDS: three tiles of keys and two of values (two workgroups a CU take all of it)
+  constexpr uint32_t kTile = kTileBytes<HD>, kV = 3 * kTile;
+  __shared__ __attribute__((aligned(1024))) char smem[5 * kTile];
   const uint32_t lds = (uint32_t)(uintptr_t)(LDS_AS const char*)smem;
   const int lane = threadIdx.x & 63, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -330,61 +331,65 @@ __global__ __launch_bounds__(64 * kPromptWaves, 2) void prompt_forward_kernel(Pr
   q.span(b, t0, n);
   const int r0 = level * kRows, w0 = r0 + 32 * wave, row = w0 + (lane & 31);
   const int kv = head / a.rep;
-  v8 qv[KS];
-  load_row<T, HD>(qv, a.Q + (t0 + min(row, n - 1)) * a.ldq + (int64_t)head * HD, a.flip);
+  const int tiles = (min(r0 + kRows, n) + kKeys - 1) / kKeys;
   TileCopy<HD> ck, cv;
   ck.init(a.K + t0 * a.ldk + (int64_t)kv * HD, a.ldk, n, wave);
   cv.init(a.V + t0 * a.ldv + (int64_t)kv * HD, a.ldv, n, wave);
+  // where tile k's, k + 1's and k + 2's keys are, and tile k's values
+  uint32_t keys = lds, keys1 = lds + kTile, keys2 = lds + 2 * kTile, values = lds + kV, values1 = lds + kV + kTile;
+  ck.go(0, keys);
+  cv.go(0, values);
+  if (tiles > 1) ck.go(kKeys, keys1);
+  v8 qv[KS];
+  load_row<T, HD>(qv, a.Q + (t0 + min(row, n - 1)) * a.ldq + (int64_t)head * HD, a.flip);
   TileRead<HD> rd;
   rd.init();
   f32x16_t o[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) o[c] = zeros16();
   float m = kNoScore, l = 0.0f;
-  const int tiles = (min(r0 + kRows, n) + kKeys - 1) / kKeys;
-  ck.go(0, lds);
-  cv.go(0, lds + kTile);
-  uint32_t buf = lds, other = lds + kBuf;
-  // the next tile's copies have landed and everybody is done with this one's
   int k = 0;
+  // Tile k + 1's keys and tile k's values have landed, and everybody is done with tile
+  // k - 1's of both.
   auto arrive = [&]() {
     wait_copies<0>();
     wait_lds_reads();
     ring_barrier();
-    if (k + 1 < tiles) {
-      ck.go(kKeys * (k + 1), other);
-      cv.go(kKeys * (k + 1), other + kTile);
-    }
+    if (k + 2 < tiles) ck.go(kKeys * (k + 2), keys2);
+    if (k + 1 < tiles) cv.go(kKeys * (k + 1), values1);
   };
   auto leave = [&]() {
-    const uint32_t t = buf;
-    buf = other;
-    other = t;
+    const uint32_t x = keys, y = values;
+    keys = keys1;
+    keys1 = keys2;
+    keys2 = x;
+    values = values1;
+    values1 = y;
     ++k;
   };
-  auto scores = [&](f32x16_t (&s)[2]) {
+  // raw scores of 32 keys: block kb of the tile at `from`
+  auto scores = [&](uint32_t from, int kb) {
+    f32x16_t s = zeros16();
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) s[kb] = zeros16();
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) s[kb] = T16<T>::mfma32(rd.template rows<v8>(buf, kb, ks), qv[ks], s[kb]);
+    for (int ks = 0; ks < KS; ++ks) s = T16<T>::mfma32(rd.template rows<v8>(from, kb, ks), qv[ks], s);
+    return s;
   };
-  // Any tile: the last one, on the diagonal; one whose scores have outgrown the
-  // maximum; one with a maximum so large that half a step of it counts.
-  auto any_tile = [&]<bool FINITE>() {
-    const int k0 = kKeys * k;
-    f32x16_t s[2];
-    scores(s);
+  auto top_of = [&](const f32x16_t& s) {
     float top = -INFINITY;
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+    for (int r = 0; r < 16; ++r) top = fmaxf(top, s[r]);
+    return over_halves_max(top) * a.scale2;
+  };
+  // This wave's tiles: w0 / 64 whole ones, then the one on the diagonal.  (A wave behind
+  // the sequence's end has none.)
+  const int last = w0 < n ? w0 / kKeys : -1;
+  // Block kb, of scores s, of any tile: the last one, on the diagonal; one whose scores have
+  // outgrown the maximum; one with a maximum so large that half a step of it counts.
+  auto any_block = [&]<bool FINITE>(int kb, f32x16_t s) {
+    const int k0 = kKeys * k + 32 * kb;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        s[kb][r] = k0 + 32 * kb + 8 * (r >> 2) + 4 * h + (r & 3) <= row ? s[kb][r] : -INFINITY;
-        top = fmaxf(top, s[kb][r]);
-      }
-    top = over_halves_max(top) * a.scale2;
+    for (int r = 0; r < 16; ++r) s[r] = k0 + 8 * (r >> 2) + 4 * h + (r & 3) <= row ? s[r] : -INFINITY;
+    const float top = top_of(s);
     // only where it has grown: a token's rounding does not depend on its neighbours
     const float m_new = top > m + kGrow ? top : m, al = __builtin_amdgcn_exp2f(m - m_new);
     m = m_new;
@@ -397,65 +402,104 @@ __global__ __launch_bounds__(64 * kPromptWaves, 2) void prompt_forward_kernel(Pr
     // a step apart, which is nothing until the maximum is large.
     const bool far = fabsf(m) > kFar;
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
+    for (int r = 0; r < 16; ++r) {
 #pragma clang fp contract(off)
-        const float x = s[kb][r] * a.scale2;
-        float p = __builtin_amdgcn_exp2f(far ? (x - m) + kUp<T> : __builtin_fmaf(s[kb][r], a.scale2, kUp<T> - m));
-        p = k0 + 32 * kb + 8 * (r >> 2) + 4 * h + (r & 3) <= row ? p : 0.0f;
-        l += p;
-        s[kb][r] = p;
-      }
+      const float x = s[r] * a.scale2;
+      float p = __builtin_amdgcn_exp2f(far ? (x - m) + kUp<T> : __builtin_fmaf(s[r], a.scale2, kUp<T> - m));
+      p = k0 + 8 * (r >> 2) + 4 * h + (r & 3) <= row ? p : 0.0f;
+      l += p;
+      s[r] = p;
+    }
 #pragma unroll
-    for (int t = 0; t < 4; ++t) add_columns<T, HD, FINITE>(o, rd, buf + kTile, t, pack8<T>(s[t >> 1], t & 1));
-    if constexpr (FINITE) add_none<T, HD>(o, rd, buf + kTile, 0, row - k0 + 1);
+    for (int u = 0; u < 2; ++u) add_columns<T, HD, FINITE>(o, rd, values, 2 * kb + u, pack8<T>(s, u));
   };
-  // This wave's tiles: w0 / 64 whole ones, then the one on the diagonal.  The sums are
-  // rescaled outside the inner loop, which stops at a tile that asks for it: as a branch
-  // inside, the compiler kept them in two sets of registers and spilled the rest.
-  const int whole = w0 / kKeys;
-  while (k <= whole && k < tiles) {
-    arrive();
-    while (k < whole) {
-      f32x16_t s[2];
-      scores(s);
-      float top = -INFINITY;
+  // Block KB of a whole tile: the next block's scores (of keys at `from`) are made while this
+  // one's exponentials are, and their largest is looked for during the second product:
+  // neither depends on what it stands beside, and the matrix pipe has as much to do as the
+  // vector one.  Operands are read four products ahead; the order is the source's (left to
+  // itself the compiler brings the reads together in front and spills, and a reload in the
+  // loop waits for every copy under way).
+  float top = 0.0f;                        // the largest of the next block's scores times scale2
+  auto whole_block = [&]<int KB>(uint32_t from, f32x16_t& s, f32x16_t& next) {
+    constexpr int EX = 16 / KS, NP = 2 * NC, MX = 16 / NP;
+    const float sub = kUp<T> - m;
+    auto value = [&](int y) {
+      const uint2 u = rd.four(values, 2 * KB + y / NC, 0, y % NC), w = rd.four(values, 2 * KB + y / NC, 1, y % NC);
+      return __builtin_bit_cast(v8, make_uint4(u.x, u.y, w.x, w.y));
+    };
+    v8 kf[4], vf[4];
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+    for (int x = 0; x < 4; ++x) kf[x] = rd.template rows<v8>(from, 1 - KB, x);
+    f32x16_t z = zeros16();
 #pragma unroll
-        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[kb][r]);
-      top = over_halves_max(top) * a.scale2;
-      if (__any(top > m + kGrow || fabsf(m) > kFar)) break;
-      const float sub = kUp<T> - m;
+    for (int x = 0; x < KS; ++x) {
+      z = T16<T>::mfma32(kf[x & 3], qv[x], z);
+      if (x + 4 < KS) kf[x & 3] = rd.template rows<v8>(from, 1 - KB, x + 4);
+      else vf[x + 4 - KS] = value(x + 4 - KS);
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+      for (int e = EX * x; e < EX * (x + 1); ++e) {
+        s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], a.scale2, sub));
+        l += s[e];
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    top = -INFINITY;
+    v8 pk = pack8<T>(s, 0);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          s[kb][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][r], a.scale2, sub));
-          l += s[kb][r];
-        }
+    for (int y = 0; y < NP; ++y) {
+      o[y % NC] = T16<T>::mfma32(vf[y & 3], pk, o[y % NC]);
+      if (y + 4 < NP) vf[y & 3] = value(y + 4);
+      if (y == NC - 1) pk = pack8<T>(s, 1);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) add_columns<T, HD, false>(o, rd, buf + kTile, t, pack8<T>(s[t >> 1], t & 1));
+      for (int e = MX * y; e < MX * (y + 1); ++e) top = fmaxf(top, z[e]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    next = z;
+    top = over_halves_max(top) * a.scale2;
+  };
+  // The sums are rescaled outside the inner loop, which stops at a block that asks for it: as a
+  // branch inside, the compiler kept them in two sets of registers and spilled the rest.
+  f32x16_t s0, s1;
+  wait_copies<0>();
+  ring_barrier();
+  if (last >= 0) {
+    s0 = scores(keys, 0);
+    top = top_of(s0);
+  }
+  arrive();
+  while (k <= last) {
+    auto plain = [&]() { return !__any(top > m + kGrow || fabsf(m) > kFar); };
+    int kb = 0;
+    while (k < last) {
+      if (!plain()) break;
+      whole_block.template operator()<0>(keys, s0, s1);
+      kb = 1;
+      if (!plain()) break;
+      whole_block.template operator()<1>(keys1, s1, s0);
+      kb = 0;
       leave();
       arrive();
     }
-    if (k == whole && tile_has_none<T, HD>(buf + kTile)) any_tile.template operator()<true>();
-    else any_tile.template operator()<false>();
-    leave();
-  }
-  for (; k < tiles; ++k) {          // the other waves' tiles
-    wait_copies<0>();
-    wait_lds_reads();
-    ring_barrier();
-    if (k + 1 < tiles) {
-      ck.go(kKeys * (k + 1), other);
-      cv.go(kKeys * (k + 1), other + kTile);
+    // the rest of the tile, block by block
+    const bool none = k == last && tile_has_none<T, HD>(values);
+    f32x16_t s = kb ? s1 : s0;
+#pragma unroll 1
+    for (;;) {
+      if (none) any_block.template operator()<true>(kb, s);
+      else any_block.template operator()<false>(kb, s);
+      if (kb == 1) break;
+      s = scores(keys, 1);
+      kb = 1;
     }
-    const uint32_t t = buf;
-    buf = other;
-    other = t;
+    if (none) add_none<T, HD>(o, rd, values, 0, row - kKeys * k + 1);
+    if (k < last) {
+      s0 = scores(keys1, 0);
+      top = top_of(s0);
+    }
+    leave();
+    if (k < tiles) arrive();
   }
+  for (leave(); k < tiles; leave()) arrive();          // the other waves' tiles
   l = over_halves_sum(l);
   if (row >= n) return;
   // a score whose log2 is beyond fp32 leaves l 0 (or no number): then so is the row
