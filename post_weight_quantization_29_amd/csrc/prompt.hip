@@ -51,6 +51,12 @@ struct PromptBatch {
     t0 = a;
     n = (int)min(max(e - a, (int64_t)0), (int64_t)max_len);
   }
+  // the same for a sequence that is one for the whole wave, in scalar registers
+  GPTQ_DEV void span_of(int b, int64_t& t0, int& n) const {
+    span(b, t0, n);
+    t0 = __builtin_amdgcn_readfirstlane((int)t0);       // rows fit 31 bits
+    n = __builtin_amdgcn_readfirstlane(n);
+  }
 };
 
 // The u-th tile (of kRows tokens) of the batch in the order of falling numbers of
@@ -198,12 +204,7 @@ GPTQ_DEV float over_halves_sum(float x) {
   return __builtin_bit_cast(float, (uint32_t)v[0]) + __builtin_bit_cast(float, (uint32_t)v[1]);
 }
 
-GPTQ_DEV f32x16_t zeros16() {
-  f32x16_t z;
-#pragma unroll
-  for (int r = 0; r < 16; ++r) z[r] = 0.0f;
-  return z;
-}
+GPTQ_DEV f32x16_t zeros16() { return f32x16_t{}; }
 
 // acc[c] += A^T B over 64 rows of the tile: A's columns by transposing reads, B the
 // columns' registers in pairs (pk[t] the 16 rows 16 t ..)
@@ -559,7 +560,8 @@ __global__ __launch_bounds__(64 * kPromptWaves, 2) void prompt_dq_kernel(PromptA
   if (!head_tile(a, q, b, level, head)) return;
   int64_t t0;
   int n;
-  q.span(b, t0, n);
+  q.span_of(b, t0, n);
+  level = __builtin_amdgcn_readfirstlane(level);
   const int r0 = level * kRows, w0 = r0 + 32 * wave, row = w0 + (lane & 31);
   const int kv = head / a.rep;
   const int64_t tok = t0 + min(row, n - 1);
@@ -699,7 +701,8 @@ __global__ __launch_bounds__(64 * kPromptWaves, HD == 64 ? 2 : 1) void prompt_dk
   if (!tile_at(q, u, b, level)) return;
   int64_t t0;
   int n;
-  q.span(b, t0, n);
+  q.span_of(b, t0, n);
+  level = __builtin_amdgcn_readfirstlane(level);
   // the levels count from the sequence's end here
   const int k0 = ((n + kRows - 1) / kRows - 1 - level) * kRows, w0 = k0 + 32 * wave, key = w0 + (lane & 31);
   const int64_t tok = t0 + min(key, n - 1);
@@ -873,7 +876,8 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs a, PromptBa
   if (!tile_at(q, u, b, level)) return;
   int64_t t0;
   int n;
-  q.span(b, t0, n);
+  q.span_of(b, t0, n);
+  level = __builtin_amdgcn_readfirstlane(level);
   const int k0 = ((n + kRows - 1) / kRows - 1 - level) * kRows;
   const int64_t plane = q.n_tokens * a.n_kv * HD;
   for (int v = threadIdx.x; v < kRows * HD / 8; v += 256) {
@@ -930,15 +934,16 @@ static int64_t tile_bound(int64_t n_tokens, int n_seqs, int max_len) {
   return std::min((n_tokens + kRows - 1) / kRows + n_seqs - 1, (int64_t)n_seqs * ((max_len + kRows - 1) / kRows));
 }
 
-// Workgroups that share a tile of keys' tokens: up to four a CU in all, up to
+// Workgroups that share the tokens of a tile of keys: up to four a CU in all, up to
 // eight, with four tiles of tokens each at least.  A few long sequences of few kv heads
-// leave most of the chip idle otherwise (13 ragged sequences up to 2900, 4 kv heads: 343
-// us for the kernel whole, see below for split).  Their parts: at most kPartRows rows of
-// one kv head's dK and dV.
+// leave most of the chip idle otherwise: 13 ragged sequences up to 2900 of 4 kv heads took
+// 343 us whole, 104 us split, and 13 us to join them; from four workgroups a CU on there is
+// nothing to gain.  The parts hold a row for each row of the batch, in sequences or not, so
+// their number is what kPartRows rows of one kv head's dK and dV leave room for.
 constexpr int64_t kPartRows = 1024 * kRows;
-static int key_splits(int64_t tiles, int n_kv, int rep, int max_len) {
+static int key_splits(int64_t tiles, int64_t n_tokens, int n_kv, int rep, int max_len) {
   const int64_t s = std::min<int64_t>(1023 / (tiles * n_kv), (int64_t)rep * ((max_len + kKeys - 1) / kKeys) / 4);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(s, 8));
+  return (int)std::max<int64_t>(1, std::min({s, (int64_t)8, kPartRows / (n_tokens * n_kv)}));
 }
 static size_t rows_part(int64_t n_tokens, int n_heads) { return align_up((size_t)2 * n_heads * n_tokens * sizeof(float)); }
 
@@ -1011,7 +1016,7 @@ extern "C" int gptq_prompt_attention_backward(const void* dOut, int64_t lddo, co
   a.ldq = ldq; a.ldk = ldk; a.ldv = ldv; a.lddo = lddo; a.ldo = ldo; a.lddq = lddq; a.lddk = lddk; a.lddv = lddv;
   a.n_heads = n_heads; a.n_kv = n_kv_heads; a.rep = n_heads / n_kv_heads;
   a.scale = scale; a.scale2 = scale * kLog2e;
-  a.splits = key_splits(tiles, n_kv_heads, a.rep, max_len);
+  a.splits = key_splits(tiles, n_tokens, n_kv_heads, a.rep, max_len);
   a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + rows_part(n_tokens, n_heads));
   const PromptBatch b{q_start, n_tokens, n_seqs, max_len};
   auto go = [&]<typename T, int HD>() {

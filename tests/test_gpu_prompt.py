@@ -239,3 +239,26 @@ def test_gradient_against_differences(P):
         diff = (loss(*up) - loss(*down)) / 2e-5
         # four roundings to fp16 (p, ds, out in D, the result) of terms that are not far larger than what they add up to
         assert abs(float((g.double() * v).sum() - diff)) <= 4 * 4 * 2.0 ** -11 * float((g.double() * v).abs().sum()) + 1e-5
+
+
+@pytest.mark.parametrize("rows,cut", [(40000, 512), (40000, 200), (131073, 512)])
+def test_many_rows_behind_the_batch(P, rows, cut):
+    """Tiles of keys whose tokens several workgroups share: their parts have a row for each row there is, in a workspace of
+    exactly its size."""
+    H, n_kv, hd, start = 8, 1, 128, [0, 500, 512]
+    Q, K, V = inputs(rows, H, n_kv, hd, BF)
+    out, lse = forward(P, Q, K, V, start, cut)
+    dO = rand((rows, H, hd), BF, 9, 0.1)
+    size = P.gptq_prompt_attention_backward_workspace_size(rows, H)
+    whole = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    d = [torch.full_like(t, 7.0) for t in (Q, K, V)]
+    P.gptq_prompt_attention_backward(dO, Q, K, V, out, lse, i32(start), cut, *d, ws=whole[:size])
+    assert bool((whole[size:] == 0xA5).all())
+    few = [t[:520] for t in (dO, Q, K, V, out, lse)]
+    ref = R.prompt_backward64(*few, start, hd ** -0.5, cut)
+    live = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    live[:cut if cut < 500 else 512] = True
+    live[500:512] = True
+    for x, name in zip(d, ("dq", "dk", "dv")):
+        R.within(x[live], ref[name][0][live[:520]], ref[name][1][live[:520]], name)
+        assert bool((x[~live] == 7).all())
