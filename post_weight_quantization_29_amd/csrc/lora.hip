@@ -641,15 +641,17 @@ GPTQ_DEV uint2 read_transposed(uint32_t at) {
 
 // scale sum_t X[t][c] S[t][r] over one adapter's tokens: 128 channels by all ranks
 // a workgroup, 32 tokens a step.  Both operands want the tokens next to each
-// other: X goes to LDS as it lies and is read transposed, S in bf16 pieces (two: 16
-// bits) with tokens innermost.  fp16 channels are two bf16 values exactly.
+// other: X goes to LDS as it lies and is read transposed, S in three bf16 pieces
+// (24 bits; two cost an error twice that of fp32 sums) with tokens innermost.  fp16 channels
+// are two bf16 values exactly; the second one's product with the third piece, 2^-27 of
+// the whole, is left out.
 template <typename T, int NB>
 __global__ __launch_bounds__(256) void lora_outer_kernel(OuterArgs p) {
   typedef typename T16<__bf16>::v8 b8;
   constexpr bool kSplitX = T16<T>::kType == GPTQ_F16;
   constexpr int kPitch = 40;                         // tokens of a rank's row in LDS: 80 bytes
   __shared__ __attribute__((aligned(1024))) uint16_t xs[2 * 32 * 128];
-  __shared__ __attribute__((aligned(16))) uint16_t ss[2 * 2 * 16 * NB * kPitch];
+  __shared__ __attribute__((aligned(16))) uint16_t ss[2 * 3 * 16 * NB * kPitch];
   const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const bool is_b = (int)blockIdx.x >= p.side[0].tiles;
@@ -695,7 +697,7 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(OuterArgs p) {
   for (int64_t t0 = t_lo; t0 < t_hi; t0 += 32) {
     const uint32_t next = (uint32_t)__ballot(next_ids == a), some = now;
     uint16_t* xb = xs + (turn & 1) * (32 * 128);
-    uint16_t* sb = ss + (turn & 1) * (2 * 16 * NB * kPitch);
+    uint16_t* sb = ss + (turn & 1) * (3 * 16 * NB * kPitch);
     if (some) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -705,11 +707,14 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(OuterArgs p) {
 #pragma unroll
       for (int k = 0; k < 2 * NB; ++k) {
         const int u = tid + 256 * k, t = u / (16 * NB), r = u % (16 * NB);
-        const float v = scale * sv[k];
-        const uint16_t hi = bits16<__bf16>((some >> t) & 1 ? v : 0.0f);
-        const float hf = (float)__builtin_bit_cast(__bf16, hi);
-        sb[r * kPitch + t] = hi;
-        sb[16 * NB * kPitch + r * kPitch + t] = bits16<__bf16>(((some >> t) & 1) && fabsf(hf) < INFINITY ? v - hf : 0.0f);
+        float v = (some >> t) & 1 ? scale * sv[k] : 0.0f;
+#pragma unroll
+        for (int z = 0; z < 3; ++z) {
+          const uint16_t piece = bits16<__bf16>(v);
+          const float f = (float)__builtin_bit_cast(__bf16, piece);
+          sb[(16 * NB * z + r) * kPitch + t] = piece;
+          v = fabsf(f) < INFINITY ? v - f : 0.0f;
+        }
       }
     }
     if (next) load(t0 + 32, next);
@@ -748,17 +753,18 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(OuterArgs p) {
     }
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-      b8 so[2];
+      b8 so[3];
 #pragma unroll
-      for (int z = 0; z < 2; ++z) so[z] = *reinterpret_cast<const b8*>(sb + (16 * NB * z + 16 * n + i) * kPitch + 8 * g);
+      for (int z = 0; z < 3; ++z) so[z] = *reinterpret_cast<const b8*>(sb + (16 * NB * z + 16 * n + i) * kPitch + 8 * g);
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         auto product = [&](const b8& x, const b8& s) {
           // dA: rows are channels, so that a lane has four channels of one rank; dB: four ranks of one channel
           acc[b][n] = is_b ? T16<__bf16>::mfma16(s, x, acc[b][n]) : T16<__bf16>::mfma16(x, s, acc[b][n]);
         };
-        product(xo[b][0], so[0]);
+        product(xo[b][0], so[2]);
         product(xo[b][0], so[1]);
+        product(xo[b][0], so[0]);
         if constexpr (kSplitX) {
           product(xo[b][kSplitX ? 1 : 0], so[0]);
           product(xo[b][kSplitX ? 1 : 0], so[1]);

@@ -123,7 +123,7 @@ def lora_backward64(dY, X, S, A, B, scale, ids, R, dtype):
     dx = torch.zeros((m, A.shape[2]), dtype=torch.float64, device=dY.device)
     edx, da, db = torch.zeros_like(dx), torch.zeros_like(A), torch.zeros_like(B)
     eda, edb = torch.zeros_like(A), torch.zeros_like(B)
-    two = 2.0 ** -16                                     # S and dS enter dA's and dB's products in two bf16 pieces
+    cut = 2.0 ** -24                                     # S and dS enter dA's and dB's products in three bf16 pieces
     for a in sorted(set(ids.tolist()) - {-1, -2}):
         t = (ids == a).to(dY.device)
         ds = dY[t] @ B[a]
@@ -133,9 +133,9 @@ def lora_backward64(dY, X, S, A, B, scale, ids, R, dtype):
         edx[t] = scale[a].abs() * ((e + piece_error(ds, dtype)) @ A[a].abs() + (2 * A.shape[1] + 32) * U32 * mag)
         sums = (3 * int(t.sum()) + 64) * U32
         da[a] = scale[a] * (ds.t() @ X[t])
-        eda[a] = scale[a].abs() * ((e + (two + sums) * (ds.abs() + e)).t() @ X[t].abs())
+        eda[a] = scale[a].abs() * ((e + (cut + sums) * (ds.abs() + e)).t() @ X[t].abs())
         db[a] = scale[a] * (dY[t].t() @ S[t])
-        edb[a] = scale[a].abs() * (two + sums) * (dY[t].abs().t() @ S[t].abs())
+        edb[a] = scale[a].abs() * (cut + sums) * (dY[t].abs().t() @ S[t].abs())
     if R is not None:
         dx = dx + R
         edx = edx + 2 * U32 * dx.abs()
