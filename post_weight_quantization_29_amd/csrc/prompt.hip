@@ -466,6 +466,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, 2) void prompt_forward_kernel(Pr
   if (last >= 0) {
     s0 = scores(keys, 0);
     top = top_of(s0);
+    if (last > 0 && top > m + kGrow) m = top;          // (nothing to rescale yet)
   }
   arrive();
   while (k <= last) {
@@ -488,7 +489,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, 2) void prompt_forward_kernel(Pr
     for (;;) {
       if (none) any_block.template operator()<true>(kb, s);
       else any_block.template operator()<false>(kb, s);
-      if (kb == 1) break;
+      if (kb == 1 || kKeys * k + 32 > w0 + 31) break;  // (block 1 behind all of the wave's rows)
       s = scores(keys, 1);
       kb = 1;
     }
@@ -668,18 +669,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, 2) void prompt_dq_kernel(PromptA
     else any_tile.template operator()<false>(kb0);
     leave();
   }
-  for (; k < tiles; ++k) {          // the other waves' tiles
-    wait_copies<0>();
-    wait_lds_reads();
-    ring_barrier();
-    if (k + 1 < tiles) {
-      ck.go(kKeys * (k + 1), other);
-      cv.go(kKeys * (k + 1), other + kTile);
-    }
-    const uint32_t t = buf;
-    buf = other;
-    other = t;
-  }
+  for (; k < tiles; leave()) arrive();                 // the other waves' tiles
   if (row < n) store_row<T, HD>(a.dQ + (t0 + row) * a.lddq + (int64_t)head * HD, acc, a.scale / sc.up);
 }
 
