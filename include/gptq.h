@@ -444,7 +444,9 @@ typedef struct {
  *  S [m x rank] fp32, contiguous, or NULL: X A_a^T, for the backward pass (0 for a
  *  token without an adapter).  Sums are fp32; X A_a^T enters the second product in
  *  two 16-bit pieces (16 bits for bf16, 22 for fp16).
- *  Y and S overlap neither X nor each other.  m is at most 2^24.
+ *  Y and S overlap neither X nor each other.  m is at most 2^24, and so are the
+ *  workgroups that the batch needs, some (m / 128 + n_seqs) * d_out / 256 (sequences of
+ *  one token: m / 16 * d_out / 64); more are refused.
  *  ws  scratch of gptq_lora_workspace_size(m, set) bytes. */
 size_t gptq_lora_workspace_size(int64_t m, const gptq_lora_set* set);
 int gptq_lora(const void* X, gptq_dtype x_dtype, int64_t m, int64_t ldx, const gptq_lora_set* set,
@@ -459,8 +461,8 @@ int gptq_lora(const void* X, gptq_dtype x_dtype, int64_t m, int64_t ldx, const g
  *  dY [m x d_out] and X [m x d_in] of dtype, the set's; dX [m x d_in] and R (NULL:
  *  0; or dX itself) of x_dtype (F32, F16 or BF16): the shared projection's dX, say.
  *  dA [n_adapters x rank x d_in], dB [n_adapters x d_out x rank] fp32.
- *  Sums are fp32, added in a fixed order; dS and S enter the products in two
- *  16-bit pieces.  Outputs overlap neither inputs nor each other.
+ *  Sums are fp32, added in a fixed order; dS enters dX's product in two 16-bit
+ *  pieces as in the forward pass, dS and S those of dA and dB in three.  Outputs overlap neither inputs nor each other.
  *  ws  scratch of gptq_lora_backward_workspace_size(m, set) bytes (NULL if m is 0). */
 size_t gptq_lora_backward_workspace_size(int64_t m, const gptq_lora_set* set);
 int gptq_lora_backward(const void* dY, gptq_dtype dtype, int64_t m, int64_t lddy, const void* X, int64_t ldx,
@@ -594,7 +596,8 @@ int gptq_kv4_attention(const void* Q, gptq_dtype dtype, int64_t n_tokens, int32_
  *  lse     [n_tokens x n_heads] fp32, or NULL: what the backward pass needs.
  * Scores and statistics are fp32; the probabilities are rounded to 16 bits for the
  * second product.  What a token does not see, infinities and NaN too, does not
- * reach it.  |scale| is at most 1e8; a key whose score is below -1e30 counts as
+ * reach it.  Tiles of 128 tokens (n_tokens / 128 + n_seqs at most) times n_heads are
+ * below 2^24, more are refused.  |scale| is at most 1e8; a key whose score is below -1e30 counts as
  * not seen, and a row that sees nothing is 0 (its lse -inf); a score above 1e38 may
  * count as infinite (the row is then no number). */
 int gptq_prompt_attention(const void* Q, const void* K, const void* V, gptq_dtype dtype, int64_t n_tokens,

@@ -14,7 +14,8 @@
 // reach it).
 //
 // s and dS are fp32.  Where they are an operand of a matrix instruction they go in
-// two pieces of the operands' 16-bit type (16 bits for bf16, 22 for fp16).
+// two pieces of the operands' 16-bit type (16 bits for bf16, 22 for fp16), whose error
+// stays below that of an output of this type; in dA and dB, which are fp32, three bf16 ones.
 #include "w4_epilogue.h"
 
 #include <climits>
@@ -157,8 +158,10 @@ GPTQ_DEV void low_product(const LowArgs& p, const uint16_t* const (&x)[MT], int 
 //
 // Runs: a workgroup takes 16 MT tokens of one sequence, so of one adapter (tiles that
 // end with their sequences: taken from the rows as they lie, a tile of two adapters
-// went through k twice, and the launch waited for it: 50 us instead of 27 for the
-// prompts below).  Sixteen waves a CU, and the loads of one step a wave in flight.
+// went through k twice, and the launch waited for it: 50 us instead of 27 for 4096 tokens
+// of rank 64 and 5120 channels in four sequences).  Those 27 us are 42 MB of X and the
+// adapters in the caches: bound by the latency of its loads, sixteen waves a CU and one step of
+// loads a wave in flight.
 template <typename T, int NB, int MT, int W, bool VEC>
 __global__ __launch_bounds__(64 * W, 4) void lora_low_runs_kernel(LowArgs p, LoraBatch batch) {
   constexpr int TOK = 16 * MT;
@@ -205,7 +208,8 @@ __global__ __launch_bounds__(64 * W, 4) void lora_low_runs_kernel(LowArgs p, Lor
 
 // Steps of mixed adapters: 16 tokens, whatever their sequences; blockIdx.z takes every
 // gridDim.z-th of the tile's adapters (one after the other they would be a chain of
-// memory latencies).
+// memory latencies).  48 requests of rank 16, 8192 channels: 6.9 us, of which some 4 are the
+// launch and the first loads.
 template <typename T, int NB, bool VEC>
 __global__ __launch_bounds__(256) void lora_low_steps_kernel(LowArgs p, LoraBatch batch) {
   constexpr int W = 4;
@@ -389,7 +393,9 @@ template <bool BITS32> struct UpRow {
 // time the sums go through LDS, so that residual and output pass in pieces of 512
 // bytes (fp32 1 KB) of a row: stored as the matrix instruction leaves them, in pieces
 // of 64 or 128 bytes, the stores alone went at 2 TB/s.  A step's residual and pieces of
-// s are on their way while the one before it is multiplied and stored.
+// s are on their way while the one before it is multiplied and stored.  4096 tokens of rank
+// 64 by 13824 channels, 226 MB: 85 us, 2.7 TB/s; two thirds of the waves' time are waits for
+// loads and for the two barriers of a step.
 template <typename T, int NB, bool VEC, bool BITS32>
 __global__ __launch_bounds__(64 * kUpWaves, NB == 8 ? 1 : (NB == 4 ? 3 : 4) - BITS32) void lora_up_runs_kernel(UpArgs p, LoraBatch batch) {
   typedef typename T16<T>::v8 v8;
@@ -493,7 +499,8 @@ __global__ __launch_bounds__(64 * kUpWaves, NB == 8 ? 1 : (NB == 4 ? 3 : 4) - BI
 
 // The same where a block of tokens has several adapters: a unit is a block of 16
 // tokens and one of the adapters in it, a workgroup's waves share the units of 64
-// channels, and s's pieces are made here, from up to eight slices.
+// channels, and s's pieces are made here, from up to eight slices.  48 requests of rank 16 by
+// 8192 channels: 8.8 us, the latency of three loads that wait for each other.
 template <typename T, int NB, bool VEC, bool BITS32>
 __global__ __launch_bounds__(64 * kUpWaves) void lora_up_steps_kernel(UpArgs p) {
   typedef typename T16<T>::v8 v8;
@@ -644,7 +651,9 @@ GPTQ_DEV uint2 read_transposed(uint32_t at) {
 // other: X goes to LDS as it lies and is read transposed, S in three bf16 pieces
 // (24 bits; two cost an error twice that of fp32 sums) with tokens innermost.  fp16 channels
 // are two bf16 values exactly; the second one's product with the third piece, 2^-27 of
-// the whole, is left out.
+// the whole, is left out.  8192 tokens of two adapters of rank 32, 4096 by 4096 channels:
+// 51 us for 136 MB and 4.3 GFLOP (three times with the pieces); vector work (making the
+// pieces) fills a third of the issue slots, the rest waits for the next step's loads.
 template <typename T, int NB>
 __global__ __launch_bounds__(256) void lora_outer_kernel(OuterArgs p) {
   typedef typename T16<__bf16>::v8 b8;
@@ -814,12 +823,17 @@ constexpr int64_t kLoraMaxTokens = 1 << 24;
 // How X A^T is dealt out.  Runs: 32 tokens a workgroup of eight waves (at rank 128
 // 16), k in slices until there are two workgroups a CU.  Steps of mixed adapters: 16
 // tokens a workgroup of four waves, one of the adapters each, up to 8 slices (which the
-// second product adds itself).
+// second product adds itself).  One slice against these, whole calls of 8192 channels: 48
+// requests 22.8 and 11.9 us, 512 tokens of rank 64 70 and 37, 4096 of them 98 and 85.
 struct LowPlan {
   bool mix;
   int mt, tiles, slices, slice_k, shares;
 };
-static bool mixed(int64_t m, int n_seqs) { return m < 16 * (int64_t)n_seqs; }     // a block of tokens has several adapters
+// Whether the batch counts as steps, whose blocks have several adapters.  Both ways, 16
+// adapters, steps first: 48 tokens of rank 16 in sequences of one 15.5 and 17.1 us, of six 11.1
+// and 14.2 (a launch fewer); 512 tokens in ones 51 and 71, in twos 35 and 35, in sixes 25 and 19;
+// of rank 64 in ones 167 and 172, in twos 117 and 90, in sixes 97 and 45.
+static bool mixed(int64_t m, int n_seqs) { return m < (m <= 128 ? 16 : 2) * (int64_t)n_seqs; }
 static LowPlan low_plan(int64_t m, int n_seqs, int K, int nb) {
   LowPlan p;
   p.mix = mixed(m, n_seqs);
@@ -840,7 +854,7 @@ struct LowLayout {
 };
 static LowLayout low_layout(int64_t m, int K, int nb) {
   LowLayout L;
-  const int slices = std::max(low_plan(m, 1, K, nb).slices, low_plan(m, (int)(m / 16 + 1), K, nb).slices);
+  const int slices = std::max(low_plan(m, 1, K, nb).slices, low_plan(m, (int)m + 1, K, nb).slices);
   L.off_part = align_up((size_t)m * sizeof(int32_t));
   L.off_pieces = L.off_part + align_up((size_t)slices * m * 16 * nb * sizeof(float));
   L.off_rows = L.off_pieces + align_up((size_t)m * 32 * nb * 2);
@@ -891,7 +905,9 @@ static int launch_up(UpArgs a, const LowPlan& lp, const LowLayout& L, int nb, co
   if (!a.Y) a.d = 1;
   const int width = lp.mix ? 64 : 256;
   const int64_t groups = (a.d + width - 1) / width;
-  // a run's tiles as long as leave four workgroups a CU, up to 128 tokens (B's rows serve them all)
+  // A run's tiles as long as leave four workgroups a CU, up to 128 tokens (B's rows serve them all): 32
+  // and 128 tokens, whole calls of rank 64: 2048 tokens by 4096 channels 44.0 and 46.8 us, 4096 by 4096 60
+  // and 56, 8192 by 13824 206 and 184.
   a.blocks = lp.mix ? 1 : a.m * groups >= 128 * 1024 ? 8 : a.m * groups >= 64 * 1024 ? 4 : 2;
   const int64_t tiles = (a.m + 16 * a.blocks - 1) / (16 * a.blocks) + (lp.mix ? 0 : b.n_seqs - 1);
   const bool vec = at16(a.B) && a.rank % 8 == 0 && a.ldb % 8 == 0 && a.set % 8 == 0;
@@ -936,9 +952,11 @@ static LoraBackLayout lora_back_layout(int64_t m, const gptq_lora_set* a) {
   L.off_at = L.off_ds + align_up((size_t)m * r * 4);
   L.off_bt = L.off_at + align_up((size_t)sets * a->d_in * pitch * 2);
   L.off_outer = L.off_bt + align_up((size_t)sets * r * ((a->d_out + 7) & ~7) * 2);
-  // splits of the tokens until there are four workgroups a CU, 64 tokens each at least
+  // Splits of the tokens until there are four workgroups a CU, 256 tokens each at least.  Whole calls of
+  // two adapters of rank 32 by 4096 channels: 512 tokens 33.0 us whole, 31.9 so, 42.8 in parts of 64; 8192
+  // tokens 224 whole, 108 so, 138 in four times as many parts.
   const int64_t tiles = ((a->d_in + 127) / 128 + (a->d_out + 127) / 128) * sets;
-  int64_t n = std::max<int64_t>(1, std::min<int64_t>({1024 / tiles, (m + 63) / 64, 16}));
+  int64_t n = std::max<int64_t>(1, std::min<int64_t>({1024 / tiles, (m + 255) / 256, 16}));
   L.slice = ((m + n - 1) / n + 31) / 32 * 32;
   L.splits = (int)((m + L.slice - 1) / L.slice);
   L.out_pitch = sets * r * (a->d_in + a->d_out);

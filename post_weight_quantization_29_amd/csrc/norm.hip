@@ -115,6 +115,9 @@ GPTQ_DEV void row_sums(float (&v)[N], float* red, int& turn, int waves) {
     for (int k = 0; k < N; ++k) v[k] += r[i * N + k];
 }
 
+// One pass, the next row's loads under way while this one's sums are made.  8192 rows of
+// 5120 with an fp32 stream and norms before and behind: 503 MB in 107 us, 4.7 TB/s, the rate of
+// a large copy within 10 %.
 template <typename TH, typename TB, int NC>
 __global__ __launch_bounds__(1024) void residual_norm_kernel(NormArgs a) {
   __shared__ float red[2 * 16];
@@ -204,8 +207,11 @@ __global__ __launch_bounds__(1024) void residual_norm_kernel(NormArgs a) {
   }
 }
 
-// MORE: there is a gate or a norm behind the sub-layer, whose column sums take
-// registers that the plain residual does not spend.
+// The rows of a workgroup one after the other, their column sums in registers (one chunk a
+// thread: the vectors and the next row's loads too).  MORE: there is a gate or a norm
+// behind the sub-layer, whose column sums take registers that the plain residual does not spend.
+// 4095 rows of 4096, 16-bit, all gradients: 201 MB in 61 us, 3.3 TB/s: three sums over a row
+// that wait for each other, at two rows a CU under way.
 template <typename TH, typename TB, int NC, bool MORE>
 __global__ __launch_bounds__(1024) void residual_norm_backward_kernel(NormArgs a) {
   __shared__ float red[2 * 16 * 3];
@@ -381,7 +387,8 @@ __global__ __launch_bounds__(1024) void residual_norm_backward_kernel(NormArgs a
 }
 
 // The workgroups' column sums, 64 columns a workgroup: sixteen threads to a column
-// take every sixteenth part each, and their sums are added in order.
+// take every sixteenth part each, and their sums are added in order (5 us for three sums of
+// 4096 columns of 256 parts).
 __global__ __launch_bounds__(1024) void norm_columns_kernel(const float* __restrict__ part, int parts, int d, float* o0, float* o1,
                                                             float* o2) {
   __shared__ float s[16][64];
@@ -416,7 +423,10 @@ static NormShape norm_shape(int d) {
   return s;
 }
 // Forward, where there are rows enough: two chunks a thread and one row a
-// workgroup, so that more rows are under way in a CU and fewer waves meet at a barrier.
+// workgroup, so that more rows are under way in a CU and fewer waves meet at a barrier.  One
+// chunk and two, fp32 stream, norms before and behind: 1024 rows of 5120 19.2 and 17.4 us, 2048
+// 32.1 and 27.7, 8192 111 and 105 (of 8192 values 160 and 167); below 1024 rows the same
+// within 4 %, and a single row has more threads.
 static NormShape forward_shape(int64_t m, int d) {
   NormShape s = norm_shape(d);
   if (m < 1024) return s;
