@@ -159,9 +159,8 @@ GPTQ_DEV void low_product(const LowArgs& p, const uint16_t* const (&x)[MT], int 
 // Runs: a workgroup takes 16 MT tokens of one sequence, so of one adapter (tiles that
 // end with their sequences: taken from the rows as they lie, a tile of two adapters
 // went through k twice, and the launch waited for it: 50 us instead of 27 for 4096 tokens
-// of rank 64 and 5120 channels in four sequences).  Those 27 us are 42 MB of X and the
-// adapters in the caches: bound by the latency of its loads, sixteen waves a CU and one step of
-// loads a wave in flight.
+// of rank 64 and 5120 channels in four sequences).  Neither memory (42 MB of X in those 27 us)
+// nor issue (9 %) bounds it: eight waves a CU here, one step of loads a wave in flight.
 template <typename T, int NB, int MT, int W, bool VEC>
 __global__ __launch_bounds__(64 * W, 4) void lora_low_runs_kernel(LowArgs p, LoraBatch batch) {
   constexpr int TOK = 16 * MT;

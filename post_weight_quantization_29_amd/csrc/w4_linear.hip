@@ -871,7 +871,7 @@ static LinearBackLayout linear_back_layout(int64_t m, const gptq_w4_weight* w) {
 
 // dX = dY W + R: the transposed 16-bit weight once into the workspace, then the 16-bit
 // product, which takes dY from where it is if its rows fit its stages.  4096 tokens, 4096 -> 11008:
-// weight 36 us (written at 2.5 TB/s), product 358 (1.03 PFLOP/s); 577 tokens, 5120 -> 5120 in
+// weight 36 us (written at 2.5 TB/s), product 320 (1.15 PFLOP/s); 577 tokens, 5120 -> 5120 in
 // act order: 20 and 41, and 8 for the last round's slices of k.
 template <typename T>
 static int linear_backward(const void* dY, int64_t lddy, int64_t m, const gptq_w4_weight* w, const LinearEpi<T>& epi, void* ws,

@@ -185,3 +185,13 @@ def test_gradient_against_differences(P):
         diff = (loss(*up) - loss(*down)) / 0.02          # linear in each argument: exact but for 2^-53 / 0.01
         # two pieces: 2^-16 of the terms; 64 fp32 additions
         assert abs(float((g.double() * v).sum() - diff)) <= 2.0 ** -15 * float((g.double() * v).abs().sum()) + 1e-9
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("r", [16, 64, 128])
+@pytest.mark.parametrize("each,count", [(1, 127), (1, 129), (2, 70), (3, 60), (9, 15), (15, 9)])
+def test_sequences_of_a_few_tokens(P, dtype, r, each, count):
+    """Where a batch counts as steps and where as runs, by its tokens (up to 128 or more) and its sequences' lengths, some of
+    them empty."""
+    lens = [each if i % 7 else each - 1 for i in range(count)]
+    check(P, lens, [(3 * i) % 5 - 1 for i in range(count)], 4, r, 144, 272, dtype)
