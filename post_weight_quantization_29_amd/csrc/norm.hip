@@ -94,14 +94,18 @@ GPTQ_DEV float wave_sum(float x) {
 }
 
 // Sums of N values over a row's threads, the same in all of them: over a wave's
-// lanes, then over its waves in order.  `red` is [2][16 waves][N]; a call takes
-// the half that the one before it did not, so one barrier a call is enough.
+// lanes, then over its waves in order.  `red` is two halves of kRowSums; a call takes
+// the half that the one before it did not, so one barrier a call is enough (both halves hold
+// the most values that a call sums: with halves of 16 N, one value's second half lay in three
+// values' first, which a slower wave was still reading).
+constexpr int kRowSums = 16 * 3;
 template <int N>
 GPTQ_DEV void row_sums(float (&v)[N], float* red, int& turn, int waves) {
 #pragma unroll
   for (int k = 0; k < N; ++k) v[k] = wave_sum(v[k]);
   const int w = threadIdx.x >> 6, first = w / waves * waves;
-  float* r = red + turn * 16 * N;
+  static_assert(16 * N <= kRowSums);
+  float* r = red + turn * kRowSums;
   turn ^= 1;
   if ((threadIdx.x & 63) == 0) {
 #pragma unroll
@@ -120,7 +124,7 @@ GPTQ_DEV void row_sums(float (&v)[N], float* red, int& turn, int waves) {
 // a large copy within 10 %.
 template <typename TH, typename TB, int NC>
 __global__ __launch_bounds__(1024) void residual_norm_kernel(NormArgs a) {
-  __shared__ float red[2 * 16];
+  __shared__ float red[2 * kRowSums];
   const int group = threadIdx.x / a.T, t = threadIdx.x - group * a.T, waves = a.T >> 6;
   int turn = 0;
   // the vectors stay in registers for all the rows that the workgroup walks (1 past the row's end)
@@ -214,7 +218,7 @@ __global__ __launch_bounds__(1024) void residual_norm_kernel(NormArgs a) {
 // that wait for each other, at two rows a CU under way.
 template <typename TH, typename TB, int NC, bool MORE>
 __global__ __launch_bounds__(1024) void residual_norm_backward_kernel(NormArgs a) {
-  __shared__ float red[2 * 16 * 3];
+  __shared__ float red[2 * kRowSums];
   extern __shared__ float cols[];
   const int group = threadIdx.x / a.T, t = threadIdx.x - group * a.T, waves = a.T >> 6;
   int turn = 0;
