@@ -304,9 +304,10 @@ __global__ __launch_bounds__(1024) void residual_norm_backward_kernel(NormArgs a
       }
     }
     row_sums<3>(sum, red, turn, waves);
-    const float r = 1.0f / sqrtf(sum[0] / (float)a.d + a.eps);
+    // (0 in a row that does not exist: with eps 0 its zeros' root has no inverse, and the column sums take all rows)
+    const float r = in ? 1.0f / sqrtf(sum[0] / (float)a.d + a.eps) : 0.0f;
     const float mean = sum[1] * r / (float)a.d;            // mean(g n)
-    const float q = MORE && a.post ? 1.0f / sqrtf(sum[2] / (float)a.d + a.eps) : 1.0f;
+    const float q = !in ? 0.0f : MORE && a.post ? 1.0f / sqrtf(sum[2] / (float)a.d + a.eps) : 1.0f;
     float dot[1] = {0.0f};
 #pragma unroll
     for (int k = 0; k < NC; ++k) {

@@ -1,6 +1,8 @@
 """GPU tests of the residual stream's norms against float64, forward and backward."""
 from __future__ import annotations
 
+import sys
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -162,3 +164,13 @@ def test_gradient_against_differences(P):
         diff = (loss(*up) - loss(*down)) / (2 * step)
         # central differences are off by step^2 times a third derivative of order 1 to 100 here, and by 2^-53 |loss| / step
         assert abs(float((g.double() * v).sum() - diff)) <= 1e-6 * float((g.double() * v).abs().sum()) + 1e-6
+
+
+@pytest.mark.parametrize("ht,dt", [(BF, BF), (F32, HF)])
+@pytest.mark.parametrize("m,d", [(1, 8), (1, 4096), (3, 64), (3, 640), (5, 8), (33, 513), (4095, 520), (3, 9000)])
+def test_without_eps(P, monkeypatch, ht, dt, m, d):
+    """eps 0: the rows that a workgroup's last step does not have add nothing to the sums over rows."""
+    monkeypatch.setattr(sys.modules[__name__], "EPS", 0.0)
+    both_ways(P, m, d, ht, dt, True, True, True, 0.7)
+    both_ways(P, m, d, ht, dt, True, False, True, 0.7)
+    both_ways(P, m, d, ht, dt, False, False, False, 1.0)
