@@ -655,8 +655,10 @@ __global__ __launch_bounds__(64 * kPromptWaves, 2) void prompt_dq_kernel(PromptA
     }
     if constexpr (FINITE) add_none<T, HD>(acc, rd, buf, 0, row - k0 + 1);
   };
-  const int whole = w0 / kKeys;
-  while (k <= whole && k < tiles) {
+  // w0 / 64 whole tiles, then the one on the diagonal.  (A wave behind the sequence's end has none: with its own
+  // number of them it went one tile, and one barrier, beyond the others.)
+  const int whole = w0 < n ? w0 / kKeys : -1;
+  while (k <= whole) {
     arrive();
     int kb0 = 0;
     while (k < whole) {

@@ -98,3 +98,127 @@ def test_row_sums_touch_nothing_that_is_still_read(tmp_path, kernel, mixes):
             assert races == 0, f"{mix} with {row} waves a row: {races} pairs"
             assert highest < room
 
+
+
+# ---------------------------------------------------------------- whole prompts: tiles and barriers
+
+PROMPT = r"""
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstdio>
+#include <cstdlib>
+#include <map>
+#include <random>
+#include <vector>
+using std::max; using std::min;
+constexpr int HD = 64, kRows = 128, kKeys = 64;
+constexpr uint32_t kTile = 1000, kBuf = 2 * kTile, kV = 3 * kTile, lds = 100000;
+constexpr float kGrow = 4.0f, kFar = 65536.0f;
+typedef int T; typedef int f32x16_t;
+static std::mt19937 random_bits(1);
+static bool some() { return random_bits() % 4 == 0; }
+static bool __any(bool) { return some(); }
+template <int N> void wait_copies() {}
+static void wait_lds_reads() {}
+static int wave, epoch;
+static void ring_barrier() { ++epoch; }
+struct Event { bool copy; uint32_t buf; int tile, epoch; };
+static std::vector<Event> events[4];
+static void copied(uint32_t buf, int tile) { events[wave].push_back({true, buf, tile, epoch}); }
+static void read(uint32_t buf, int tile) { events[wave].push_back({false, buf, tile, epoch}); }
+struct TileCopy { void go(int row0, uint32_t to) const { copied(to, row0 / kKeys); } };
+static uint32_t looked_at;
+template <typename A, int B> bool tile_has_none(uint32_t at) { looked_at = at; return some(); }
+template <typename A, int B, typename... X> void add_none(X...) {}
+template <typename A, int B, bool C, typename... X> void add_columns(X...) {}
+template <typename A> int pack8(int, int) { return 0; }
+struct { bool fits(int) { return !some(); } void apply(int) {} } sc;
+
+@BODY@
+
+static int bad, passed;
+static void check(const char* what, int n, int level) {
+  for (int w = 1; w < 4; ++w) {
+    const auto barriers = [](int x) { int e = 0; for (const Event& v : events[x]) if (v.tile == -1) e = v.epoch; return e; };
+    if (barriers(w) != barriers(0)) {
+      if (++bad < 5) printf("%s n %d level %d: wave %d passes %d barriers, wave 0 %d\n", what, n, level, w, barriers(w), barriers(0));
+    }
+  }
+  // a tile is read behind a barrier that all of its copies stand in front of, and before the buffer's next copies
+  std::map<uint32_t, std::vector<Event>> copies;
+  for (const auto& e : events) for (const Event& v : e) if (v.copy) copies[v.buf].push_back(v);
+  for (int w = 0; w < 4; ++w)
+    for (const Event& r : events[w]) {
+      if (r.copy || r.tile == -1) continue;
+      int parts = 0, newest = -1;
+      bool over = false;
+      for (const Event& c : copies[r.buf]) if (c.epoch <= r.epoch && c.epoch > newest) newest = c.epoch;
+      for (const Event& c : copies[r.buf]) {
+        if (c.epoch == newest && c.tile == r.tile) ++parts;
+        if (c.epoch == r.epoch) over = true;
+      }
+      ++passed;
+      if ((parts != 4 || over) && ++bad < 5)
+        printf("%s n %d level %d: wave %d reads tile %d, where %d waves copied it%s\n", what, n, level, w, r.tile, parts, over ? ", while it is copied over" : "");
+    }
+  for (auto& e : events) e.clear();
+}
+int main() {
+  for (int n = 1; n <= 460; ++n)
+    for (int level = 0; level * kRows < n; ++level)
+      for (int again = 0; again < 3; ++again) {
+        for (wave = 0; wave < 4; ++wave) { epoch = 0; forward(n, level); read(0, -1); }
+        check("forward", n, level);
+        for (wave = 0; wave < 4; ++wave) { epoch = 0; queries(n, level); read(0, -1); }
+        check("dq", n, level);
+        const int rep = 1 + random_bits() % 3, splits = 1 + random_bits() % 4, split = random_bits() % splits;
+        for (wave = 0; wave < 4; ++wave) { epoch = 0; keys_values(n, level, rep, splits, split); read(0, -1); }
+        check("dkv", n, level);
+      }
+  printf("%d %d\n", bad, passed);
+}
+"""
+
+
+def between(text, first, last, whole_line=False):
+    """The text from `first` to in front of `last` (whole_line: to the end of its line)."""
+    a = text.index(first)
+    b = text.index(last, a)
+    return text[a:text.index("\n", b) + 1] if whole_line else text[a:b]
+
+
+def test_the_waves_of_a_prompt_tile_meet_at_every_barrier(tmp_path):
+    """The loops over tiles, forward, dQ, dK and dV: every wave of a workgroup passes as many barriers, and reads a tile where
+    all waves' copies of it have landed and before the next ones start, for every length, also where the workgroup's last
+    tokens do not exist."""
+    text = source("prompt.hip")
+    kernel = lambda name: between(text, f"void {name}(", "\n}\n")  # noqa: E731
+    f, q, kv = kernel("prompt_forward_kernel"), kernel("prompt_dq_kernel"), kernel("prompt_dkv_kernel")
+    head = "  const int r0 = level * kRows, w0 = r0 + 32 * wave, row = w0;\n  TileCopy ck, cv;\n"
+    forward = ["static void forward(int n, int level) {\n", head,
+               between(f, "  const int tiles =", "\n", True), between(f, "  uint32_t keys = lds", "\n", True), "  ck.go(0, keys);\n  cv.go(0, values);\n",
+               between(f, "  if (tiles > 1) ck.go", "\n", True), "  int o = 0, rd = 0;\n  float m = 0.0f, top = 0.0f;\n",
+               between(f, "  int k = 0;\n", "  // raw scores"),
+               """  auto tile_of = [&](uint32_t at) { return at == keys || at == values ? k : at == keys1 ? k + 1 : -2; };
+  auto scores = [&](uint32_t from, int) { read(from, tile_of(from)); return 0; };
+  auto top_of = [&](int) { return 0.0f; };
+  auto any_block = [&]<bool FINITE>(int, int) { read(values, k); };
+  auto whole_block = [&]<int KB>(uint32_t from, int&, int&) { read(from, tile_of(from)); read(values, k); };
+""", between(f, "  const int last =", "\n", True), between(f, "  f32x16_t s0, s1;", "the other waves' tiles", True), "}\n"]
+    dq = ["static void queries(int n, int level) {\n", head, "  ck.go(0, lds);\n  cv.go(0, lds + kTile);\n  int acc = 0, rd = 0;\n",
+          between(q, "  const int tiles =", "  // ds of 32 keys"),
+          """  auto slopes = [&](int, int& s) { s = 0; read(buf, k); read(buf + kTile, k); };
+  auto any_tile = [&]<bool FINITE>(int) { read(buf, k); read(buf + kTile, k); };
+""", between(q, "  const int whole =", "the other waves' tiles", True), "}\n"]
+    dkv = ["static void keys_values(int n, int level, int rep, int splits, int split) {\n  struct { int rep, splits; } a{rep, splits};\n",
+           between(kv, "  const int k0 =", ", key =").replace("\n", " ") + ";\n", between(kv, "  const int first =", "  TileCopy<HD> cq"),
+           "  int dk = 0, dv = 0, rd = 0;\n  auto copy = [&](int t, uint32_t to) { copied(to, t); };\n",
+           between(kv, "  uint32_t buf = lds", "  // p and ds of 32 tokens"),
+           """  auto slopes = [&](int, int& s, int& ds) { s = ds = 0; read(buf, i); };
+  auto any_tile = [&]<bool FINITE>(int) { read(buf, i); };
+""", between(kv, "  while (i < total) {\n", "  if (key >= n) return;"), "}\n"]
+    out = run(tmp_path, PROMPT.replace("@BODY@", "".join(forward + dq + dkv)))
+    bad, passed = map(int, out[-1].split())
+    assert passed > 100000
+    assert bad == 0, "\n".join(out[:-1])
