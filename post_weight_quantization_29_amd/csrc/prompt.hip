@@ -800,7 +800,8 @@ __global__ __launch_bounds__(64 * kPromptWaves, HD == 64 ? 2 : 1) void prompt_dk
       slopes(qb, s, ds);
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const bool seen = q0 + 32 * qb + 8 * (r >> 2) + 4 * h + (r & 3) >= key;
+        // from the key's own token to the sequence's end
+        const bool seen = (uint32_t)(q0 + 32 * qb + 8 * (r >> 2) + 4 * h + (r & 3) - key) < (uint32_t)(n - key);
         s[r] = seen ? s[r] : 0.0f;
         ds[r] = seen ? ds[r] : 0.0f;
       }
@@ -817,10 +818,14 @@ __global__ __launch_bounds__(64 * kPromptWaves, HD == 64 ? 2 : 1) void prompt_dk
       add_none<T, HD>(dk, rd, buf, max(key - q0, 0), n - q0);
     }
   };
+  // Tiles of 64 tokens that see all of the wave's keys: those from q0 = w0 + 31 on, but for one that the sequence ends
+  // in.  (Rows behind it are zeros in LDS, but zero times a key that is no number is none.)  One comparison: with
+  // two the compiler spilled in the loop (four sequences of 2048 618 -> 753 us).
+  const uint32_t whole = max(n - kKeys - w0 - 30, 0);
   while (i < total) {
     arrive();
     int qb0 = 0;
-    while (i < total && q0 >= w0 + 31) {       // tiles that see all of the wave's keys
+    while (i < total && (uint32_t)(q0 - w0 - 31) < whole) {
       bool stop = false;
 #pragma unroll
       for (int qb = 0; qb < 2; ++qb) {
@@ -844,7 +849,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, HD == 64 ? 2 : 1) void prompt_dk
     }
     if (i >= total) break;
     if (q0 + kKeys > w0) {
-      // on the diagonal, or out of range
+      // on the diagonal, the last one, or out of range
       const bool none = q0 < w0 + 31 && (tile_has_none<T, HD>(buf) || tile_has_none<T, HD>(buf + kTile));
       if (none) any_tile.template operator()<true>(qb0);
       else any_tile.template operator()<false>(qb0);

@@ -217,7 +217,7 @@ def test_the_waves_of_a_prompt_tile_meet_at_every_barrier(tmp_path):
            between(kv, "  uint32_t buf = lds", "  // p and ds of 32 tokens"),
            """  auto slopes = [&](int, int& s, int& ds) { s = ds = 0; read(buf, i); };
   auto any_tile = [&]<bool FINITE>(int) { read(buf, i); };
-""", between(kv, "  while (i < total) {\n", "  if (key >= n) return;"), "}\n"]
+""", between(kv, "  const uint32_t whole =", "  if (key >= n) return;"), "}\n"]
     out = run(tmp_path, PROMPT.replace("@BODY@", "".join(forward + dq + dkv)))
     bad, passed = map(int, out[-1].split())
     assert passed > 100000

@@ -262,3 +262,24 @@ def test_many_rows_behind_the_batch(P, rows, cut):
     for x, name in zip(d, ("dq", "dk", "dv")):
         R.within(x[live], ref[name][0][live[:520]], ref[name][1][live[:520]], name)
         assert bool((x[~live] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("n", [64, 65, 100, 128, 150])
+def test_a_key_that_no_token_can_reach(P, dtype, hd, n):
+    """A key of -inf, whose scores are all -inf: it has no weight, so its gradients are 0, wherever the sequence ends inside
+    the last tile of tokens."""
+    j, H = 40, 4
+    Q, K, V = (t.clone() for t in inputs(n, H, 2, hd, dtype))
+    Q[:, :, 3] = Q[:, :, 3].abs() + 0.1
+    K[j, 1, 3] = float("-inf")
+    out, lse = forward(P, Q, K, V, [0, n], n)
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    dO = rand((n, H, hd), dtype, 9, 0.1)
+    dq, dk, dv = backward(P, dO, Q, K, V, out, lse, [0, n], n)
+    assert bool((dk[j, 1] == 0).all()) and bool((dv[j, 1] == 0).all())
+    assert bool(torch.isfinite(dk).all()) and bool(torch.isfinite(dv).all()) and bool(torch.isfinite(dq[:j]).all())
+    # the formula's own 0 * inf, in that channel and head alone
+    rest = [c for c in range(hd) if c != 3]
+    assert bool(torch.isfinite(dq[:, :, rest]).all()) and bool(torch.isfinite(dq[:, :2]).all())
