@@ -516,8 +516,9 @@ __global__ __launch_bounds__(64 * kPromptWaves, 2) void prompt_forward_kernel(Pr
   for (leave(); k < tiles; leave()) arrive();          // the other waves' tiles
   l = over_halves_sum(l);
   if (row >= n) return;
-  // a score whose log2 is beyond fp32 leaves l 0 (or no number): then so is the row
-  const bool none = m == kNoScore;
+  // A score whose log2 is beyond fp32 leaves l 0 (or no number): then so is the row.  Scores that are all no
+  // number leave m as it was, but not l.
+  const bool none = m == kNoScore && l == l;
   const float inv = none ? 0.0f : 1.0f / l;
   store_row<T, HD>(a.out + (t0 + row) * a.ldo + (int64_t)head * HD, o, inv);
   if (a.lse && h == 0) a.lse[(t0 + row) * a.n_heads + head] = none ? -INFINITY : (m + __builtin_amdgcn_logf(l) - kUp<T>) * kLn2;

@@ -283,3 +283,15 @@ def test_a_key_that_no_token_can_reach(P, dtype, hd, n):
     # the formula's own 0 * inf, in that channel and head alone
     rest = [c for c in range(hd) if c != 3]
     assert bool(torch.isfinite(dq[:, :, rest]).all()) and bool(torch.isfinite(dq[:, :2]).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_log_sum_of_a_row_that_is_no_number(P, dtype):
+    """NaN in a query: its scores are none, so its log-sum is none either, not that of a row that sees nothing."""
+    n = 70
+    Q, K, V = (t.clone() for t in inputs(n, 2, 1, 64, dtype))
+    Q[5, 0, 0] = Q[66, 1, 9] = float("nan")
+    K[0, 0, 1] = float("nan")                 # token 0 sees nothing else
+    out, lse = forward(P, Q, K, V, [0, n], n)
+    assert bool(out[5, 0].isnan().all()) and bool(lse[5, 0].isnan()) and bool(lse[66, 1].isnan())
+    assert bool(out[0].isnan().all()) and bool(lse[0].isnan().all())
