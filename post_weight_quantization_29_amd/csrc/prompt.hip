@@ -945,8 +945,8 @@ static bool prompt_ok(gptq_dtype t, int64_t n_tokens, int n_heads, int n_kv, int
   return fabsf(scale) <= 1e8f;
 }
 // tiles of 128 tokens that n_tokens in n_seqs sequences can have
-static int64_t tile_bound(int64_t n_tokens, int n_seqs, int max_len) {
-  return std::min((n_tokens + kRows - 1) / kRows + n_seqs - 1, (int64_t)n_seqs * ((max_len + kRows - 1) / kRows));
+static int64_t tile_bound(int64_t n_tokens, int n_seqs, int64_t max_len) {
+  return std::min((n_tokens + kRows - 1) / kRows + n_seqs - 1, n_seqs * ((max_len + kRows - 1) / kRows));
 }
 
 // Workgroups that share the tokens of a tile of keys: up to four a CU in all, up to
@@ -956,8 +956,8 @@ static int64_t tile_bound(int64_t n_tokens, int n_seqs, int max_len) {
 // nothing to gain.  The parts hold a row for each row of the batch, in sequences or not, so
 // their number is what kPartRows rows of one kv head's dK and dV leave room for.
 constexpr int64_t kPartRows = 1024 * kRows;
-static int key_splits(int64_t tiles, int64_t n_tokens, int n_kv, int rep, int max_len) {
-  const int64_t s = std::min<int64_t>(1023 / (tiles * n_kv), (int64_t)rep * ((max_len + kKeys - 1) / kKeys) / 4);
+static int key_splits(int64_t tiles, int64_t n_tokens, int n_kv, int rep, int64_t max_len) {
+  const int64_t s = std::min<int64_t>(1023 / (tiles * n_kv), rep * ((max_len + kKeys - 1) / kKeys) / 4);
   return (int)std::max<int64_t>(1, std::min({s, (int64_t)8, kPartRows / (n_tokens * n_kv)}));
 }
 static size_t rows_part(int64_t n_tokens, int n_heads) { return align_up((size_t)2 * n_heads * n_tokens * sizeof(float)); }
@@ -972,6 +972,7 @@ extern "C" int gptq_prompt_attention(const void* Q, const void* K, const void* V
                                      float* lse, hipStream_t s) {
   if (!prompt_ok(dtype, n_tokens, n_heads, n_kv_heads, head_dim, n_seqs, max_len, scale)) return GPTQ_ERR_INVALID_ARG;
   if (n_tokens == 0) return GPTQ_OK;
+  max_len = (int32_t)std::min<int64_t>(max_len, n_tokens);      // (the kernels round it up to whole tiles in 32 bits)
   const HeadRows q{Q, ldq, n_heads}, k{K, ldk, n_kv_heads}, v{V, ldv, n_kv_heads}, o{out, ldo, n_heads};
   for (const HeadRows& r : {q, k, v, o})
     if (!head_rows_ok(r, head_dim)) return GPTQ_ERR_INVALID_ARG;
@@ -1007,6 +1008,7 @@ extern "C" int gptq_prompt_attention_backward(const void* dOut, int64_t lddo, co
                                               size_t ws_bytes, hipStream_t s) {
   if (!prompt_ok(dtype, n_tokens, n_heads, n_kv_heads, head_dim, n_seqs, max_len, scale)) return GPTQ_ERR_INVALID_ARG;
   if (n_tokens == 0) return GPTQ_OK;
+  max_len = (int32_t)std::min<int64_t>(max_len, n_tokens);      // (the kernels round it up to whole tiles in 32 bits)
   const HeadRows ins[] = {{dOut, lddo, n_heads}, {Q, ldq, n_heads}, {K, ldk, n_kv_heads}, {V, ldv, n_kv_heads}, {out, ldo, n_heads}};
   const HeadRows outs[] = {{dQ, lddq, n_heads}, {dK, lddk, n_kv_heads}, {dV, lddv, n_kv_heads}};
   for (const HeadRows& r : ins)

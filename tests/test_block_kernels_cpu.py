@@ -17,12 +17,12 @@ def source(name):
         return f.read()
 
 
-def run(folder, text, *args):
+def run(folder, text, *args, flags=("-O1",)):
     """The program's output lines; it is compiled once a folder."""
     cpp, exe = folder / "model.cpp", folder / "model"
     if not exe.exists():
         cpp.write_text(text)
-        made = subprocess.run(["g++", "-std=c++20", "-O1", "-w", str(cpp), "-o", str(exe)], capture_output=True, text=True)
+        made = subprocess.run(["g++", "-std=c++20", *flags, "-w", str(cpp), "-o", str(exe)], capture_output=True, text=True)
         assert made.returncode == 0, made.stderr[-3000:]
     return subprocess.run([str(exe), *map(str, args)], capture_output=True, text=True, check=True, timeout=100).stdout.splitlines()
 
@@ -222,3 +222,25 @@ def test_the_waves_of_a_prompt_tile_meet_at_every_barrier(tmp_path):
     bad, passed = map(int, out[-1].split())
     assert passed > 100000
     assert bad == 0, "\n".join(out[:-1])
+
+
+# ---------------------------------------------------------------- whole prompts: counts
+
+def test_prompt_counts_at_the_end_of_32_bits(tmp_path):
+    """How many tiles a batch may have and in how many parts a tile's tokens go, of bounds of nearly 2^31, with a trap at
+    every overflow."""
+    text = source("prompt.hip")
+    body = between(text, "// tiles of 128 tokens that n_tokens", "static size_t rows_part")
+    out = run(tmp_path, "#include <algorithm>\n#include <climits>\n#include <cstdint>\n#include <cstdio>\n"
+              "constexpr int kRows = 128, kKeys = 64;\n" + body + """
+int main() {
+  for (int64_t most : {INT_MAX, INT_MAX - 1, INT_MAX - 62, INT_MAX - 63, INT_MAX - 126, INT_MAX - 127, 1 << 30, 700, 1})
+    for (int64_t tokens : {(int64_t)INT_MAX, (int64_t)700, (int64_t)1}) {
+      const int64_t tiles = tile_bound(tokens, 2, most);
+      printf("%ld %ld %ld %d\\n", (long)most, (long)tokens, (long)tiles, key_splits(tiles, tokens, 1, 4, most));
+    }
+}
+""", flags=("-ftrapv", "-O0"))
+    assert len(out) == 27
+    for most, tokens, tiles, splits in (map(int, line.split()) for line in out):
+        assert tiles == min(-(-tokens // 128) + 1, 2 * -(-most // 128)) and 1 <= splits <= 8

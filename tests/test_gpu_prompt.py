@@ -295,3 +295,8 @@ def test_log_sum_of_a_row_that_is_no_number(P, dtype):
     out, lse = forward(P, Q, K, V, [0, n], n)
     assert bool(out[5, 0].isnan().all()) and bool(lse[5, 0].isnan()) and bool(lse[66, 1].isnan())
     assert bool(out[0].isnan().all()) and bool(lse[0].isnan().all())
+
+
+@pytest.mark.parametrize("most", [2 ** 31 - 1, 2 ** 31 - 100, 2 ** 31 - 128])
+def test_a_bound_at_the_end_of_32_bits(P, most):
+    check(P, [150, 20, 700], 4, 2, 64, BF, max_len=most)
