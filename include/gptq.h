@@ -588,7 +588,7 @@ int gptq_kv4_attention(const void* Q, gptq_dtype dtype, int64_t n_tokens, int32_
  *  Q, out  token t, head h at Q + t*ldq + h*head_dim elements; K, V likewise with
  *          n_kv_heads heads: rows of a fused projection as they are.  f16 or bf16,
  *          rows 16-byte aligned; pitches below 2^22 elements.  head_dim 64 or 128;
- *          n_heads a multiple of n_kv_heads.  out overlaps no input.
+ *          n_heads a multiple of n_kv_heads.  out and lse overlap no input, nor each other.
  *  q_start [n_seqs + 1] int32 (device, not decreasing): sequence b is rows
  *          q_start[b] .. q_start[b+1]-1.  Rows outside [q_start[0], q_start[n_seqs])
  *          are left as they are, and so are a sequence's tokens past max_len
@@ -614,9 +614,10 @@ int gptq_prompt_attention(const void* Q, const void* K, const void* V, gptq_dtyp
  *  pitch (gradients of one fused row are written in place).  p and ds are rounded
  *  to 16 bits for the products (fp16: below a power of two that follows ds); sums are
  *  fp32, in a fixed order.
- *  dQ, dK and dV overlap no input and, row by row, not each other.
+ *  dQ, dK and dV overlap no input (lse and q_start among them) and, row by row, not each
+ *  other.
  *  ws  scratch of gptq_prompt_attention_backward_workspace_size(n_tokens, n_heads)
- *      bytes. */
+ *      bytes, apart from all arrays. */
 size_t gptq_prompt_attention_backward_workspace_size(int64_t n_tokens, int32_t n_heads);
 int gptq_prompt_attention_backward(const void* dOut, int64_t lddo, const void* Q, const void* K, const void* V,
                                    gptq_dtype dtype, int64_t n_tokens, int32_t n_heads, int32_t n_kv_heads,

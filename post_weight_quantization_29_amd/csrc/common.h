@@ -40,6 +40,11 @@ inline uint64_t rows_bytes(int64_t m, int64_t ld, int64_t d, int64_t elem) {
   const __int128 n = ((__int128)(m - 1) * ld + d) * elem;
   return n > ((__int128)1 << 62) ? (uint64_t)1 << 62 : (uint64_t)n;
 }
+// do two arrays share a byte (NULL: none)
+inline bool share_bytes(const void* a, uint64_t na, const void* b, uint64_t nb) {
+  const uint64_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
 inline size_t align_up(size_t x, size_t a = kAlign) { return (x + a - 1) / a * a; }
 
 // Copies HBM -> LDS without registers: lane l's 16 (4) bytes at the

@@ -930,10 +930,6 @@ static int launch_up(UpArgs a, const LowPlan& lp, const LowLayout& L, int nb, co
 
 static bool is_16(gptq_dtype t) { return t == GPTQ_F16 || t == GPTQ_BF16; }
 static bool elem_at(const void* p, gptq_dtype t) { return (reinterpret_cast<uintptr_t>(p) & (t == GPTQ_F32 ? 3 : 1)) == 0; }
-static bool share_bytes(const void* a, uint64_t na, const void* b, uint64_t nb) {
-  const uint64_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + nb && y < x + na;
-}
 static bool rows_vec(const void* p, int64_t ld, gptq_dtype t) { return !p || (at16(p) && ld % (t == GPTQ_F32 ? 4 : 8) == 0); }
 
 struct LoraBackLayout {

@@ -937,6 +937,9 @@ static bool heads_meet(const HeadRows& a, const HeadRows& b, int64_t m, int hd) 
   const uint64_t d = x >= y ? (x - y) % pitch : (pitch - (y - x) % pitch) % pitch;   // a's row behind b's
   return !(d >= wb && d + wa <= pitch);
 }
+static bool heads_meet(const HeadRows& a, int64_t m, int hd, const void* p, uint64_t bytes) {
+  return share_bytes(a.p, rows_bytes(m, a.ld, (int64_t)a.heads * hd, 2), p, bytes);
+}
 
 static bool prompt_ok(gptq_dtype t, int64_t n_tokens, int n_heads, int n_kv, int hd, int n_seqs, int max_len, float scale) {
   if (t != GPTQ_F16 && t != GPTQ_BF16) return false;
@@ -977,8 +980,12 @@ extern "C" int gptq_prompt_attention(const void* Q, const void* K, const void* V
   for (const HeadRows& r : {q, k, v, o})
     if (!head_rows_ok(r, head_dim)) return GPTQ_ERR_INVALID_ARG;
   if (!q_start || ((reinterpret_cast<uintptr_t>(q_start) | reinterpret_cast<uintptr_t>(lse)) & 3)) return GPTQ_ERR_INVALID_ARG;
+  const uint64_t lse_bytes = (uint64_t)n_tokens * n_heads * sizeof(float), start_bytes = ((uint64_t)n_seqs + 1) * sizeof(int32_t);
   for (const HeadRows& r : {q, k, v})
     if (heads_meet(o, r, n_tokens, head_dim)) return GPTQ_ERR_INVALID_ARG;
+  for (const HeadRows& r : {q, k, v, o})
+    if (heads_meet(r, n_tokens, head_dim, lse, lse_bytes)) return GPTQ_ERR_INVALID_ARG;
+  if (heads_meet(o, n_tokens, head_dim, q_start, start_bytes) || share_bytes(lse, lse_bytes, q_start, start_bytes)) return GPTQ_ERR_INVALID_ARG;
   const int64_t grid = tile_bound(n_tokens, n_seqs, max_len) * n_heads;
   if (grid > (1 << 24) - 1) return GPTQ_ERR_INVALID_ARG;
   PromptArgs a{};
@@ -1021,10 +1028,18 @@ extern "C" int gptq_prompt_attention_backward(const void* dOut, int64_t lddo, co
       if (heads_meet(outs[i], outs[j], n_tokens, head_dim)) return GPTQ_ERR_INVALID_ARG;
   }
   if (!lse || !q_start || ((reinterpret_cast<uintptr_t>(q_start) | reinterpret_cast<uintptr_t>(lse)) & 3)) return GPTQ_ERR_INVALID_ARG;
+  const uint64_t lse_bytes = (uint64_t)n_tokens * n_heads * sizeof(float), start_bytes = ((uint64_t)n_seqs + 1) * sizeof(int32_t);
+  for (const HeadRows& r : outs)
+    if (heads_meet(r, n_tokens, head_dim, lse, lse_bytes) || heads_meet(r, n_tokens, head_dim, q_start, start_bytes)) return GPTQ_ERR_INVALID_ARG;
   const int64_t tiles = tile_bound(n_tokens, n_seqs, max_len);
   if (tiles * n_heads > (1 << 24) - 1) return GPTQ_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < gptq_prompt_attention_backward_workspace_size(n_tokens, n_heads) || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)))
-    return GPTQ_ERR_WORKSPACE;
+  const size_t need = gptq_prompt_attention_backward_workspace_size(n_tokens, n_heads);
+  if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return GPTQ_ERR_WORKSPACE;
+  for (const HeadRows& r : ins)
+    if (heads_meet(r, n_tokens, head_dim, ws, need)) return GPTQ_ERR_INVALID_ARG;
+  for (const HeadRows& r : outs)
+    if (heads_meet(r, n_tokens, head_dim, ws, need)) return GPTQ_ERR_INVALID_ARG;
+  if (share_bytes(ws, need, lse, lse_bytes) || share_bytes(ws, need, q_start, start_bytes)) return GPTQ_ERR_INVALID_ARG;
   PromptArgs a{};
   auto c = [](const void* p) { return static_cast<const uint16_t*>(p); };
   a.Q = c(Q); a.K = c(K); a.V = c(V); a.dO = c(dOut); a.O = c(out);

@@ -210,3 +210,15 @@ def test_binding_refuses():
     q = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="Q must be on a GPU"):
         P.gptq_prompt_attention(q, q, q, torch.tensor([0, 4], dtype=torch.int32), 4, q)
+
+
+def test_prompt_refuses_a_log_sum_or_description_in_the_way(L):
+    """lse is an output of the forward pass and an input of the backward pass; what describes the batch is an input of both;
+    the scratch lies apart from all."""
+    for kw in (dict(lse=at(1)), dict(lse=at(2, 64)), dict(lse=at(3)), dict(lse=at(5)), dict(out=at(5), lse=at(5, 2 * 256 * 49 + 508)),
+               dict(lse=at(4)), dict(lse=at(4, 8)), dict(out=at(4)), dict(out=at(5), qs=at(5, 64))):
+        assert prompt(L, **kw) == M.ERR_INVALID_ARG, kw
+    for kw in (dict(dQ=at(6)), dict(dK=at(6, 16)), dict(dV=at(6, 784)), dict(dQ=at(7)), dict(dK=at(7)), dict(dV=at(7)), dict(qs=at(8, 512)),
+               dict(lse=at(8, 2 * 256 * 50 - 4)), dict(ws=at(1)), dict(ws=at(2, 256)), dict(ws=at(3)), dict(ws=at(4)), dict(ws=at(5)), dict(ws=at(6)),
+               dict(ws=at(7)), dict(ws=at(8)), dict(ws=at(9)), dict(ws=at(10)), dict(dV=at(11, 256))):
+        assert prompt_back(L, **{"nb": 2 * MB, **kw}) == M.ERR_INVALID_ARG, kw
