@@ -497,8 +497,8 @@ int gptq_residual_rmsnorm(const void* R, gptq_dtype h_dtype, int64_t ldr, const 
  *      NULL).  dR of h_dtype, dB of dtype, dgamma, dpost_gamma and dgate [d] fp32:
  *      each may be NULL.  The sums are written, not added to (0 if m is 0), and do not
  *      depend on timing.
- *  dR and dB may each be one of dY, H, dH, B whole (same type and pitch); they overlap
- *  nothing else, nor each other.
+ *  dR and dB may each be one of dY, H, dH, B whole (same type and pitch); outputs and
+ *  the scratch overlap nothing else, nor each other.
  *  ws  scratch of gptq_residual_rmsnorm_backward_workspace_size(m, d) bytes (NULL
  *      without dgamma, dpost_gamma and dgate). */
 size_t gptq_residual_rmsnorm_backward_workspace_size(int64_t m, int32_t d);

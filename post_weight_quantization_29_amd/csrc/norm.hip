@@ -464,6 +464,10 @@ static bool apart(NormRows a, NormRows b, int64_t m, int d) {
   const uint64_t na = rows_bytes(m, a.ld, d, norm_bytes(a.t)), nb = rows_bytes(m, b.ld, d, norm_bytes(b.t));
   return x >= y + nb || y >= x + na;
 }
+// an array that is a vector or scratch, against rows
+static bool rows_meet(NormRows a, int64_t m, int d, const void* p, uint64_t bytes) {
+  return share_bytes(a.p, rows_bytes(m, a.ld, d, norm_bytes(a.t)), p, bytes);
+}
 static bool same_or_apart(NormRows a, NormRows b, int64_t m, int d) {
   return (a.p == b.p && a.ld == b.ld && a.t == b.t) || apart(a, b, m, d);
 }
@@ -494,6 +498,8 @@ extern "C" int gptq_residual_rmsnorm(const void* R, gptq_dtype h_dtype, int64_t 
   if (!on(gamma, 4) || !on(post_gamma, 4) || !on(gate, 4)) return GPTQ_ERR_INVALID_ARG;
   if (!apart(h, y, m, d) || !same_or_apart(h, r, m, d) || !same_or_apart(h, b, m, d) || !same_or_apart(y, r, m, d) ||
       !same_or_apart(y, b, m, d)) return GPTQ_ERR_INVALID_ARG;
+  for (const float* p : {gamma, post_gamma, gate})
+    if (rows_meet(h, m, d, p, (uint64_t)d * 4) || rows_meet(y, m, d, p, (uint64_t)d * 4)) return GPTQ_ERR_INVALID_ARG;
   const NormShape n = forward_shape(m, d);
   NormArgs a{};
   a.R = R; a.B = B; a.gamma = gamma; a.post = post_gamma; a.gate = gate; a.Hout = H; a.Y = Y;
@@ -541,8 +547,28 @@ extern "C" int gptq_residual_rmsnorm_backward(const void* dY, gptq_dtype dtype, 
   if (!apart(r, o, m, d)) return GPTQ_ERR_INVALID_ARG;
   for (const NormRows& t : {y, h, x, b})
     if (!same_or_apart(r, t, m, d) || !same_or_apart(o, t, m, d)) return GPTQ_ERR_INVALID_ARG;
+  // the sums, the vectors and the scratch: vectors may be one another, nothing else meets
+  const uint64_t vb = (uint64_t)d * 4;
+  const float *const vectors[] = {gamma, post_gamma, gate}, *const totals[] = {dgamma, dpost_gamma, dgate};
+  for (const float* v : vectors)
+    if (rows_meet(r, m, d, v, vb) || rows_meet(o, m, d, v, vb)) return GPTQ_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i) {
+    for (const NormRows& t : {y, h, x, b, r, o})
+      if (rows_meet(t, m, d, totals[i], vb)) return GPTQ_ERR_INVALID_ARG;
+    for (const float* v : vectors)
+      if (share_bytes(totals[i], vb, v, vb)) return GPTQ_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (share_bytes(totals[i], vb, totals[j], vb)) return GPTQ_ERR_INVALID_ARG;
+  }
   const bool sums = dgamma || dpost_gamma || dgate;
-  if (sums && (!ws || ws_bytes < gptq_residual_rmsnorm_backward_workspace_size(m, d) || !on(ws, kAlign))) return GPTQ_ERR_WORKSPACE;
+  const size_t need = gptq_residual_rmsnorm_backward_workspace_size(m, d);
+  if (sums && (!ws || ws_bytes < need || !on(ws, kAlign))) return GPTQ_ERR_WORKSPACE;
+  if (sums) {
+    for (const NormRows& t : {y, h, x, b, r, o})
+      if (rows_meet(t, m, d, ws, need)) return GPTQ_ERR_INVALID_ARG;
+    for (int i = 0; i < 3; ++i)
+      if (share_bytes(vectors[i], vb, ws, need) || share_bytes(totals[i], vb, ws, need)) return GPTQ_ERR_INVALID_ARG;
+  }
   const NormShape n = norm_shape(d);
   const int parts = norm_parts(m, n.groups);
   NormArgs a{};

@@ -222,3 +222,25 @@ def test_prompt_refuses_a_log_sum_or_description_in_the_way(L):
                dict(lse=at(8, 2 * 256 * 50 - 4)), dict(ws=at(1)), dict(ws=at(2, 256)), dict(ws=at(3)), dict(ws=at(4)), dict(ws=at(5)), dict(ws=at(6)),
                dict(ws=at(7)), dict(ws=at(8)), dict(ws=at(9)), dict(ws=at(10)), dict(dV=at(11, 256))):
         assert prompt_back(L, **{"nb": 2 * MB, **kw}) == M.ERR_INVALID_ARG, kw
+
+
+def test_norm_refuses_vectors_and_scratch_in_the_way(L):
+    """The sums over rows and the scratch lie apart from all else, and rows that are written from the vectors."""
+    for kw in (dict(gamma=at(4)), dict(gamma=at(5, 1276)), dict(post=at(4, 16)), dict(gate=at(5)), dict(post=at(6), gate=at(4, 64)), dict(B=None, H=None, gamma=at(5))):
+        assert norm(L, **kw) == M.ERR_INVALID_ARG, kw
+    need = L.gptq_residual_rmsnorm_backward_workspace_size(i64(10), i32(64))
+    rows = dict(dY=1, H=2, dH=3, B=4, dR=8, dB=9)
+    for name in ("dg", "dp", "dw"):
+        for k in rows.values():
+            assert norm_back(L, **{name: at(k, 1276)}) == M.ERR_INVALID_ARG, (name, k)
+        for k in (5, 6, 7, 10, 11, 12):
+            if at(k) != dict(dg=at(10), dp=at(11), dw=at(12))[name]:
+                assert norm_back(L, **{name: at(k, 252)}) == M.ERR_INVALID_ARG and norm_back(L, **{name: at(k)}) == M.ERR_INVALID_ARG, (name, k)
+    for name, k in (("post", 8), ("gate", 9), ("gamma", 8)):
+        assert norm_back(L, **{name: at(k, 64)}) == M.ERR_INVALID_ARG, name
+    for k in range(1, 13):
+        assert norm_back(L, ws=at(k)) == M.ERR_INVALID_ARG, k
+    for name in (*rows, "dg", "dp", "dw", "post", "gate", "gamma"):
+        assert norm_back(L, **{name: at(13, need - 4 & -16)}) == M.ERR_INVALID_ARG, name
+    # the sums alone need no place of their own among what is not given
+    assert norm_back(L, dR=None, dB=None, dg=at(8), dp=at(9), ws=None) == M.ERR_WORKSPACE
