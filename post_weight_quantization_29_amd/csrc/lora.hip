@@ -861,11 +861,31 @@ static LowLayout low_layout(int64_t m, int K, int nb) {
   return L;
 }
 
+// How the second product by d channels is dealt out: tiles of 16 `blocks` tokens by `groups` of channels
+struct UpPlan {
+  int blocks;
+  int64_t groups, tiles;
+};
+static UpPlan up_plan(const LowPlan& lp, int64_t m, int n_seqs, int d) {
+  UpPlan p;
+  const int width = lp.mix ? 64 : 256;
+  p.groups = (d + width - 1) / width;
+  // A run's tiles as long as leave four workgroups a CU, up to 128 tokens (B's rows serve them all): 32
+  // and 128 tokens, whole calls of rank 64: 2048 tokens by 4096 channels 44.0 and 46.8 us, 4096 by 4096 60
+  // and 56, 8192 by 13824 206 and 184.
+  p.blocks = lp.mix ? 1 : m * p.groups >= 128 * 1024 ? 8 : m * p.groups >= 64 * 1024 ? 4 : 2;
+  p.tiles = (m + 16 * p.blocks - 1) / (16 * p.blocks) + (lp.mix ? 0 : n_seqs - 1);
+  return p;
+}
+// whether both products' launches are within the hardware's limits
+static bool plans_fit(const LowPlan& lp, const UpPlan& up) {
+  return (int64_t)lp.tiles * 512 <= UINT32_MAX && up.tiles * up.groups <= (1 << 24) - 1;
+}
+
 // s of every token into the workspace at base; where they are runs, as pieces
 template <typename T>
 static int launch_low(const LowPlan& p, const LowLayout& L, int nb, bool vec, LowArgs a, const LoraBatch& b, char* base, float* S, hipStream_t s) {
   const dim3 grid((unsigned)p.tiles, (unsigned)p.slices, (unsigned)p.shares);
-  if ((int64_t)p.tiles * 512 > UINT32_MAX) return GPTQ_ERR_INVALID_ARG;
   a.slice_k = p.slice_k;
   a.ids = reinterpret_cast<int32_t*>(base);
   a.part = reinterpret_cast<float*>(base + L.off_part);
@@ -895,23 +915,15 @@ static int launch_low(const LowPlan& p, const LowLayout& L, int nb, bool vec, Lo
 
 // The second product (a.Y; a.S where the pieces are made here), from what launch_low left at base.
 template <typename T>
-static int launch_up(UpArgs a, const LowPlan& lp, const LowLayout& L, int nb, const LoraBatch& b, char* base, hipStream_t s) {
+static int launch_up(UpArgs a, const LowPlan& lp, const UpPlan& up, const LowLayout& L, int nb, const LoraBatch& b, char* base, hipStream_t s) {
   a.part = reinterpret_cast<float*>(base + L.off_part);
   a.pieces = reinterpret_cast<uint16_t*>(base + L.off_pieces);
   a.rows = reinterpret_cast<float*>(base + L.off_rows);
   a.ids = reinterpret_cast<int32_t*>(base);
   a.slices = lp.slices;
-  if (!a.Y) a.d = 1;
-  const int width = lp.mix ? 64 : 256;
-  const int64_t groups = (a.d + width - 1) / width;
-  // A run's tiles as long as leave four workgroups a CU, up to 128 tokens (B's rows serve them all): 32
-  // and 128 tokens, whole calls of rank 64: 2048 tokens by 4096 channels 44.0 and 46.8 us, 4096 by 4096 60
-  // and 56, 8192 by 13824 206 and 184.
-  a.blocks = lp.mix ? 1 : a.m * groups >= 128 * 1024 ? 8 : a.m * groups >= 64 * 1024 ? 4 : 2;
-  const int64_t tiles = (a.m + 16 * a.blocks - 1) / (16 * a.blocks) + (lp.mix ? 0 : b.n_seqs - 1);
+  a.blocks = up.blocks;
   const bool vec = at16(a.B) && a.rank % 8 == 0 && a.ldb % 8 == 0 && a.set % 8 == 0;
-  if (tiles * groups > (1 << 24) - 1) return GPTQ_ERR_INVALID_ARG;
-  const unsigned grid = (unsigned)(tiles * groups);
+  const unsigned grid = (unsigned)(up.tiles * up.groups);
   auto go = [&]<int NB>() {
     auto on = [&]<bool VEC, bool BITS32>() {
       if (lp.mix) lora_up_steps_kernel<T, NB, VEC, BITS32><<<grid, 64 * kUpWaves, 0, s>>>(a);
@@ -964,6 +976,9 @@ static int lora_backward(const void* dY, int64_t lddy, const void* X, int64_t ld
                          const LoraBatch& b, const void* R, int64_t ldr, void* dX, gptq_dtype x_dtype, int64_t lddx, float* dA,
                          float* dB, char* base, hipStream_t s) {
   const LoraBackLayout L = lora_back_layout(b.m, a);
+  const LowPlan lp = low_plan(b.m, b.n_seqs, a->d_out, L.nb);
+  const UpPlan up = up_plan(lp, b.m, b.n_seqs, dX ? a->d_in : 1);
+  if (!plans_fit(lp, up)) return GPTQ_ERR_INVALID_ARG;
   const int sets = a->n_adapters, r = a->rank, pitch = (r + 7) & ~7, kp = (a->d_out + 7) & ~7;
   const int32_t* ids = reinterpret_cast<const int32_t*>(base);
   float* ds = reinterpret_cast<float*>(base + L.off_ds);
@@ -977,7 +992,6 @@ static int lora_backward(const void* dY, int64_t lddy, const void* X, int64_t ld
   if (!dX) ta.tiles = 0;
   lora_transpose_kernel<<<dim3((unsigned)(tb.tiles + ta.tiles), (unsigned)sets), 256, 0, s>>>(tb, ta);
   GPTQ_LAUNCH_CHECK();
-  const LowPlan lp = low_plan(b.m, b.n_seqs, a->d_out, L.nb);
   const bool vec = rows_vec(dY, lddy, GPTQ_BF16) && a->d_out % 8 == 0;
   LowArgs low{static_cast<const uint16_t*>(dY), bt, lddy, kp, (int64_t)r * kp, a->d_out, r};
   int st = launch_low<T>(lp, L.low, L.nb, vec, low, b, base, dA ? ds : nullptr, s);
@@ -985,9 +999,9 @@ static int lora_backward(const void* dY, int64_t lddy, const void* X, int64_t ld
   if (dX || (dA && lp.mix)) {
     UpArgs u{};
     u.B = at; u.scale = a->scale; u.R = R; u.Y = dX; u.S = dA ? ds : nullptr;
-    u.ldb = pitch; u.set = (int64_t)a->d_in * pitch; u.ldr = ldr; u.ldy = lddx; u.m = b.m; u.rank = r; u.d = a->d_in; u.y_type = x_dtype;
+    u.ldb = pitch; u.set = (int64_t)a->d_in * pitch; u.ldr = ldr; u.ldy = lddx; u.m = b.m; u.rank = r; u.d = dX ? a->d_in : 1; u.y_type = x_dtype;
     u.vec = rows_vec(R, ldr, x_dtype) && rows_vec(dX, lddx, x_dtype);
-    st = launch_up<T>(u, lp, L.low, L.nb, b, base, s);
+    st = launch_up<T>(u, lp, up, L.low, L.nb, b, base, s);
     if (st != GPTQ_OK) return st;
   }
   if (!dA && !dB) return GPTQ_OK;
@@ -1042,6 +1056,8 @@ extern "C" int gptq_lora(const void* X, gptq_dtype x_dtype, int64_t m, int64_t l
   if (!ws || ws_bytes < gptq_lora_workspace_size(m, a) || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return GPTQ_ERR_WORKSPACE;
   const int nb = rank_blocks(a->rank);
   const LowPlan lp = low_plan(m, n_seqs, a->d_in, nb);
+  const UpPlan upp = up_plan(lp, m, n_seqs, a->d_out);
+  if (!plans_fit(lp, upp)) return GPTQ_ERR_INVALID_ARG;
   const LowLayout L = low_layout(m, a->d_in, nb);
   const LoraBatch b{q_start, adapter, n_seqs, a->n_adapters, m};
   char* base = static_cast<char*>(ws);
@@ -1053,7 +1069,7 @@ extern "C" int gptq_lora(const void* X, gptq_dtype x_dtype, int64_t m, int64_t l
   up.vec = rows_vec(R, ldr, y_dtype) && rows_vec(Y, ldy, y_dtype);
   auto go = [&]<typename T>() {
     const int st = launch_low<T>(lp, L, nb, vec, low, b, base, S, s);
-    return st != GPTQ_OK ? st : launch_up<T>(up, lp, L, nb, b, base, s);
+    return st != GPTQ_OK ? st : launch_up<T>(up, lp, upp, L, nb, b, base, s);
   };
   return x_dtype == GPTQ_BF16 ? go.template operator()<__bf16>() : go.template operator()<_Float16>();
 }

@@ -244,3 +244,14 @@ def test_norm_refuses_vectors_and_scratch_in_the_way(L):
         assert norm_back(L, **{name: at(13, need - 4 & -16)}) == M.ERR_INVALID_ARG, name
     # the sums alone need no place of their own among what is not given
     assert norm_back(L, dR=None, dB=None, dg=at(8), dp=at(9), ws=None) == M.ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("m,n_seqs,d_in,d_out", [(1 << 20, 1 << 20, 256, 32768), (1 << 24, 1, 256, 1 << 20), (1 << 22, 5, 32, 1 << 18)])
+def test_lora_refuses_too_many_workgroups_before_any_work(L, m, n_seqs, d_in, d_out):
+    """Refused on the host, by both calls (the gradient's wide side is d_in), where no kernel could start either."""
+    far = lambda k: k << 46  # noqa: E731
+    apart = dict(X=far(4), qs=far(5), ad=far(6), ws=far(8), nb=BIG << 20, m=m, n_seqs=n_seqs)
+    s = a_set(far(1), far(2), far(3), d_in=d_in, d_out=d_out)
+    assert lora(L, s, **apart, ldx=d_in, Y=far(7), ldy=d_out, S=far(9)) == M.ERR_INVALID_ARG
+    s = a_set(far(1), far(2), far(3), d_in=d_out, d_out=d_in)
+    assert lora_back(L, s, **apart, dY=far(9), lddy=d_in, ldx=d_out, S=far(10), dX=far(11), lddx=d_out, dA=far(12), dB=far(13)) == M.ERR_INVALID_ARG
