@@ -444,7 +444,8 @@ typedef struct {
  *  S [m x rank] fp32, contiguous, or NULL: X A_a^T, for the backward pass (0 for a
  *  token without an adapter).  Sums are fp32; X A_a^T enters the second product in
  *  two 16-bit pieces (16 bits for bf16, 22 for fp16).
- *  Y and S overlap neither X nor each other.  m is at most 2^24, and so are the
+ *  Y, S and the scratch overlap no input (the set's and the batch's among them; but Y
+ *  may be R), nor each other.  m is at most 2^24, and so are the
  *  workgroups that the batch needs, some (m / 128 + n_seqs) * d_out / 256 (sequences of
  *  one token: m / 16 * d_out / 64); more are refused.
  *  ws  scratch of gptq_lora_workspace_size(m, set) bytes. */

@@ -818,6 +818,13 @@ static bool lora_ok(const gptq_lora_set* a) {
   return ((reinterpret_cast<uintptr_t>(a->A) | reinterpret_cast<uintptr_t>(a->B)) & 1) == 0 && (reinterpret_cast<uintptr_t>(a->scale) & 3) == 0;
 }
 constexpr int64_t kLoraMaxTokens = 1 << 24;
+// whether an array shares a byte with the set's matrices and scales or with the batch's description
+static bool meets_set(const void* p, uint64_t n, const gptq_lora_set* a, const int32_t* q_start, const int32_t* adapter, int n_seqs) {
+  const uint64_t pairs = (uint64_t)a->n_adapters * a->rank * 2;
+  return share_bytes(p, n, a->A, pairs * a->d_in) || share_bytes(p, n, a->B, pairs * a->d_out) ||
+         share_bytes(p, n, a->scale, (uint64_t)a->n_adapters * 4) || share_bytes(p, n, q_start, ((uint64_t)n_seqs + 1) * 4) ||
+         share_bytes(p, n, adapter, (uint64_t)n_seqs * 4);
+}
 
 // How X A^T is dealt out.  Runs: 32 tokens a workgroup of eight waves (at rank 128
 // 16), k in slices until there are two workgroups a CU.  Steps of mixed adapters: 16
@@ -1053,7 +1060,11 @@ extern "C" int gptq_lora(const void* X, gptq_dtype x_dtype, int64_t m, int64_t l
   if (share_bytes(Y, yb, X, xb) || share_bytes(Y, yb, S, sb) || share_bytes(S, sb, X, xb)) return GPTQ_ERR_INVALID_ARG;
   if (R && !(R == Y && ldr == ldy) && share_bytes(Y, yb, R, rows_bytes(m, ldr, a->d_out, e))) return GPTQ_ERR_INVALID_ARG;
   if (R && share_bytes(S, sb, R, rows_bytes(m, ldr, a->d_out, e))) return GPTQ_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < gptq_lora_workspace_size(m, a) || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return GPTQ_ERR_WORKSPACE;
+  if (meets_set(Y, yb, a, q_start, adapter, n_seqs) || meets_set(S, sb, a, q_start, adapter, n_seqs)) return GPTQ_ERR_INVALID_ARG;
+  const size_t need = gptq_lora_workspace_size(m, a);
+  if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return GPTQ_ERR_WORKSPACE;
+  if (meets_set(ws, need, a, q_start, adapter, n_seqs) || share_bytes(ws, need, X, xb) || share_bytes(ws, need, Y, yb) || share_bytes(ws, need, S, sb) ||
+      (R && share_bytes(ws, need, R, rows_bytes(m, ldr, a->d_out, e)))) return GPTQ_ERR_INVALID_ARG;
   const int nb = rank_blocks(a->rank);
   const LowPlan lp = low_plan(m, n_seqs, a->d_in, nb);
   const UpPlan upp = up_plan(lp, m, n_seqs, a->d_out);
@@ -1115,7 +1126,15 @@ extern "C" int gptq_lora_backward(const void* dY, gptq_dtype dtype, int64_t m, i
     if (!(R == dX && ldr == lddx) && share_bytes(dX, dxb, R, rb)) return GPTQ_ERR_INVALID_ARG;
     if (share_bytes(dA, na, R, rb) || share_bytes(dB, nb, R, rb)) return GPTQ_ERR_INVALID_ARG;
   }
-  if (!ws || ws_bytes < lora_back_layout(m, a).total || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return GPTQ_ERR_WORKSPACE;
+  for (const auto& o : outs)
+    if (meets_set(o.p, o.n, a, q_start, adapter, n_seqs)) return GPTQ_ERR_INVALID_ARG;
+  const size_t need = lora_back_layout(m, a).total;
+  if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return GPTQ_ERR_WORKSPACE;
+  for (const auto& o : outs)
+    if (share_bytes(ws, need, o.p, o.n)) return GPTQ_ERR_INVALID_ARG;
+  for (const auto& i : ins)
+    if (share_bytes(ws, need, i.p, i.n)) return GPTQ_ERR_INVALID_ARG;
+  if (meets_set(ws, need, a, q_start, adapter, n_seqs) || (R && share_bytes(ws, need, R, rows_bytes(m, ldr, a->d_in, e)))) return GPTQ_ERR_INVALID_ARG;
   const LoraBatch b{q_start, adapter, n_seqs, a->n_adapters, m};
   char* base = static_cast<char*>(ws);
   if (dtype == GPTQ_BF16) return lora_backward<__bf16>(dY, lddy, X, ldx, S, a, b, R, ldr, dX, x_dtype, lddx, dA, dB, base, s);

@@ -255,3 +255,19 @@ def test_lora_refuses_too_many_workgroups_before_any_work(L, m, n_seqs, d_in, d_
     assert lora(L, s, **apart, ldx=d_in, Y=far(7), ldy=d_out, S=far(9)) == M.ERR_INVALID_ARG
     s = a_set(far(1), far(2), far(3), d_in=d_out, d_out=d_in)
     assert lora_back(L, s, **apart, dY=far(9), lddy=d_in, ldx=d_out, S=far(10), dX=far(11), lddx=d_out, dA=far(12), dB=far(13)) == M.ERR_INVALID_ARG
+
+
+def test_lora_refuses_outputs_and_scratch_over_the_set_and_the_batch(L):
+    """The adapters' matrices, scales and the batch's description are inputs too; the scratch lies apart from all."""
+    na, nb = 4 * 16 * 256 * 2, 4 * 128 * 16 * 2
+    for kw in (dict(Y=at(1)), dict(Y=at(2, nb - 2)), dict(Y=at(3)), dict(Y=at(5)), dict(Y=at(6, 8)), dict(S=at(1, na - 4)), dict(S=at(2)), dict(S=at(3, 12)),
+               dict(S=at(5)), dict(S=at(6)), dict(ws=at(1)), dict(ws=at(2)), dict(ws=at(3)), dict(ws=at(4)), dict(ws=at(5)), dict(ws=at(6)), dict(ws=at(7)),
+               dict(ws=at(9), S=at(9, 256)), dict(ws=at(9), R=at(9, 256), ldr=128), dict(R=at(7), ldr=128, S=at(7, 128))):
+        assert lora(L, **kw) == M.ERR_INVALID_ARG, kw
+    for name in ("dX", "dA", "dB"):
+        for place in (at(1), at(2), at(1, na - 16), at(2, nb - 16), at(3), at(7), at(8)):
+            assert lora_back(L, **{name: place}) == M.ERR_INVALID_ARG, (name, place)
+    for k in (*range(1, 12), 13):
+        assert lora_back(L, ws=at(k), R=at(13), ldr=256) == M.ERR_INVALID_ARG, k
+    # the shared projection's output is where the adapters are added, and the limits of an array are not in it
+    assert lora(L, R=at(7), ldr=128, nb=0) == M.ERR_WORKSPACE and lora(L, Y=at(2, nb), nb=0) == M.ERR_WORKSPACE
