@@ -246,10 +246,12 @@ __global__ __launch_bounds__(256) void lora_low_steps_kernel(LowArgs p, LoraBatc
 }
 
 // Rows of s as an operand: in two pieces of T, [hi ranks | lo ranks], below the
-// row's power of two (fp16 has not the range of fp32), which `row` takes.
+// row's power of two (fp16 has not the range of fp32), which `row` takes: that of its
+// largest finite value, so that an infinity does not make the others infinite.
+GPTQ_DEV float finite_top(float top, float v) { return fabsf(v) < INFINITY ? fmaxf(top, fabsf(v)) : top; }
 template <typename T> GPTQ_DEV float piece_scale(float top, float& row) {
   int ex = (int)(__builtin_bit_cast(uint32_t, top) >> 23);
-  ex = ex == 255 || ex == 0 ? 127 : min(ex, 252);
+  ex = ex == 0 ? 127 : min(ex, 252);
   row = __builtin_bit_cast(float, (uint32_t)ex << 23);
   return __builtin_bit_cast(float, (uint32_t)(254 - ex) << 23);
 }
@@ -293,7 +295,7 @@ __global__ __launch_bounds__(256) void lora_pieces_kernel(const float* __restric
   }
   float top = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(s[e]));
+  for (int e = 0; e < 8; ++e) top = finite_top(top, s[e]);
   for (int o = 1; o < per; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
   if (t >= m) return;
   float row;
@@ -537,7 +539,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_steps_kernel(UpArgs p) 
         }
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(s[kb][e]));
+      for (int e = 0; e < 8; ++e) top = finite_top(top, s[kb][e]);
     }
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));

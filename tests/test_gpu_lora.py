@@ -195,3 +195,32 @@ def test_sequences_of_a_few_tokens(P, dtype, r, each, count):
     them empty."""
     lens = [each if i % 7 else each - 1 for i in range(count)]
     check(P, lens, [(3 * i) % 5 - 1 for i in range(count)], 4, r, 144, 272, dtype)
+
+
+@pytest.mark.parametrize("lens,which", [([40, 25], [0, 1]), ([1, 1, 1, 1, 1], [0, 1, 0, -1, 1])])
+def test_one_infinite_value_among_wide_ones(P, lens, which):
+    """A rank of an adapter is infinite: its tokens' outputs are infinite with its sign, though other ranks' values, of the
+    other sign, are beyond fp16's range; so are the gradient's."""
+    r, d, m = 16, 64, sum(lens)
+    A, B = torch.ones((2, r, d), dtype=HF, device="cuda"), torch.ones((2, d, r), dtype=HF, device="cuda")
+    A[:, 3, 7], B[:, 7, 3] = float("inf"), float("inf")
+    A[:, 5], B[:, :, 5] = -4000.0, -4000.0
+    s = P.LoRASet(A, B, torch.ones(2, device="cuda"))
+    start = [0]
+    for n in lens:
+        start.append(start[-1] + n)
+    X, Y, S = torch.ones((m, d), dtype=HF, device="cuda"), torch.empty((m, d), device="cuda"), torch.empty((m, r), device="cuda")
+    has = R.token_adapters(start, which, 2, m).cuda() >= 0
+    plain = [c for c in range(d) if c != 7]              # (channel 7 of the output has the infinite column of B)
+    B2 = B.clone()
+    B2[:, 7, 3] = 1.0
+    P.gptq_lora(X, P.LoRASet(A, B2, s.scale), i32(start), i32(which), Y, S=S)
+    assert bool((S[has][:, 3] == float("inf")).all()) and bool((S[has][:, 5] == -4000.0 * d).all())
+    B2[:, :, 5] = 1.0                                    # -256000 times 1 against +inf
+    P.gptq_lora(X, P.LoRASet(A, B2, s.scale), i32(start), i32(which), Y)
+    assert bool((Y[has] == float("inf")).all()) and bool((Y[~has] == 0).all())
+    A2 = A.clone()
+    A2[:, 3, 7], A2[:, 5] = 1.0, 1.0
+    dX = torch.empty((m, d), device="cuda")
+    P.gptq_lora_backward(X, None, None, P.LoRASet(A2, B, s.scale), i32(start), i32(which), dX=dX)
+    assert bool((dX[has][:, plain] == float("inf")).all()) and bool((dX[~has] == 0).all())
