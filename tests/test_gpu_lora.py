@@ -224,3 +224,33 @@ def test_one_infinite_value_among_wide_ones(P, lens, which):
     dX = torch.empty((m, d), device="cuda")
     P.gptq_lora_backward(X, None, None, P.LoRASet(A2, B, s.scale), i32(start), i32(which), dX=dX)
     assert bool((dX[has][:, plain] == float("inf")).all()) and bool((dX[~has] == 0).all())
+
+
+def _tile_lens(tok, most):
+    """Sequences that end 1, 31, 32, 33, 63, 64, 65 and tok - 1 tokens into a tile of tok, up to about `most` tokens in all."""
+    ends = [e for e in (1, 31, 32, 33, 63, 64, 65, 97, tok - 1, tok) if e <= tok]
+    lens, k = [], 0
+    while sum(lens) < most:
+        lens.append(tok * (k % 3) + ends[k % len(ends)])
+        k += 1
+    return lens
+
+
+@pytest.mark.parametrize("dtype,yt", [(BF, BF), (HF, F32)])
+@pytest.mark.parametrize("r", [16, 64, 128])
+@pytest.mark.parametrize("tok,most", [(64, 2100), (128, 4100)])
+def test_long_tiles_of_runs(P, dtype, yt, r, tok, most):
+    """Batches large enough for tiles of 64 and 128 tokens in the second product, which go 32 at a time: whole and ragged tiles,
+    several steps of one, residuals in place, sequences without an adapter; forward by d_out, backward by d_in."""
+    lens = _tile_lens(tok, most)
+    which = [(5 * i) % 4 - 1 for i in range(len(lens))]
+    m, wide = sum(lens) + 2, 8200                         # 33 groups of 256 channels
+    assert 64 * 1024 <= m * 33 < 128 * 1024 if tok == 64 else m * 33 >= 128 * 1024
+    check(P, lens, which, 3, r, 72, wide, dtype, yt)
+    check(P, lens, which, 3, r, wide, 72, dtype, yt, lead=3)
+
+
+@pytest.mark.parametrize("r", [16, 64])
+def test_one_long_run_of_pitched_rows(P, r):
+    check(P, [4200], [0], 1, r, 40, 8195, BF, None, True, 5, 3)
+    check(P, [4200], [0], 1, r, 8195, 40, HF, None, True, 5, 3)

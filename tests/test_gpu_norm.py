@@ -174,3 +174,34 @@ def test_without_eps(P, monkeypatch, ht, dt, m, d):
     both_ways(P, m, d, ht, dt, True, True, True, 0.7)
     both_ways(P, m, d, ht, dt, True, False, True, 0.7)
     both_ways(P, m, d, ht, dt, False, False, False, 1.0)
+
+
+@pytest.mark.parametrize("m,d", [(4101, 520), (4101, 1000), (4099, 5120), (4097, 8200), (1025, 16384), (6201, 2048)])
+@pytest.mark.parametrize("ht,dt,post,gate", [(F32, BF, True, True), (BF, BF, True, False), (HF, HF, False, True), (F32, F32, False, False)])
+def test_many_wide_rows(P, ht, dt, post, gate, m, d):
+    """Workgroups that walk several rows, of one chunk a thread and of two, the last step with rows that do not exist."""
+    both_ways(P, m, d, ht, dt, True, post, gate, 0.6)
+
+
+@pytest.mark.parametrize("m,d", [(1101, 4096), (2051, 640), (601, 8200), (515, 16384)])
+@pytest.mark.parametrize("ht,dt", [(BF, BF), (F32, F32)])
+def test_many_rows_in_place(P, ht, dt, m, d):
+    """As above, over the inputs: the next row is on its way while one is written."""
+    r, b, gamma, post, gate = rows(m, d, ht, 1), rows(m, d, dt, 2), vector(d, 3), vector(d, 4), vector(d, 5)
+    h, y = torch.empty_like(r), torch.empty_like(b)
+    P.gptq_residual_rmsnorm(r, y, B=b, H=h, gamma=gamma, post_gamma=post, gate=gate, alpha=0.5, eps=EPS)
+    r2, b2 = r.clone(), b.clone()
+    P.gptq_residual_rmsnorm(r2, b2, B=b2, H=r2, gamma=gamma, post_gamma=post, gate=gate, alpha=0.5, eps=EPS)
+    assert torch.equal(r2, h) and torch.equal(b2, y)
+    dy, dh = rows(m, d, dt, 6), rows(m, d, ht, 7)
+    outs = [torch.empty_like(r), torch.empty_like(b)] + [torch.empty(d, device="cuda") for _ in range(3)]
+    P.gptq_residual_rmsnorm_backward(dy, h, outs[0], dH=dh, B=b, dB=outs[1], gamma=gamma, post_gamma=post, gate=gate, alpha=0.5, eps=EPS,
+                                     dgamma=outs[2], dpost_gamma=outs[3], dgate=outs[4])
+    ref = R.norm_backward64(f64(dy), f64(h), f64(dh), f64(b), f64(gamma), f64(post), f64(gate), 0.5, EPS)
+    for name, got in zip(("dr", "db", "dgamma", "dpost", "dgate"), outs):
+        R.within(got, *ref[name], name)
+    dr2, db2, sums = dh.clone(), dy.clone(), [torch.empty(d, device="cuda") for _ in range(3)]
+    P.gptq_residual_rmsnorm_backward(db2, h, dr2, dH=dr2, B=b, dB=db2, gamma=gamma, post_gamma=post, gate=gate, alpha=0.5, eps=EPS,
+                                     dgamma=sums[0], dpost_gamma=sums[1], dgate=sums[2])
+    for a, x in zip([dr2, db2, *sums], outs):
+        assert torch.equal(a, x)
