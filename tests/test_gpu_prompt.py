@@ -300,3 +300,29 @@ def test_log_sum_of_a_row_that_is_no_number(P, dtype):
 @pytest.mark.parametrize("most", [2 ** 31 - 1, 2 ** 31 - 100, 2 ** 31 - 128])
 def test_a_bound_at_the_end_of_32_bits(P, most):
     check(P, [150, 20, 700], 4, 2, 64, BF, max_len=most)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("lens,H,n_kv", [([77], 8, 8), ([700, 1, 350, 129], 8, 2), ([1900], 2, 1), ([64] * 30, 4, 4)])
+def test_calls_repeat_bit_for_bit(P, dtype, hd, lens, H, n_kv):
+    """The same call gives the same bits, whatever else runs: workgroups come in any order, sums do not."""
+    start = [0]
+    for n in lens:
+        start.append(start[-1] + n)
+    T, most = start[-1], max(lens)
+    Q, K, V = inputs(T, H, n_kv, hd, dtype)
+    dO = rand((T, H, hd), dtype, 9, 0.1)
+    out, lse = forward(P, Q, K, V, start, most)
+    good = [t.clone() for t in backward(P, dO, Q, K, V, out, lse, start, most)]
+    other, busy = torch.cuda.Stream(), rand((2048, 2048), BF, 3)
+    for k in range(4):
+        if k % 2:
+            other.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(other):
+                for _ in range(3):
+                    torch.mm(busy, busy)
+        out2, lse2 = forward(P, Q, K, V, start, most)
+        got = backward(P, dO, Q, K, V, out, lse, start, most)
+        torch.cuda.synchronize()
+        assert torch.equal(out2, out) and torch.equal(lse2, lse) and all(torch.equal(a, b) for a, b in zip(got, good)), k
