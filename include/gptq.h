@@ -443,7 +443,8 @@ typedef struct {
  *  of y_dtype (F32, F16 or BF16), row pitch ldy, rounded once.
  *  S [m x rank] fp32, contiguous, or NULL: X A_a^T, for the backward pass (0 for a
  *  token without an adapter).  Sums are fp32; X A_a^T enters the second product in
- *  two 16-bit pieces (16 bits for bf16, 22 for fp16).
+ *  two 16-bit pieces (16 bits for bf16, 22 for fp16, for an F32 output too; an infinity
+ *  in B may then come out as NaN).
  *  Y, S and the scratch overlap no input (the set's and the batch's among them; but Y
  *  may be R), nor each other.  m is at most 2^24, and so are the
  *  workgroups that the batch needs, some (m / 128 + n_seqs) * d_out / 256 (sequences of
@@ -596,10 +597,11 @@ int gptq_kv4_attention(const void* Q, gptq_dtype dtype, int64_t n_tokens, int32_
  *          (a host bound on the lengths, at least 1), which nobody sees.
  *  lse     [n_tokens x n_heads] fp32, or NULL: what the backward pass needs.
  * Scores and statistics are fp32; the probabilities are rounded to 16 bits for the
- * second product.  What a token does not see, infinities and NaN too, does not
- * reach it.  Tiles of 128 tokens (n_tokens / 128 + n_seqs at most) times n_heads are
- * below 2^24, more are refused.  |scale| is at most 1e8; a key whose score is below -1e30 counts as
- * not seen, and a row that sees nothing is 0 (its lse -inf); a score above 1e38 may
+ * second product.  What comes behind a token or belongs to another sequence, infinities
+ * and NaN too, does not reach it.  Tiles of 128 tokens (n_tokens / 128 + n_seqs at most)
+ * times n_heads are below 2^24, more are refused.  |scale| is at most 1e8; a key whose
+ * score is below -6e29 has no weight (but a value of it that is no number still makes
+ * the row none), and a row of such keys alone is 0 (its lse -inf); a score above 1e38 may
  * count as infinite (the row is then no number). */
 int gptq_prompt_attention(const void* Q, const void* K, const void* V, gptq_dtype dtype, int64_t n_tokens,
                           int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int64_t ldq, int64_t ldk,

@@ -15,7 +15,9 @@
 //
 // s and dS are fp32.  Where they are an operand of a matrix instruction they go in
 // two pieces of the operands' 16-bit type (16 bits for bf16, 22 for fp16), whose error
-// stays below that of an output of this type; in dA and dB, which are fp32, three bf16 ones.
+// stays below that of rounding an output to this type; an fp32 Y or dX is as exact as the
+// pieces, not as fp32 sums (a third piece would be half as much again of that product).  In
+// dA and dB, always fp32, three bf16 ones.
 #include "w4_epilogue.h"
 
 #include <climits>
@@ -832,7 +834,11 @@ static bool meets_set(const void* p, uint64_t n, const gptq_lora_set* a, const i
 // 16), k in slices until there are two workgroups a CU.  Steps of mixed adapters: 16
 // tokens a workgroup of four waves, one of the adapters each, up to 8 slices (which the
 // second product adds itself).  One slice against these, whole calls of 8192 channels: 48
-// requests 22.8 and 11.9 us, 512 tokens of rank 64 70 and 37, 4096 of them 98 and 85.
+// requests 22.8 and 11.9 us, 512 tokens of rank 64 70 and 37, 4096 of them 98 and 85.  Half and twice
+// as many workgroups: 4096 tokens of rank 64, 5120 -> 13824, 115, 110 (these) and 112, of rank 16, 4096
+// channels, 38, 36 and 35, smaller batches the same within 3 %.  Up to 8, 16 and 32 slices: 40 tokens of
+// rank 64 23.8, 22.3 and 22.3, more of them the same.  Steps, up to 4 and 8: 48 requests of rank 16 13.3 and
+// 12.0, 8 of them 12.1 and 11.4, 256 of 4096 channels 16.6 and 20.0.
 struct LowPlan {
   bool mix;
   int mt, tiles, slices, slice_k, shares;

@@ -24,7 +24,10 @@
 namespace gptq {
 
 constexpr int kNormMax = 16384;        // two chunks of eight for each of 1024 threads
-constexpr int kNormParts = 256;        // workgroups of the backward pass, each with its column sums
+// Workgroups of the backward pass, each with its column sums: one a CU.  128, 256 and 512, us, 16-bit with
+// all gradients: 4095 rows of 4096 81, 56 and 69, 512 of them 23, 21 and 21, 16384 of 1024 72, 52 and 62,
+// 1024 of 16384 259, 180 and 219.
+constexpr int kNormParts = 256;
 
 struct NormArgs {
   const void *R, *B;          // forward: stream in, branch; backward: R is dH
@@ -214,7 +217,7 @@ __global__ __launch_bounds__(1024) void residual_norm_kernel(NormArgs a) {
 // The rows of a workgroup one after the other, their column sums in registers (one chunk a
 // thread: the vectors and the next row's loads too).  MORE: there is a gate or a norm
 // behind the sub-layer, whose column sums take registers that the plain residual does not spend.
-// 4095 rows of 4096, 16-bit, all gradients: 201 MB in 61 us, 3.3 TB/s: three sums over a row
+// 4095 rows of 4096, 16-bit, all gradients: 201 MB in 62 us, 3.2 TB/s: three sums over a row
 // that wait for each other, at two rows a CU under way.
 template <typename TH, typename TB, int NC, bool MORE>
 __global__ __launch_bounds__(1024) void residual_norm_backward_kernel(NormArgs a) {
@@ -416,7 +419,9 @@ __global__ __launch_bounds__(1024) void norm_columns_kernel(const float* __restr
   }
 }
 
-// Threads of a row: whole waves, one chunk of eight values each up to 8192 values, then two.
+// Threads of a row: whole waves, one chunk of eight values each up to 8192 values, then two (in the
+// backward pass two chunks leave no registers for the vectors and the next row: 4095 rows of 4096 in
+// half as many threads 189 us for 56, without post-norm and gate 36 for 34).
 struct NormShape {
   int T, groups, nc;
 };
@@ -430,8 +435,9 @@ static NormShape norm_shape(int d) {
 // Forward, where there are rows enough: two chunks a thread and one row a
 // workgroup, so that more rows are under way in a CU and fewer waves meet at a barrier.  One
 // chunk and two, fp32 stream, norms before and behind: 1024 rows of 5120 19.2 and 17.4 us, 2048
-// 32.1 and 27.7, 8192 111 and 105 (of 8192 values 160 and 167); below 1024 rows the same
-// within 4 %, and a single row has more threads.
+// 32.1 and 27.7, 8192 112 and 106 (of 8192 values 162 and 167, of 4096 84 and 84, of 2048 43 and 37,
+// of 1000 24.3 and 22.5, of 512, where the second chunk is behind every row's end, 14.6 and 13.9, of 128
+// and 64 both the launch's 9); below 1024 rows the same within 4 %, and a single row has more threads.
 static NormShape forward_shape(int64_t m, int d) {
   NormShape s = norm_shape(d);
   if (m < 1024) return s;

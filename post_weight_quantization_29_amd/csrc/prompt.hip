@@ -16,8 +16,9 @@
 //
 // p and ds are rounded once to 16 bits where they are an operand (ds of fp16 below a power
 // of two, its own for each token or key): half a step of a term, so the outputs' errors are
-// 1.3 (forward) to 1.5 times (gradients) those of rounding the outputs alone.  Two pieces
-// instead would be two more products of the seven.  Sums, maxima and D are fp32.
+// 1.2 to 1.3 (forward), 1.5 (bf16 gradients) and 1.6 times (fp16's dQ and dK) those of rounding the
+// outputs alone, of which a tenth is D's, from the rounded out.  Two pieces instead would be two
+// more products of the seven.  Sums, maxima and D are fp32.
 //
 // Tiles lie in LDS as rows of head_dim values whose 16-byte chunk c sits at c ^
 // f(row): 16 consecutive rows' reads of one chunk, and the transposing reads of
@@ -321,9 +322,9 @@ GPTQ_DEV bool head_tile(const PromptArgs& a, const PromptBatch& q, int& b, int& 
 }
 
 // Prompts of 4096, 2048, 2048 and 1371 tokens, 64 heads of 128 on 8 kv heads, bf16: 443
-// GFLOP in 571 us, 0.78 PFLOP/s, the matrix pipe busy in 35 % of the cycles, waves waiting in
-// 40 %.  No single thing bounds it: in copies of the kernel the time was 690 as it is (with a
-// profiler), 533 without the copies of tiles behind the first, 624 without LDS reads in the
+// GFLOP in 550 to 575 us back to back, 0.77 to 0.81 PFLOP/s, the matrix pipe busy in 35 % of the cycles,
+// waves waiting in 40 %.  No single thing bounds it: in copies of the kernel the time under the profiler
+// (655 to 690 as it is, with the box) was, of 690, 533 without the copies of tiles behind the first, 624 without LDS reads in the
 // loop, some 640 without exponentials, 489 without any of them.  256 tokens a workgroup (half
 // the copies) took as long, with tiles three ahead too, and so did a loop over pairs of tiles
 // with constant addresses and half of the vector instructions.
@@ -561,7 +562,8 @@ template <typename T, int HD> struct Scaled {
 };
 
 // dQ: per tile S^T and dP^T = V dO^T, then dQ^T += K^T dS^T.  Four sequences of 2048, 32 heads
-// of 128 on 8 kv heads, bf16: 257 us of the pass's 640, 0.80 PFLOP/s, matrix pipe busy in 38 %.
+// of 128 on 8 kv heads, bf16: 254 us under the profiler (dK and dV 408 there, together 661; the whole
+// pass takes 618 back to back without it), 0.81 PFLOP/s, matrix pipe busy in 38 %.
 template <typename T, int HD>
 __global__ __launch_bounds__(64 * kPromptWaves, 2) void prompt_dq_kernel(PromptArgs a, PromptBatch q) {
   typedef typename T16<T>::v8 v8;
@@ -692,10 +694,10 @@ __global__ __launch_bounds__(64 * kPromptWaves, 2) void prompt_dq_kernel(PromptA
 // dK and dV: a wave has 32 keys, in registers, and walks the tokens that see them in
 // tiles of 64, of all query heads of its kv head: S = Q K^T and dP = dO V^T, so that
 // a lane's registers are tokens of one key (its column), then dV^T += dO^T P and dK^T
-// += Q^T dS.  One wave a SIMD at head_dim 128 (K, V and both sums are 192 registers): 415 us for
-// the batch above, 0.66 PFLOP/s, matrix pipe busy in 30 %.  In copies of the kernel 463 us (with
-// a profiler) became 392 without copies, 394 without the first products' LDS reads, 414 without
-// exponentials, 335 without any.  Exponentials beside the other block's products, reads four
+// += Q^T dS.  One wave a SIMD at head_dim 128 (K, V and both sums are 192 registers): 408 us under
+// the profiler for the batch above (455 on a slower box), 0.67 PFLOP/s, matrix pipe busy in 30 %.  In
+// copies of the kernel on that box: 333 without the first products' LDS reads, 403 without
+// exponentials, no less without copies.  Exponentials beside the other block's products, reads four
 // products ahead, took as long (fp16, with its checks of range, twice as long).
 template <typename T, int HD>
 __global__ __launch_bounds__(64 * kPromptWaves, HD == 64 ? 2 : 1) void prompt_dkv_kernel(PromptArgs a, PromptBatch q) {
@@ -954,9 +956,12 @@ static int64_t tile_bound(int64_t n_tokens, int n_seqs, int64_t max_len) {
 
 // Workgroups that share the tokens of a tile of keys: up to four a CU in all, up to
 // eight, with four tiles of tokens each at least.  A few long sequences of few kv heads
-// leave most of the chip idle otherwise: 13 ragged sequences up to 2900 of 4 kv heads took
-// 343 us whole, 104 us split, and 13 us to join them; from four workgroups a CU on there is
-// nothing to gain.  The parts hold a row for each row of the batch, in sequences or not, so
+// leave most of the chip idle otherwise.  Whole passes, us, four query heads to a kv head, of 13 ragged
+// sequences up to 2900 of 4 kv heads / one of 2048 of 2, 4 and 8 kv heads / one of 4096 of 1 / of 512 of 2:
+// as here 179 / 143 166 242 / 224 / 76, unsplit 391 / 374 376 383 / 701 / 123; up to four parts 180 / 165 171
+// 206 / 284 / 73, up to 16 179 / 167 214 243 / 228 / 76; up to two workgroups a CU 249 / 144 170 216 / 225 / 76,
+// eight 170 / 143 166 248 / 224 / 76.  Two tiles a part at least, four and eight: 512 tokens 76, 76 and 73,
+// 300 of 4 kv heads 70, 67 and 78, eight of 128 29, 33 and 35.  The parts hold a row for each row of the batch, in sequences or not, so
 // their number is what kPartRows rows of one kv head's dK and dV leave room for.
 constexpr int64_t kPartRows = 1024 * kRows;
 static int key_splits(int64_t tiles, int64_t n_tokens, int n_kv, int rep, int64_t max_len) {
