@@ -18,7 +18,9 @@
 // of two, its own for each token or key): half a step of a term, so the outputs' errors are
 // 1.2 to 1.3 (forward), 1.5 (bf16 gradients) and 1.6 times (fp16's dQ and dK) those of rounding the
 // outputs alone, of which a tenth is D's, from the rounded out.  Two pieces instead would be two
-// more products of the seven.  Sums, maxima and D are fp32.
+// more products of the seven; of ds in dQ alone they took four sequences of 2048 from 618 to 681 us and
+// 13 ragged ones from 182 to 195, for an error of dQ 1.2 times that of rounding it.  Sums, maxima
+// and D are fp32.
 //
 // Tiles lie in LDS as rows of head_dim values whose 16-byte chunk c sits at c ^
 // f(row): 16 consecutive rows' reads of one chunk, and the transposing reads of
