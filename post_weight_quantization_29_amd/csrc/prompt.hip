@@ -325,11 +325,11 @@ GPTQ_DEV bool head_tile(const PromptArgs& a, const PromptBatch& q, int& b, int& 
 
 // Prompts of 4096, 2048, 2048 and 1371 tokens, 64 heads of 128 on 8 kv heads, bf16: 443
 // GFLOP in 550 to 575 us back to back, 0.77 to 0.81 PFLOP/s, the matrix pipe busy in 35 % of the cycles,
-// waves waiting in 40 %.  No single thing bounds it: in copies of the kernel the time under the profiler
-// (655 to 690 as it is, with the box) was, of 690, 533 without the copies of tiles behind the first, 624 without LDS reads in the
-// loop, some 640 without exponentials, 489 without any of them.  256 tokens a workgroup (half
-// the copies) took as long, with tiles three ahead too, and so did a loop over pairs of tiles
-// with constant addresses and half of the vector instructions.
+// waves waiting in 40 %.  No single thing bounds it: in copies of the kernel the time under the
+// profiler (655 to 690 as it is, with the box) was, of 690, 533 without the copies of tiles behind
+// the first, 624 without LDS reads in the loop, some 640 without exponentials, 489 without any of
+// them.  256 tokens a workgroup (half the copies) took as long, with tiles three ahead too, and so
+// did a loop over pairs of tiles with constant addresses and half of the vector instructions.
 template <typename T, int HD>
 __global__ __launch_bounds__(64 * kPromptWaves, 2) void prompt_forward_kernel(PromptArgs a, PromptBatch q) {
   typedef typename T16<T>::v8 v8;
@@ -963,7 +963,8 @@ static int64_t tile_bound(int64_t n_tokens, int n_seqs, int64_t max_len) {
 // as here 179 / 143 166 242 / 224 / 76, unsplit 391 / 374 376 383 / 701 / 123; up to four parts 180 / 165 171
 // 206 / 284 / 73, up to 16 179 / 167 214 243 / 228 / 76; up to two workgroups a CU 249 / 144 170 216 / 225 / 76,
 // eight 170 / 143 166 248 / 224 / 76.  Two tiles a part at least, four and eight: 512 tokens 76, 76 and 73,
-// 300 of 4 kv heads 70, 67 and 78, eight of 128 29, 33 and 35.  The parts hold a row for each row of the batch, in sequences or not, so
+// 300 of 4 kv heads 70, 67 and 78, eight of 128 29, 33 and 35.  The parts hold a row for each row
+// of the batch, in sequences or not, so
 // their number is what kPartRows rows of one kv head's dK and dV leave room for.
 constexpr int64_t kPartRows = 1024 * kRows;
 static int key_splits(int64_t tiles, int64_t n_tokens, int n_kv, int rep, int64_t max_len) {

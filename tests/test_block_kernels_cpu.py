@@ -5,10 +5,12 @@ from __future__ import annotations
 
 import os
 import re
+import shutil
 import subprocess
 
 import pytest
 
+pytestmark = pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "post_weight_quantization_29_amd", "csrc")
 
 
